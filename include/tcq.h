@@ -321,6 +321,147 @@ tcq_status tcq_gemv_vec(const uint32_t* bits, const uint32_t* start_state, const
                         int64_t rows, int64_t cols, const float* x, float* y, tcq_stream_t stream);
 
 /*
+ * Products of a batch of 16-bit activations with a trellis-coded matrix: a
+ * layer's forward pass and its gradients.  (The sources stop at the matrix-vector
+ * product, the 2-bit post's Pingala-8 section, and say only that prompts are
+ * bound by arithmetic; the rest is this library's.)
+ *
+ * The matrix is tcq_gemv's, W[r, c] = scale[r, j] * c[s_{r,j,t}] with c = jT + t.
+ * Activations and gradients are binary16 or bfloat16 rows of unit-stride elements
+ * with a row stride in elements (ld*, at least the row's length); n rows ("tokens").
+ */
+typedef enum {
+    TCQ_X_F16 = 0, /* IEEE binary16 */
+    TCQ_X_BF16 = 1 /* bfloat16 */
+} tcq_xdtype;
+
+typedef enum {
+    TCQ_ACT_NONE = 0,
+    TCQ_ACT_RELU = 1,     /* max(z, 0); slope 0 at 0 */
+    TCQ_ACT_SILU = 2,     /* z / (1 + e^-z) */
+    TCQ_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2 */
+    TCQ_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+} tcq_activation;
+
+/*
+ * 8-bit checkpoints of activations.  A row of m elements is stored as m code bytes
+ * and ceil(m / 32) scale bytes: the elements of a group of 32 neighbours share the
+ * scale 2^(byte - 127) and are codes * scale, with codes int8 (-127 .. 127) or e4m3.
+ * The scale is the smallest power of two (at least 2^-127) for which the group's
+ * largest magnitude fits (127 or 448 times the scale), and a code is its element
+ * over the scale, rounded to nearest even.  Both steps are exact functions of the
+ * input, so equal inputs give equal bytes everywhere.  A group with an infinity or a
+ * NaN gets the byte 255 and code 0, and stands for NaN.
+ */
+typedef enum {
+    TCQ_Q8_INT8 = 0,
+    TCQ_Q8_E4M3 = 1
+} tcq_q8;
+
+/*
+ *   x      [n, cols] of xdtype, row stride ldx, 2-byte aligned.
+ *   codes  uint8 [n, cols] contiguous.   scales  uint8 [n, ceil(cols / 32)] contiguous.
+ * tcq_unpack8 writes the stored values to x in xdtype: exact when the checkpoint
+ * was made from that type and no larger than its largest number, else rounded to
+ * nearest even (binary16 saturates at 65504).  n == 0 or cols == 0 is a no-op.
+ */
+tcq_status tcq_pack8(const void* x, tcq_xdtype xdtype, int64_t ldx, int64_t n, int64_t cols,
+                     tcq_q8 format, uint8_t* codes, uint8_t* scales, tcq_stream_t stream);
+
+tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 format, int64_t n,
+                       int64_t cols, void* x, tcq_xdtype xdtype, int64_t ldx,
+                       tcq_stream_t stream);
+
+/*
+ * Forward product with the layer's bias, activation and residual:
+ *     Z[i, r] = sum_c X[i, c] W[r, c] + bias[r],   Y[i, r] = act(Z[i, r]) + residual[i, r]
+ * computed in fp32 and rounded once to xdtype.
+ *
+ * The products run on the tensor cores with both operands in binary16: a weight is
+ * its codeword times its block's scale rounded once to binary16 (exact without
+ * scales for a binary16 table and the computed code), relative to a power of two
+ * per row of W; a bfloat16 row of X is scaled to binary16 by a power of two of its
+ * own, exactly for elements above 2^-32 of the row's largest and within 2^-39 of
+ * that largest for the others.  Sums are fp32.
+ *
+ *   bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols  as tcq_gemv
+ *               (T % 4 == 0, cols % T == 0, a binary16 table when L >= 15; the
+ *               entries of a table are at most 65504 in magnitude).
+ *   x           [n, cols] of xdtype, row stride ldx.
+ *   bias        fp32 [rows] or NULL.
+ *   residual    [n, rows] of xdtype, row stride ldr, or NULL.
+ *   y           out: [n, rows] of xdtype, row stride ldy.  It may be the residual
+ *               itself (same pointer and stride); it must not overlap x.
+ *   z_codes, z_scales  out: the 8-bit checkpoint of Z in z_format ([n, rows] codes
+ *               and [n, ceil(rows / 32)] scale bytes), or both NULL.
+ *   workspace   device scratch, 256-byte aligned, at least tcq_gemm_workspace_bytes
+ *               of the same shape (else TCQ_ERR_WORKSPACE).  Contents on entry do not
+ *               matter; calls that may overlap need a workspace each.
+ * 16-bit arrays 2-byte aligned, fp32 arrays 4-byte aligned (16 bytes and row strides
+ * that are multiples of 8 elements run faster).  n == 0 or rows == 0 is a no-op;
+ * cols == 0 is TCQ_ERR_INVALID_ARG.  A row of X with an infinity or a NaN affects only its
+ * own row of Y.  Results do not depend on timing: equal calls give equal bits.
+ */
+size_t tcq_gemm_workspace_bytes(int L, int k, int T, int64_t rows, int64_t cols, int64_t n,
+                                tcq_dtype cb_dtype);
+
+tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const float* scale,
+                    const void* codebook, tcq_dtype cb_dtype, int L, int k, int T, int64_t rows,
+                    int64_t cols, const void* x, tcq_xdtype xdtype, int64_t ldx, int64_t n,
+                    const float* bias, tcq_activation act, const void* residual, int64_t ldr,
+                    void* y, int64_t ldy, uint8_t* z_codes, uint8_t* z_scales, tcq_q8 z_format,
+                    void* workspace, size_t workspace_bytes, tcq_stream_t stream);
+
+/*
+ * Input gradient: dX[i, c] = sum_r dZ[i, r] W[r, c], with tcq_gemm's operand
+ * formats (dZ takes the place of X), fp32 sums, rounded once to xdtype.
+ *   dz  [n, rows], row stride lddz.   dx  out: [n, cols], row stride lddx.
+ * rows == 0 gives dX = 0; n == 0 or cols == 0 is a no-op.  Everything else as tcq_gemm.
+ */
+size_t tcq_gemm_dgrad_workspace_bytes(int L, int k, int T, int64_t rows, int64_t cols, int64_t n,
+                                      tcq_dtype cb_dtype);
+
+tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, const float* scale,
+                          const void* codebook, tcq_dtype cb_dtype, int L, int k, int T,
+                          int64_t rows, int64_t cols, const void* dz, tcq_xdtype xdtype,
+                          int64_t lddz, int64_t n, void* dx, int64_t lddx, void* workspace,
+                          size_t workspace_bytes, tcq_stream_t stream);
+
+/*
+ * Gradient through the activation, from the 8-bit checkpoint of Z:
+ *     dZ[i, r] = dY[i, r] act'(Zhat[i, r]) rounded to xdtype,
+ *     dbias[r] = sum_i dY[i, r] act'(Zhat[i, r])   (unrounded terms, fp32, a fixed order)
+ *   dy  [n, rows], row stride lddy.   dz  out: [n, rows], row stride lddz; may be dy
+ *   itself (same pointer and stride).   dbias  out: fp32 [rows], or NULL.
+ *   z_codes, z_scales  as tcq_gemm writes them; both may be NULL for TCQ_ACT_NONE.
+ *   workspace  as above, tcq_act_grad8_workspace_bytes (only read when dbias is wanted).
+ * n == 0 gives dbias = 0.
+ */
+size_t tcq_act_grad8_workspace_bytes(int64_t n, int64_t rows);
+
+tcq_status tcq_act_grad8(const void* dy, tcq_xdtype xdtype, int64_t lddy, const uint8_t* z_codes,
+                         const uint8_t* z_scales, tcq_q8 z_format, tcq_activation act, int64_t n,
+                         int64_t rows, void* dz, int64_t lddz, float* dbias, void* workspace,
+                         size_t workspace_bytes, tcq_stream_t stream);
+
+/*
+ * Weight gradient from the 8-bit checkpoint of the layer's input:
+ *     dW[r, c] = sum_i dZ[i, r] Xhat[i, c]   (+ dW[r, c] on entry when accumulate)
+ * on the tensor cores with both operands in dZ's type, Xhat being what tcq_unpack8
+ * gives in that type (so every product is exact), fp32 sums.
+ *   dz  [n, rows], row stride lddz.   x_codes, x_scales  [n, cols] checkpoint.
+ *   dw  fp32 [rows, cols], row stride lddw.
+ *   workspace  as above, tcq_wgrad8_workspace_bytes.
+ * n == 0 gives dW = 0 (or leaves it when accumulate); rows == 0 or cols == 0 is a no-op.
+ */
+size_t tcq_wgrad8_workspace_bytes(int64_t rows, int64_t cols, int64_t n);
+
+tcq_status tcq_wgrad8(const void* dz, tcq_xdtype xdtype, int64_t lddz, const uint8_t* x_codes,
+                      const uint8_t* x_scales, tcq_q8 x_format, int64_t n, int64_t rows,
+                      int64_t cols, float* dw, int64_t lddw, int accumulate, void* workspace,
+                      size_t workspace_bytes, tcq_stream_t stream);
+
+/*
  * Trellis-coded quantization over Ungerboeck's 8-state set-partitioned trellis
  * (the 2-bit post, Pingala-8 section: an 8-state set-partitioned trellis with
  * Ungerboeck's labels over symbols of several weights at about 2 bits per
@@ -395,6 +536,9 @@ tcq_status tcq_ub8_decode(const uint32_t* bits, const uint32_t* start_state, con
  *                            (bounded) for what it had issued, wrote NaN
  *                            targets for its rows and freed its tensor memory;
  *                            the affected blocks then carry non-finite costs.
+ *                            The products of tcq_gemm, tcq_gemm_dgrad and
+ *                            tcq_wgrad8 stop the same way and leave the outputs
+ *                            of the tiles not yet finished unwritten.
  *   TCQ_DEVERR_BOUNDS        an index failed its bounds check and the access
  *                            was skipped (only the TCQ_DEBUG build,
  *                            libtcq_debug.so, checks indices).

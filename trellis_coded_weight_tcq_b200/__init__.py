@@ -12,17 +12,22 @@ from .tcq import (  # noqa: F401
     Encoded,
     HostPipeline,
     LdlqResult,
+    Packed8,
     TCQError,
     Workspace,
+    act_grad8,
     bcjr,
     decode,
     decode_vec,
     encode,
     encode_vec,
+    gemm,
+    gemm_dgrad,
     gemv,
     gemv_vec,
     ldlq,
     load_library,
+    pack8,
     tcq_decode,
     tcq_encode,
     tcq_encode_path,
@@ -31,4 +36,6 @@ from .tcq import (  # noqa: F401
     tcq_gemv_vec,
     tcq_status_string,
     tcq_words_per_block,
+    unpack8,
+    wgrad8,
 )

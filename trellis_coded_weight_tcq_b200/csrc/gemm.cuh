@@ -1,0 +1,90 @@
+// gemm.cuh -- internal launch interface of the batched products with a
+// trellis-coded matrix, their gradients and the 8-bit checkpoints.
+#pragma once
+
+#include "common.cuh"
+
+namespace tcq {
+
+// A trellis-coded matrix (tcq_gemv's layout).
+struct CodedMatrix {
+    const uint32_t* bits;
+    const uint32_t* start_state;
+    const float* scale;  // [rows * cols / T] or nullptr
+    const void* cb;
+    int cb_f16;          // 0 binary32 table, 1 binary16 table, kMadCodebook computed
+    int L, K, T, W;
+    long long rows, cols;
+};
+
+// What happens to a product before it is stored.
+struct Epilogue {
+    const float* row_scale;  // power of two per output row, or nullptr
+    const float* col_scale;  // power of two per output column, or nullptr
+    const float* bias;       // per output column, or nullptr
+    const void* residual;    // output type, or nullptr
+    long long ldr;
+    void* out;
+    long long ldo;
+    int act;
+    uint8_t* z_codes;        // [m, n] contiguous, or nullptr
+    uint8_t* z_scales;       // [m, ceil(n / 32)]
+    int z_format;
+    int accumulate;          // fp32 outputs: add to what is there
+};
+
+enum GemmKind { kGemmForward = 0, kGemmDgrad = 1, kGemmWgrad = 2 };
+
+// out[m, n] = epilogue(sum_k a b), 16-bit operands (fmt 0 binary16, 1 bfloat16):
+//   forward  a [m, k] row-major, b [n, k] row-major
+//   dgrad    a [m, k] row-major, b [k, n] row-major
+//   wgrad    a [k, m] row-major, b [k, n] row-major, fp32 out
+// Leading dimensions in elements, multiples of 8; bases 16-byte aligned.
+struct GemmProblem {
+    const void* a;
+    long long lda;
+    const void* b;
+    long long ldb;
+    long long m, n, k;
+    int fmt;
+    int xdtype;  // output type of forward and dgrad
+};
+
+cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, int num_sms, unsigned int* err,
+                           cudaStream_t stream);
+
+// W as binary16 [rows, ldw], each weight over its row's power of two (row_pow2[r],
+// written when the matrix has scales).
+cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, int num_sms,
+                            cudaStream_t stream);
+
+// x [n, cols] as binary16 rows over a power of two each (row_pow2[n]); col_pow2
+// (or nullptr) multiplies the columns first.
+cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long long n, long long cols,
+                              const float* col_pow2, void* out, long long ldo, float* row_pow2, cudaStream_t stream);
+// 16-bit rows copied to another stride.
+cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
+                          int num_sms, cudaStream_t stream);
+
+cudaError_t launch_pack8(const void* x, int xdtype, long long ldx, long long n, long long cols, int format,
+                         uint8_t* codes, uint8_t* scales, int num_sms, cudaStream_t stream);
+cudaError_t launch_unpack8(const uint8_t* codes, const uint8_t* scales, int format, long long n, long long cols,
+                           void* x, int xdtype, long long ldx, int num_sms, cudaStream_t stream);
+
+struct ActGradArgs {
+    const void* dy;
+    long long lddy;
+    const uint8_t* z_codes;
+    const uint8_t* z_scales;
+    int act;
+    long long n, rows;
+    void* dz;
+    long long lddz;
+    float* partial;  // [splits, rows], or nullptr: no dbias
+    float* dbias;
+    int splits;      // row ranges
+};
+int act_grad8_splits(long long n, long long rows);
+cudaError_t launch_act_grad8(const ActGradArgs& a, int xdtype, int format, cudaStream_t stream);
+
+}  // namespace tcq

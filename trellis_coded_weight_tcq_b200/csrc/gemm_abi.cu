@@ -1,0 +1,299 @@
+// gemm_abi.cu -- C entry points of the batched products and the 8-bit checkpoints:
+// host-side checks, workspace layout and launches.  Like every entry point, they
+// neither allocate nor synchronise nor keep anything between calls.
+#include <stdint.h>
+
+#include "codes.cuh"
+#include "gemm.cuh"
+
+using namespace tcq;
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 30;  // rows, columns and tokens
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+bool valid_x(tcq_xdtype t) { return t == TCQ_X_F16 || t == TCQ_X_BF16; }
+bool valid_q8(tcq_q8 f) { return f == TCQ_Q8_INT8 || f == TCQ_Q8_E4M3; }
+bool valid_act(tcq_activation a) { return a >= TCQ_ACT_NONE && a <= TCQ_ACT_GELU_TANH; }
+
+bool valid_dim(int64_t v) { return v >= 0 && v <= kMaxDim; }
+
+// a [n, cols] array of 16-bit rows: its stride reaches the next row without overlap
+bool valid_rows(const void* p, int64_t ld, int64_t cols) { return p && aligned(p, 2) && ld >= cols && ld <= 2 * kMaxDim; }
+
+bool direct(const void* p, int64_t ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+int sms()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+tcq_status check_matrix(tcq_dtype dt, int L, int k, int T, int64_t rows, int64_t cols)
+{
+    if (!valid_dim(rows) || !valid_dim(cols)) return TCQ_ERR_INVALID_ARG;
+    if (dt != TCQ_F32 && dt != TCQ_F16 && dt != TCQ_MAD) return TCQ_ERR_INVALID_ARG;
+    if (k < 1 || k > TCQ_MAX_K || L < k || L > TCQ_MAX_L || T < 1 || T > TCQ_MAX_T || T % 4 != 0)
+        return TCQ_ERR_UNSUPPORTED;
+    if (dt == TCQ_F32 && L >= 15) return TCQ_ERR_UNSUPPORTED;  // the table lives in shared memory
+    if (cols % T != 0) return TCQ_ERR_INVALID_ARG;
+    if ((unsigned long long)rows * (unsigned long long)cols > (1ull << 42)) return TCQ_ERR_INVALID_ARG;
+    return TCQ_OK;
+}
+
+bool matrix_pointers(const uint32_t* bits, const uint32_t* start, const float* scale, const void* cb, tcq_dtype dt)
+{
+    return bits && start && aligned(bits, 4) && aligned(start, 4) && (!scale || aligned(scale, 4)) &&
+           (dt == TCQ_MAD || (cb && aligned(cb, dt == TCQ_F16 ? 2 : 4)));
+}
+
+CodedMatrix matrix(const uint32_t* bits, const uint32_t* start, const float* scale, const void* cb, tcq_dtype dt, int L,
+                   int k, int T, int64_t rows, int64_t cols)
+{
+    return {bits, start, scale, cb, dt == TCQ_F16 ? 1 : dt == TCQ_MAD ? kMadCodebook : 0, L, k, T,
+            tcq_words_per_block(k, T), rows, cols};
+}
+
+// Workspace of a product: the binary16 matrix, its row powers, the binary16
+// activations (rows of `inner` elements) and theirs.
+struct GemmSpace {
+    size_t weights, row_pow2, x, x_pow2, total;
+};
+
+GemmSpace gemm_space(int64_t rows, int64_t cols, int64_t n, int64_t inner)
+{
+    GemmSpace s;
+    s.weights = 0;
+    s.row_pow2 = align256((size_t)rows * round_up(cols, 8) * 2);
+    s.x = s.row_pow2 + align256((size_t)rows * 4);
+    s.x_pow2 = s.x + align256((size_t)n * round_up(inner, 8) * 2);
+    s.total = s.x_pow2 + align256((size_t)n * 4);
+    return s;
+}
+
+Epilogue plain_epilogue(void* out, int64_t ldo)
+{
+    Epilogue e = {};
+    e.out = out;
+    e.ldo = ldo;
+    return e;
+}
+
+tcq_status status(cudaError_t e) { return e == cudaSuccess ? TCQ_OK : TCQ_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+size_t tcq_gemm_workspace_bytes(int L, int k, int T, int64_t rows, int64_t cols, int64_t n, tcq_dtype cb_dtype)
+{
+    if (check_matrix(cb_dtype, L, k, T, rows, cols) != TCQ_OK || !valid_dim(n) || n == 0 || rows == 0 || cols == 0)
+        return 0;
+    return gemm_space(rows, cols, n, cols).total;
+}
+
+tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const float* scale, const void* codebook,
+                    tcq_dtype cb_dtype, int L, int k, int T, int64_t rows, int64_t cols, const void* x,
+                    tcq_xdtype xdtype, int64_t ldx, int64_t n, const float* bias, tcq_activation act,
+                    const void* residual, int64_t ldr, void* y, int64_t ldy, uint8_t* z_codes, uint8_t* z_scales,
+                    tcq_q8 z_format, void* workspace, size_t workspace_bytes, tcq_stream_t stream)
+{
+    const tcq_status shape = check_matrix(cb_dtype, L, k, T, rows, cols);
+    if (shape != TCQ_OK) return shape;
+    if (!valid_dim(n) || !valid_x(xdtype) || !valid_act(act) || !valid_q8(z_format)) return TCQ_ERR_INVALID_ARG;
+    if (n == 0 || rows == 0) return TCQ_OK;
+    if (cols == 0 || !matrix_pointers(bits, start_state, scale, codebook, cb_dtype) || !valid_rows(x, ldx, cols) ||
+        !valid_rows(y, ldy, rows) || (residual && !valid_rows(residual, ldr, rows)) || (bias && !aligned(bias, 4)) ||
+        (z_codes == nullptr) != (z_scales == nullptr) || !workspace || !aligned(workspace, 256))
+        return TCQ_ERR_INVALID_ARG;
+    const GemmSpace sp = gemm_space(rows, cols, n, cols);
+    if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
+    const int num_sms = sms();
+    if (num_sms <= 0) return TCQ_ERR_CUDA;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    unsigned int* err = device_error_word(st);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    float* row_pow2 = reinterpret_cast<float*>(ws + sp.row_pow2);
+    float* x_pow2 = reinterpret_cast<float*>(ws + sp.x_pow2);
+    const CodedMatrix w = matrix(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols);
+    const int64_t ldw = round_up(cols, 8);
+
+    cudaError_t e = launch_decode16(w, ws, ldw, row_pow2, num_sms, st);
+    if (e != cudaSuccess) return TCQ_ERR_CUDA;
+    GemmProblem p = {x, ldx, ws, ldw, n, rows, cols, 0, xdtype};
+    Epilogue ep = plain_epilogue(y, ldy);
+    // binary16 rows that TMA can read are used where they are
+    if (xdtype != TCQ_X_F16 || !direct(x, ldx)) {
+        e = launch_scale_rows(x, xdtype, ldx, n, cols, nullptr, ws + sp.x, ldw, x_pow2, st);
+        if (e != cudaSuccess) return TCQ_ERR_CUDA;
+        p.a = ws + sp.x;
+        p.lda = ldw;
+        ep.row_scale = x_pow2;
+    }
+    ep.col_scale = scale ? row_pow2 : nullptr;
+    ep.bias = bias;
+    ep.residual = residual;
+    ep.ldr = ldr;
+    ep.act = act;
+    ep.z_codes = z_codes;
+    ep.z_scales = z_scales;
+    ep.z_format = z_format;
+    return status(launch_gemm_tc(kGemmForward, p, ep, num_sms, err, st));
+}
+
+size_t tcq_gemm_dgrad_workspace_bytes(int L, int k, int T, int64_t rows, int64_t cols, int64_t n, tcq_dtype cb_dtype)
+{
+    if (check_matrix(cb_dtype, L, k, T, rows, cols) != TCQ_OK || !valid_dim(n) || n == 0 || rows == 0 || cols == 0)
+        return 0;
+    return gemm_space(rows, cols, n, rows).total;
+}
+
+tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, const float* scale, const void* codebook,
+                          tcq_dtype cb_dtype, int L, int k, int T, int64_t rows, int64_t cols, const void* dz,
+                          tcq_xdtype xdtype, int64_t lddz, int64_t n, void* dx, int64_t lddx, void* workspace,
+                          size_t workspace_bytes, tcq_stream_t stream)
+{
+    const tcq_status shape = check_matrix(cb_dtype, L, k, T, rows, cols);
+    if (shape != TCQ_OK) return shape;
+    if (!valid_dim(n) || !valid_x(xdtype)) return TCQ_ERR_INVALID_ARG;
+    if (n == 0 || cols == 0) return TCQ_OK;
+    if (!valid_rows(dx, lddx, cols)) return TCQ_ERR_INVALID_ARG;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (rows == 0) return status(cudaMemset2DAsync(dx, (size_t)lddx * 2, 0, (size_t)cols * 2, (size_t)n, st));
+    if (!matrix_pointers(bits, start_state, scale, codebook, cb_dtype) || !valid_rows(dz, lddz, rows) || !workspace ||
+        !aligned(workspace, 256))
+        return TCQ_ERR_INVALID_ARG;
+    const GemmSpace sp = gemm_space(rows, cols, n, rows);
+    if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
+    const int num_sms = sms();
+    if (num_sms <= 0) return TCQ_ERR_CUDA;
+    unsigned int* err = device_error_word(st);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    float* row_pow2 = reinterpret_cast<float*>(ws + sp.row_pow2);
+    float* x_pow2 = reinterpret_cast<float*>(ws + sp.x_pow2);
+    const CodedMatrix w = matrix(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols);
+    const int64_t ldw = round_up(cols, 8);
+
+    cudaError_t e = launch_decode16(w, ws, ldw, row_pow2, num_sms, st);
+    if (e != cudaSuccess) return TCQ_ERR_CUDA;
+    GemmProblem p = {dz, lddz, ws, ldw, n, cols, rows, 0, xdtype};
+    Epilogue ep = plain_epilogue(dx, lddx);
+    // W's rows run along the reduction: their powers go with dZ's columns
+    if (xdtype != TCQ_X_F16 || scale || !direct(dz, lddz)) {
+        const int64_t ldz = round_up(rows, 8);
+        e = launch_scale_rows(dz, xdtype, lddz, n, rows, scale ? row_pow2 : nullptr, ws + sp.x, ldz, x_pow2, st);
+        if (e != cudaSuccess) return TCQ_ERR_CUDA;
+        p.a = ws + sp.x;
+        p.lda = ldz;
+        ep.row_scale = x_pow2;
+    }
+    return status(launch_gemm_tc(kGemmDgrad, p, ep, num_sms, err, st));
+}
+
+size_t tcq_wgrad8_workspace_bytes(int64_t rows, int64_t cols, int64_t n)
+{
+    if (!valid_dim(rows) || !valid_dim(cols) || !valid_dim(n) || n == 0 || rows == 0 || cols == 0) return 0;
+    return align256((size_t)n * round_up(cols, 8) * 2) + align256((size_t)n * round_up(rows, 8) * 2);
+}
+
+tcq_status tcq_wgrad8(const void* dz, tcq_xdtype xdtype, int64_t lddz, const uint8_t* x_codes, const uint8_t* x_scales,
+                      tcq_q8 x_format, int64_t n, int64_t rows, int64_t cols, float* dw, int64_t lddw, int accumulate,
+                      void* workspace, size_t workspace_bytes, tcq_stream_t stream)
+{
+    if (!valid_dim(n) || !valid_dim(rows) || !valid_dim(cols) || !valid_x(xdtype) || !valid_q8(x_format))
+        return TCQ_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return TCQ_OK;
+    if (!dw || !aligned(dw, 4) || lddw < cols || lddw > 2 * kMaxDim) return TCQ_ERR_INVALID_ARG;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (n == 0) {
+        if (accumulate) return TCQ_OK;
+        return status(cudaMemset2DAsync(dw, (size_t)lddw * 4, 0, (size_t)cols * 4, (size_t)rows, st));
+    }
+    if (!valid_rows(dz, lddz, rows) || !x_codes || !x_scales || !workspace || !aligned(workspace, 256))
+        return TCQ_ERR_INVALID_ARG;
+    if (workspace_bytes < tcq_wgrad8_workspace_bytes(rows, cols, n)) return TCQ_ERR_WORKSPACE;
+    const int num_sms = sms();
+    if (num_sms <= 0) return TCQ_ERR_CUDA;
+    unsigned int* err = device_error_word(st);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const int64_t ldq = round_up(cols, 8);
+    cudaError_t e = launch_unpack8(x_codes, x_scales, x_format, n, cols, ws, xdtype, ldq, num_sms, st);
+    if (e != cudaSuccess) return TCQ_ERR_CUDA;
+    GemmProblem p = {dz, lddz, ws, ldq, rows, cols, n, xdtype == TCQ_X_BF16 ? 1 : 0, xdtype};
+    if (!direct(dz, lddz)) {
+        unsigned char* copy = ws + align256((size_t)n * ldq * 2);
+        const int64_t ldz = round_up(rows, 8);
+        e = launch_copy16(dz, lddz, n, rows, copy, ldz, num_sms, st);
+        if (e != cudaSuccess) return TCQ_ERR_CUDA;
+        p.a = copy;
+        p.lda = ldz;
+    }
+    Epilogue ep = plain_epilogue(dw, lddw);
+    ep.accumulate = accumulate != 0;
+    return status(launch_gemm_tc(kGemmWgrad, p, ep, num_sms, err, st));
+}
+
+tcq_status tcq_pack8(const void* x, tcq_xdtype xdtype, int64_t ldx, int64_t n, int64_t cols, tcq_q8 format,
+                     uint8_t* codes, uint8_t* scales, tcq_stream_t stream)
+{
+    if (!valid_dim(n) || !valid_dim(cols) || !valid_x(xdtype) || !valid_q8(format)) return TCQ_ERR_INVALID_ARG;
+    if (n == 0 || cols == 0) return TCQ_OK;
+    if (!valid_rows(x, ldx, cols) || !codes || !scales) return TCQ_ERR_INVALID_ARG;
+    const int num_sms = sms();
+    if (num_sms <= 0) return TCQ_ERR_CUDA;
+    return status(launch_pack8(x, xdtype, ldx, n, cols, format, codes, scales, num_sms,
+                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 format, int64_t n, int64_t cols, void* x,
+                       tcq_xdtype xdtype, int64_t ldx, tcq_stream_t stream)
+{
+    if (!valid_dim(n) || !valid_dim(cols) || !valid_x(xdtype) || !valid_q8(format)) return TCQ_ERR_INVALID_ARG;
+    if (n == 0 || cols == 0) return TCQ_OK;
+    if (!valid_rows(x, ldx, cols) || !codes || !scales) return TCQ_ERR_INVALID_ARG;
+    const int num_sms = sms();
+    if (num_sms <= 0) return TCQ_ERR_CUDA;
+    return status(launch_unpack8(codes, scales, format, n, cols, x, xdtype, ldx, num_sms,
+                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t tcq_act_grad8_workspace_bytes(int64_t n, int64_t rows)
+{
+    if (!valid_dim(n) || !valid_dim(rows) || n == 0 || rows == 0) return 0;
+    return align256((size_t)act_grad8_splits(n, rows) * rows * 4);
+}
+
+tcq_status tcq_act_grad8(const void* dy, tcq_xdtype xdtype, int64_t lddy, const uint8_t* z_codes,
+                         const uint8_t* z_scales, tcq_q8 z_format, tcq_activation act, int64_t n, int64_t rows, void* dz,
+                         int64_t lddz, float* dbias, void* workspace, size_t workspace_bytes, tcq_stream_t stream)
+{
+    if (!valid_dim(n) || !valid_dim(rows) || !valid_x(xdtype) || !valid_q8(z_format) || !valid_act(act))
+        return TCQ_ERR_INVALID_ARG;
+    if (rows == 0) return TCQ_OK;
+    if (dbias && !aligned(dbias, 4)) return TCQ_ERR_INVALID_ARG;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (n == 0) return dbias ? status(cudaMemsetAsync(dbias, 0, (size_t)rows * 4, st)) : TCQ_OK;
+    if (!valid_rows(dy, lddy, rows) || !valid_rows(dz, lddz, rows) ||
+        (act != TCQ_ACT_NONE && (!z_codes || !z_scales)))
+        return TCQ_ERR_INVALID_ARG;
+    if (dbias) {
+        if (!workspace || !aligned(workspace, 256)) return TCQ_ERR_INVALID_ARG;
+        if (workspace_bytes < tcq_act_grad8_workspace_bytes(n, rows)) return TCQ_ERR_WORKSPACE;
+    }
+    ActGradArgs a = {dy, lddy, z_codes, z_scales, act, n, rows, dz, lddz,
+                     dbias ? static_cast<float*>(workspace) : nullptr, dbias, act_grad8_splits(n, rows)};
+    return status(launch_act_grad8(a, xdtype, z_format, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,486 @@
+// gemm_tc.cu -- the 16-bit matrix products of the batched layer on the
+// fifth-generation tensor cores, and the passes that bring their operands to
+// binary16 rows.
+//
+// One kernel serves the three products; they differ in which operands run along
+// the reduction (the tensor core reads either order from 128-byte swizzled tiles)
+// and in the epilogue.  A pair of CTAs (a cluster of two, cta_group::2) computes a
+// 256 x 256 tile: each CTA loads its half of both operands by TMA, 128 x 64 elements
+// of each per stage, six stages deep (192 KB), and one thread of the first CTA issues
+// the pair's MMAs (256 x 256 x 16).  The accumulators take 256 columns of each CTA's
+// tensor memory; two sets of them let the four epilogue warps store a tile while the
+// next one is multiplied.  The grid is persistent, one pair per two SMs.
+//
+// Roles: warp 0 TMA, warp 1 MMA (first CTA of the pair only), warp 2 tensor memory,
+// warps 4-7 epilogue.  Barriers: full (both CTAs' loads of a stage landed; in the
+// first CTA), empty (the MMAs that read a stage are done; in both, by a commit to
+// both), tfull / tempty (an accumulator set is complete / has been read).
+#include "gemm.cuh"
+#include "q8.cuh"
+#include "tc.cuh"
+#include "decode16.cuh"
+
+namespace tcq {
+
+bool make_map_16bit(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld, int box_rows)
+{
+    typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            fn = nullptr;
+        }
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
+    const cuuint32_t step[2] = {1u, 1u};
+    // the element type only matters for the fill, which is zero in both
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kTile = 256;            // rows and columns of a pair's tile
+constexpr int kDepth = 64;            // reduction depth of a stage
+constexpr int kHalfBytes = 128 * kDepth * 2;  // one CTA's half of one operand's stage
+constexpr int kThreads = 256;
+
+struct __align__(1024) Smem {
+    unsigned char a[kStages][kHalfBytes];
+    unsigned char b[kStages][kHalfBytes];
+    unsigned long long full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int stop;
+};
+
+struct Shape {
+    long long m, n, k;
+    int m_tiles, n_tiles, k_steps;
+    int fmt;
+};
+
+// 32 consecutive 16-bit outputs of one row: row r, columns c .. c + 31, `count` of
+// them below n.
+template <int KIND, int XT>
+__device__ __forceinline__ void store32_16bit(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
+                                              int count, bool vec, float row_scale)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= row_scale;
+    if constexpr (KIND == kGemmForward) {
+        if (e.col_scale || e.bias) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                if (i < count) {
+                    if (e.col_scale) v[i] *= __ldg(e.col_scale + c + i);
+                    if (e.bias) v[i] += __ldg(e.bias + c + i);
+                }
+            }
+        }
+        if (e.z_codes) {
+            const long long group = r * ((n + 31) / 32) + c / 32;
+            uint32_t top = 0u;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < count) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+            uint8_t* z = e.z_codes + r * n + c;
+            const bool int8 = e.z_format == TCQ_Q8_INT8;
+            const uint32_t byte = int8 ? q8_scale_byte<TCQ_Q8_INT8>(top) : q8_scale_byte<TCQ_Q8_E4M3>(top);
+            const float inv = q8_inv(byte);
+            e.z_scales[group] = (uint8_t)byte;
+            uint32_t code[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) code[i] = 0u;
+            if (byte != 255u) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t q = int8 ? q8_encode<TCQ_Q8_INT8>(v[i], inv) : q8_encode<TCQ_Q8_E4M3>(v[i], inv);
+                    code[i / 4] |= q << (8 * (i & 3));
+                }
+            }
+            if (count == 32 && (reinterpret_cast<uintptr_t>(z) & 15) == 0) {
+                reinterpret_cast<uint4*>(z)[0] = make_uint4(code[0], code[1], code[2], code[3]);
+                reinterpret_cast<uint4*>(z)[1] = make_uint4(code[4], code[5], code[6], code[7]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < count) z[i] = (uint8_t)(code[i / 4] >> (8 * (i & 3)));
+            }
+        }
+        switch (e.act) {  // one loop per activation: the choice is made once
+        case TCQ_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_RELU);
+            break;
+        case TCQ_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_SILU);
+            break;
+        case TCQ_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_GELU);
+            break;
+        case TCQ_ACT_GELU_TANH:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_GELU_TANH);
+            break;
+        default: break;
+        }
+        if (e.residual) {
+            const uint16_t* res = static_cast<const uint16_t*>(e.residual) + r * e.ldr + c;
+            if (vec && count == 32) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    const uint4 t = *reinterpret_cast<const uint4*>(res + i);
+                    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float2 f = x_unpack2<XT>(w[h]);
+                        v[i + 2 * h] += f.x;
+                        v[i + 2 * h + 1] += f.y;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i < count) v[i] += x_load<XT>(res, i);
+            }
+        }
+    }
+    uint16_t* o = static_cast<uint16_t*>(e.out) + r * e.ldo + c;
+    if (vec && count == 32) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(o + i) =
+                make_uint4(x_pack2<XT>(v[i], v[i + 1]), x_pack2<XT>(v[i + 2], v[i + 3]),
+                           x_pack2<XT>(v[i + 4], v[i + 5]), x_pack2<XT>(v[i + 6], v[i + 7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < count) o[i] = x_bits<XT>(v[i]);
+    }
+}
+
+// The same for either output type.
+template <int KIND, int XT>
+__device__ __forceinline__ void store32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
+                                        bool vec, float row_scale)
+{
+    const int count = n - c < 32 ? (int)(n - c) : 32;
+    if constexpr (KIND == kGemmWgrad) {
+        float* o = static_cast<float*>(e.out) + r * e.ldo + c;
+        if (vec && count == 32) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                float4 t = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                if (e.accumulate) {
+                    const float4 old = *reinterpret_cast<const float4*>(o + i);
+                    t.x += old.x; t.y += old.y; t.z += old.z; t.w += old.w;
+                }
+                *reinterpret_cast<float4*>(o + i) = t;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < count) o[i] = e.accumulate ? o[i] + v[i] : v[i];
+        }
+    } else {
+        store32_16bit<KIND, XT>(e, r, c, n, v, count, vec, row_scale);
+    }
+}
+
+template <int KIND, int XT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Shape p, Epilogue e,
+            bool vec, unsigned int* err)
+{
+    constexpr int AMN = KIND == kGemmWgrad, BMN = KIND != kGemmForward;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    Smem& S = *reinterpret_cast<Smem*>(raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = p.m_tiles * p.n_tiles;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_addr(&S.full[i]), 1);
+            mbar_init(smem_addr(&S.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&S.tfull[i]), 1);
+            mbar_init(smem_addr(&S.tempty[i]), 8);  // four epilogue warps in each CTA
+        }
+        mbar_init(smem_addr(&S.drain), 1);
+        S.stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+    }
+    if (warp == 2) tmem_alloc<2>(smem_addr(&S.tmem), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    volatile int* stop = &S.stop;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const int m0 = (t % p.m_tiles) * kTile + (int)rank * 128;
+                const int n0 = (t / p.m_tiles) * kTile + (int)rank * 128;
+                for (int ks = 0; ks < p.k_steps; ++ks, ++it) {
+                    const int s = it % kStages;
+                    ok = mbar_wait(smem_addr(&S.empty[s]), ((it / kStages) & 1) ^ 1, stop, err);
+                    if (!ok) break;
+                    const uint32_t full = map_to_cta(smem_addr(&S.full[s]), 0);
+                    if (rank == 0) mbar_expect_tx(smem_addr(&S.full[s]), 4 * kHalfBytes);
+                    const int k0 = ks * kDepth;
+                    const uint32_t a = smem_addr(S.a[s]), b = smem_addr(S.b[s]);
+                    if constexpr (AMN) {
+                        tma_load_2d_pair(a, &map_a, full, m0, k0);
+                        tma_load_2d_pair(a + kHalfBytes / 2, &map_a, full, m0 + 64, k0);
+                    } else {
+                        tma_load_2d_pair(a, &map_a, full, k0, m0);
+                    }
+                    if constexpr (BMN) {
+                        tma_load_2d_pair(b, &map_b, full, n0, k0);
+                        tma_load_2d_pair(b + kHalfBytes / 2, &map_b, full, n0 + 64, k0);
+                    } else {
+                        tma_load_2d_pair(b, &map_b, full, k0, n0);
+                    }
+                }
+            }
+            // after a stop, what was loaded last is still waited for
+            if (*stop && rank == 0)
+                for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
+                    mbar_drain(smem_addr(&S.full[i % kStages]), (i / kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        if (lane == 0) {
+            const uint32_t idesc = mma_idesc(256, 256, p.fmt, AMN, BMN);
+            int it = 0, done = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs, ++done) {
+                const int acc = done & 1;
+                ok = mbar_wait(smem_addr(&S.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
+                if (!ok) break;
+                tc_fence_after();
+                for (int ks = 0; ks < p.k_steps; ++ks, ++it) {
+                    const int s = it % kStages;
+                    ok = mbar_wait(smem_addr(&S.full[s]), (it / kStages) & 1, stop, err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = smem_addr(S.a[s]), b = smem_addr(S.b[s]);
+#pragma unroll
+                    for (int j = 0; j < kDepth / 16; ++j) {
+                        // 16 deep: 32 bytes along a K-major row, 16 rows of 128 bytes otherwise
+                        const unsigned long long da = smem_desc_sw128(a + j * (AMN ? 2048 : 32), kHalfBytes / 2);
+                        const unsigned long long db = smem_desc_sw128(b + j * (BMN ? 2048 : 32), kHalfBytes / 2);
+                        mma_f16<2>(tmem + acc * 256, da, db, idesc, (ks | j) != 0);
+                    }
+                    mma_commit<2>(smem_addr(&S.empty[s]));
+                }
+                if (ok) mma_commit<2>(smem_addr(&S.tfull[acc]));
+            }
+            if (*stop) {  // nothing issued may still run when the tensor memory is freed
+                mma_commit<2>(smem_addr(&S.drain));
+                mbar_drain(smem_addr(&S.drain), 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int quarter = warp & 3;
+        int done = 0;
+        for (int t = pair; t < tiles; t += pairs, ++done) {
+            const int acc = done & 1;
+            bool ok = mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const long long r = (long long)(t % p.m_tiles) * kTile + rank * 128 + quarter * 32 + lane;
+            const long long n0 = (long long)(t / p.m_tiles) * kTile;
+            const float row_scale = e.row_scale && r < p.m ? __ldg(e.row_scale + r) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 32) {
+                if (n0 + c >= p.n) break;
+                float v[32];
+                tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * 256 + c, v);
+                if (r < p.m) store32<KIND, XT>(e, r, n0 + c, p.n, v, vec, row_scale);
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_addr(&S.tempty[acc]), 0));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_free<2>(tmem, 512);
+    }
+}
+
+template <int KIND, int XT>
+cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigned int* err, cudaStream_t stream)
+{
+    CUtensorMap ma, mb;
+    const bool ok = (KIND == kGemmWgrad ? make_map_16bit(&ma, g.a, g.k, g.m, g.lda, 64)
+                                        : make_map_16bit(&ma, g.a, g.m, g.k, g.lda, 128)) &&
+                    (KIND == kGemmForward ? make_map_16bit(&mb, g.b, g.n, g.k, g.ldb, 128)
+                                          : make_map_16bit(&mb, g.b, g.k, g.n, g.ldb, 64));
+    if (!ok) return cudaErrorInvalidValue;
+    Shape s;
+    s.m = g.m;
+    s.n = g.n;
+    s.k = g.k;
+    s.m_tiles = (int)((g.m + kTile - 1) / kTile);
+    s.n_tiles = (int)((g.n + kTile - 1) / kTile);
+    s.k_steps = (int)((g.k + kDepth - 1) / kDepth);
+    s.fmt = g.fmt;
+    const int es = KIND == kGemmWgrad ? 4 : 2;
+    bool vec = (reinterpret_cast<uintptr_t>(e.out) & 15) == 0 && e.ldo * es % 16 == 0;
+    if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 15) == 0 && e.ldr % 8 == 0;
+    cudaError_t st = cudaFuncSetAttribute(gemm_kernel<KIND, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)sizeof(Smem));
+    if (st != cudaSuccess) return st;
+    const long long tiles = (long long)s.m_tiles * s.n_tiles;
+    if (tiles > INT32_MAX - num_sms) return cudaErrorInvalidValue;
+    const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    gemm_kernel<KIND, XT><<<2 * pairs, kThreads, sizeof(Smem), stream>>>(ma, mb, s, e, vec, err);
+    return cudaGetLastError();
+}
+
+// ---- operand passes
+// One CTA per row: the row's largest finite magnitude, then the row over the power of
+// two that brings it to [2^14, 2^15).  Memory bound (2 bytes read twice, the second
+// time from L2, and 2 written per element).
+constexpr int kRowThreads = 256;
+
+template <int XT>
+__global__ void __launch_bounds__(kRowThreads) scale_rows_kernel(const uint16_t* x, long long ldx, long long cols,
+                                                                 const float* col_pow2, uint16_t* out, long long ldo,
+                                                                 float* row_pow2, bool vec)
+{
+    __shared__ uint32_t part[kRowThreads / 32];
+    const long long r = blockIdx.x;
+    const uint16_t* xr = x + r * ldx;
+    uint16_t* o = out + r * ldo;
+    uint32_t top = 0u;
+    auto eight = [&](long long c, float (&f)[8]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(xr + c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const float2 t = x_unpack2<XT>(w[h]);
+            f[2 * h] = t.x;
+            f[2 * h + 1] = t.y;
+        }
+        if (col_pow2) {
+            const float4 p = *reinterpret_cast<const float4*>(col_pow2 + c);
+            const float4 q = *reinterpret_cast<const float4*>(col_pow2 + c + 4);
+            f[0] *= p.x; f[1] *= p.y; f[2] *= p.z; f[3] *= p.w;
+            f[4] *= q.x; f[5] *= q.y; f[6] *= q.z; f[7] *= q.w;
+        }
+    };
+    const long long vcols = vec ? cols / 8 * 8 : 0;
+    for (long long c = 8ll * threadIdx.x; c < vcols; c += 8 * kRowThreads) {
+        float f[8];
+        eight(c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, finite_magnitude(f[i]));
+    }
+    for (long long c = vcols + threadIdx.x; c < cols; c += kRowThreads)
+        top = max(top, finite_magnitude(x_load<XT>(xr, c) * (col_pow2 ? col_pow2[c] : 1.f)));
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRowThreads / 32; ++i) top = max(top, part[i]);
+    // |x| < 2^p; the factor stays in the normal range, so tiny rows end lower than 2^15
+    int p = 0;
+    if (top != 0u) p = power_above(top) - 15;
+    if (p < -126) p = -126;
+    const float inv = pow2_clamped(-p);
+    if (threadIdx.x == 0) row_pow2[r] = pow2_clamped(p);
+    for (long long c = 8ll * threadIdx.x; c < vcols; c += 8 * kRowThreads) {
+        float f[8];
+        eight(c, f);
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) w[h] = x_pack2<TCQ_X_F16>(f[2 * h] * inv, f[2 * h + 1] * inv);
+        *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    for (long long c = vcols + threadIdx.x; c < cols; c += kRowThreads)
+        o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (col_pow2 ? col_pow2[c] : 1.f) * inv);
+}
+
+__global__ void __launch_bounds__(256) copy16_kernel(const uint16_t* x, long long ldx, long long n, long long cols,
+                                                     uint16_t* out, long long ldo)
+{
+    const long long total = n * cols;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+         i += (long long)gridDim.x * blockDim.x) {
+        const long long r = i / cols, c = i - r * cols;
+        out[r * ldo + c] = x[r * ldx + c];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, int num_sms, unsigned int* err,
+                           cudaStream_t stream)
+{
+    const bool bf = p.xdtype == TCQ_X_BF16;
+    switch (kind) {
+    case kGemmForward:
+        return bf ? launch<kGemmForward, TCQ_X_BF16>(p, e, num_sms, err, stream)
+                  : launch<kGemmForward, TCQ_X_F16>(p, e, num_sms, err, stream);
+    case kGemmDgrad:
+        return bf ? launch<kGemmDgrad, TCQ_X_BF16>(p, e, num_sms, err, stream)
+                  : launch<kGemmDgrad, TCQ_X_F16>(p, e, num_sms, err, stream);
+    default: return launch<kGemmWgrad, TCQ_X_F16>(p, e, num_sms, err, stream);
+    }
+}
+
+cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long long n, long long cols,
+                              const float* col_pow2, void* out, long long ldo, float* row_pow2, cudaStream_t stream)
+{
+    const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
+    const uint16_t* xi = static_cast<const uint16_t*>(x);
+    uint16_t* o = static_cast<uint16_t*>(out);
+    if (xdtype == TCQ_X_BF16)
+        scale_rows_kernel<TCQ_X_BF16><<<(unsigned)n, kRowThreads, 0, stream>>>(xi, ldx, cols, col_pow2, o, ldo, row_pow2, vec);
+    else
+        scale_rows_kernel<TCQ_X_F16><<<(unsigned)n, kRowThreads, 0, stream>>>(xi, ldx, cols, col_pow2, o, ldo, row_pow2, vec);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
+                          int num_sms, cudaStream_t stream)
+{
+    long long grid = (n * cols + 1023) / 1024;
+    if (grid > 16ll * num_sms) grid = 16ll * num_sms;
+    copy16_kernel<<<(int)grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x), ldx, n, cols,
+                                                 static_cast<uint16_t*>(out), ldo);
+    return cudaGetLastError();
+}
+
+}  // namespace tcq

@@ -10,6 +10,7 @@ computing anything itself.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -31,6 +32,18 @@ TCQ_ERR_INTERNAL = 5
 TCQ_F32 = 0
 TCQ_F16 = 1
 TCQ_MAD = 2
+TCQ_X_F16 = 0
+TCQ_X_BF16 = 1
+TCQ_ACT_NONE = 0
+TCQ_ACT_RELU = 1
+TCQ_ACT_SILU = 2
+TCQ_ACT_GELU = 3
+TCQ_ACT_GELU_TANH = 4
+TCQ_Q8_INT8 = 0
+TCQ_Q8_E4M3 = 1
+ACTIVATIONS = {"none": TCQ_ACT_NONE, "relu": TCQ_ACT_RELU, "silu": TCQ_ACT_SILU, "gelu": TCQ_ACT_GELU,
+               "gelu_tanh": TCQ_ACT_GELU_TANH}
+Q8_FORMATS = {"int8": TCQ_Q8_INT8, "e4m3": TCQ_Q8_E4M3}
 
 
 class _ComputedCode:
@@ -106,6 +119,27 @@ def load_library() -> ctypes.CDLL:
     lib.tcq_ub8_encode.restype = ci
     lib.tcq_ub8_decode.argtypes = [vp, vp, vp, ci, ci, ci, ci, i64, vp, vp]
     lib.tcq_ub8_decode.restype = ci
+    lib.tcq_pack8.argtypes = [vp, ci, i64, i64, i64, ci, vp, vp, vp]
+    lib.tcq_pack8.restype = ci
+    lib.tcq_unpack8.argtypes = [vp, vp, ci, i64, i64, vp, ci, i64, vp]
+    lib.tcq_unpack8.restype = ci
+    lib.tcq_gemm_workspace_bytes.argtypes = [ci, ci, ci, i64, i64, i64, ci]
+    lib.tcq_gemm_workspace_bytes.restype = sz
+    lib.tcq_gemm.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, i64, i64, vp, ci, i64, i64, vp, ci, vp, i64, vp, i64,
+                             vp, vp, ci, vp, sz, vp]
+    lib.tcq_gemm.restype = ci
+    lib.tcq_gemm_dgrad_workspace_bytes.argtypes = [ci, ci, ci, i64, i64, i64, ci]
+    lib.tcq_gemm_dgrad_workspace_bytes.restype = sz
+    lib.tcq_gemm_dgrad.argtypes = [vp, vp, vp, vp, ci, ci, ci, ci, i64, i64, vp, ci, i64, i64, vp, i64, vp, sz, vp]
+    lib.tcq_gemm_dgrad.restype = ci
+    lib.tcq_act_grad8_workspace_bytes.argtypes = [i64, i64]
+    lib.tcq_act_grad8_workspace_bytes.restype = sz
+    lib.tcq_act_grad8.argtypes = [vp, ci, i64, vp, vp, ci, ci, i64, i64, vp, i64, vp, vp, sz, vp]
+    lib.tcq_act_grad8.restype = ci
+    lib.tcq_wgrad8_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.tcq_wgrad8_workspace_bytes.restype = sz
+    lib.tcq_wgrad8.argtypes = [vp, ci, i64, vp, vp, ci, i64, i64, i64, vp, i64, ci, vp, sz, vp]
+    lib.tcq_wgrad8.restype = ci
     lib.tcq_device_errors.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.tcq_device_errors.restype = ci
     _lib = lib
@@ -209,6 +243,55 @@ def tcq_ub8_encode(x, d, codebook, cb_dtype, V, m, T, n_blocks, fixed_start, sta
 def tcq_ub8_decode(bits, start_state, codebook, cb_dtype, V, m, T, n_blocks, y, stream) -> int:
     return int(load_library().tcq_ub8_decode(bits, start_state, codebook, cb_dtype, V, m, T,
                                              n_blocks, y, stream))
+
+
+def tcq_pack8(x, xdtype, ldx, n, cols, fmt, codes, scales, stream) -> int:
+    return int(load_library().tcq_pack8(x, xdtype, ldx, n, cols, fmt, codes, scales, stream))
+
+
+def tcq_unpack8(codes, scales, fmt, n, cols, x, xdtype, ldx, stream) -> int:
+    return int(load_library().tcq_unpack8(codes, scales, fmt, n, cols, x, xdtype, ldx, stream))
+
+
+def tcq_gemm_workspace_bytes(L, k, T, rows, cols, n, cb_dtype) -> int:
+    return int(load_library().tcq_gemm_workspace_bytes(L, k, T, rows, cols, n, cb_dtype))
+
+
+def tcq_gemm(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols, x, xdtype, ldx, n, bias, act,
+             residual, ldr, y, ldy, z_codes, z_scales, z_format, workspace, workspace_bytes, stream) -> int:
+    return int(load_library().tcq_gemm(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols, x, xdtype,
+                                       ldx, n, bias, act, residual, ldr, y, ldy, z_codes, z_scales, z_format,
+                                       workspace, workspace_bytes, stream))
+
+
+def tcq_gemm_dgrad_workspace_bytes(L, k, T, rows, cols, n, cb_dtype) -> int:
+    return int(load_library().tcq_gemm_dgrad_workspace_bytes(L, k, T, rows, cols, n, cb_dtype))
+
+
+def tcq_gemm_dgrad(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols, dz, xdtype, lddz, n, dx, lddx,
+                   workspace, workspace_bytes, stream) -> int:
+    return int(load_library().tcq_gemm_dgrad(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols, dz,
+                                             xdtype, lddz, n, dx, lddx, workspace, workspace_bytes, stream))
+
+
+def tcq_act_grad8_workspace_bytes(n: int, rows: int) -> int:
+    return int(load_library().tcq_act_grad8_workspace_bytes(n, rows))
+
+
+def tcq_act_grad8(dy, xdtype, lddy, z_codes, z_scales, z_format, act, n, rows, dz, lddz, dbias, workspace,
+                  workspace_bytes, stream) -> int:
+    return int(load_library().tcq_act_grad8(dy, xdtype, lddy, z_codes, z_scales, z_format, act, n, rows, dz, lddz,
+                                            dbias, workspace, workspace_bytes, stream))
+
+
+def tcq_wgrad8_workspace_bytes(rows: int, cols: int, n: int) -> int:
+    return int(load_library().tcq_wgrad8_workspace_bytes(rows, cols, n))
+
+
+def tcq_wgrad8(dz, xdtype, lddz, x_codes, x_scales, x_format, n, rows, cols, dw, lddw, accumulate, workspace,
+               workspace_bytes, stream) -> int:
+    return int(load_library().tcq_wgrad8(dz, xdtype, lddz, x_codes, x_scales, x_format, n, rows, cols, dw, lddw,
+                                         accumulate, workspace, workspace_bytes, stream))
 
 
 TCQ_DEVERR_WAIT_TIMEOUT = 0x1
@@ -491,6 +574,252 @@ def decode_vec(bits, start_state, codebook, L: int, k: int, V: int, T: int, out=
         raise ValueError("decode_vec: out must be a contiguous float32 tensor of n_blocks * T")
     _check(tcq_decode_vec(_ptr(bits), _ptr(start_state), _ptr(codebook), cb_dtype_of(codebook), L,
                           k, V, T, n, _ptr(out), _stream_handle(stream)), "tcq_decode_vec")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# batched 16-bit products and 8-bit checkpoints
+# ---------------------------------------------------------------------------
+@dataclass
+class Packed8:
+    """An 8-bit checkpoint of a 16-bit tensor [n, cols]: ``codes`` (int8 [n, cols];
+    for "e4m3" the bytes of the numbers), ``scales`` (uint8 [n, ceil(cols / 32)], the
+    exponent + 127 of each group's power of two) and the format's name."""
+
+    codes: "object"
+    scales: "object"
+    format: str = "int8"
+
+
+def _x_dtype(t, what: str) -> int:
+    """TCQ_X_* of a 2-D 16-bit CUDA tensor with unit-stride rows."""
+    torch = _torch()
+    if t.dim() != 2 or not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel()):
+        raise ValueError(f"{what} must be a 2-D CUDA tensor with unit-stride rows")
+    if t.dtype == torch.bfloat16:
+        return TCQ_X_BF16
+    if t.dtype == torch.float16:
+        return TCQ_X_F16
+    raise TypeError(f"{what} must be float16 or bfloat16, got {t.dtype}")
+
+
+def _ld(t) -> int:
+    """Row stride in elements (that of one row, or of none, does not matter)."""
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] else max(t.shape[1], 1)
+
+
+def _on_device(device):
+    """The tensors' device made current for the call, if it is not."""
+    torch = _torch()
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t is not MAD and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, x on {device}")
+
+
+def _choice(table, name, what):
+    if name not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)}; got {name!r}")
+    return table[name]
+
+
+def _check_out(out, shape, dtype, what):
+    if tuple(out.shape) != shape or out.dtype != dtype or (out.stride(1) != 1 and shape[1] > 1 and out.numel()):
+        raise ValueError(f"{what} must be a {dtype} tensor {list(shape)} with unit-stride rows")
+    if shape[0] > 1 and out.numel() and out.stride(0) < shape[1]:
+        raise ValueError(f"{what}: rows overlap")
+
+
+def _check_packed(p, n, cols, device, what):
+    torch = _torch()
+    fmt = _choice(Q8_FORMATS, p.format, f"{what}.format")
+    if (tuple(p.codes.shape) != (n, cols) or p.codes.element_size() != 1 or not p.codes.is_contiguous() or
+            tuple(p.scales.shape) != (n, -(-cols // 32)) or p.scales.dtype != torch.uint8 or
+            not p.scales.is_contiguous()):
+        raise ValueError(f"{what} must hold contiguous 8-bit codes [{n}, {cols}] and uint8 scales "
+                         f"[{n}, {-(-cols // 32)}]")
+    _same_device(device, **{f"{what}.codes": p.codes, f"{what}.scales": p.scales})
+    return fmt
+
+
+def _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, device, what):
+    torch = _torch()
+    nb = rows * (cols // T) if T > 0 else 0
+    W = tcq_words_per_block(k, T)
+    if W < 0:
+        raise TCQError(TCQ_ERR_UNSUPPORTED, "tcq_words_per_block")
+    if bits.numel() < nb * W or start_state.numel() < nb or (scale is not None and scale.numel() < nb):
+        raise ValueError(f"{what}: tensors too small for a {rows} x {cols} matrix of T={T} blocks")
+    if (bits.element_size() != 4 or start_state.element_size() != 4 or not bits.is_contiguous() or
+            not start_state.is_contiguous() or
+            (scale is not None and (scale.dtype != torch.float32 or not scale.is_contiguous()))):
+        raise ValueError(f"{what}: bits and start_state are contiguous 32-bit words, scale contiguous float32")
+    if codebook is not MAD and (codebook.numel() < (1 << L) or not codebook.is_contiguous()):
+        raise ValueError(f"{what}: codebook must hold 2^L contiguous entries")
+    _same_device(device, bits=bits, start_state=start_state, scale=scale, codebook=codebook)
+
+
+def _scratch(workspace, nbytes, device, what):
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"{what}: workspace must be a contiguous uint8 tensor on x's device")
+    return workspace
+
+
+def _stream_on(device, stream):
+    torch = _torch()
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def pack8(x, format: str = "int8", out: Packed8 | None = None, stream=None) -> Packed8:
+    """8-bit checkpoint of ``x`` (float16 or bfloat16 CUDA [n, cols], unit-stride rows)."""
+    torch = _torch()
+    xt = _x_dtype(x, "x")
+    n, cols = x.shape
+    if out is None:
+        fmt = _choice(Q8_FORMATS, format, "format")
+        out = Packed8(torch.empty((n, cols), dtype=torch.int8, device=x.device),
+                      torch.empty((n, -(-cols // 32)), dtype=torch.uint8, device=x.device), format)
+    else:
+        fmt = _check_packed(out, n, cols, x.device, "out")
+    with _on_device(x.device):
+        _check(tcq_pack8(_ptr(x), xt, _ld(x), n, cols, fmt, _ptr(out.codes), _ptr(out.scales),
+                         _stream_on(x.device, stream)), "tcq_pack8")
+    return out
+
+
+def unpack8(packed: Packed8, dtype=None, out=None, stream=None):
+    """The values of an 8-bit checkpoint, as ``dtype`` (bfloat16 when not given) [n, cols]."""
+    torch = _torch()
+    n, cols = packed.codes.shape
+    dev = packed.codes.device
+    fmt = _check_packed(packed, n, cols, dev, "packed")
+    if out is None:
+        out = torch.empty((n, cols), dtype=dtype or torch.bfloat16, device=dev)
+    else:
+        _check_out(out, (n, cols), dtype or out.dtype, "out")
+        _same_device(dev, out=out)
+    xt = _x_dtype(out, "out")
+    with _on_device(dev):
+        _check(tcq_unpack8(_ptr(packed.codes), _ptr(packed.scales), fmt, n, cols, _ptr(out), xt, _ld(out),
+                           _stream_on(dev, stream)), "tcq_unpack8")
+    return out
+
+
+def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, cols: int, x, bias=None,
+         act: str = "none", residual=None, checkpoint=None, out=None, workspace=None, stream=None):
+    """act(x W^T + bias) + residual for a trellis-coded W [rows, cols] (gemv's blocks)
+    and ``x`` float16 or bfloat16 [n, cols]; [n, rows] of x's type.
+
+    ``bias`` float32 [rows]; ``residual`` like the result; ``checkpoint`` a Packed8 of
+    [n, rows] that receives the pre-activation in 8 bits.  ``workspace`` (uint8, at
+    least tcq_gemm_workspace_bytes) and ``out`` are allocated when not given."""
+    torch = _torch()
+    xt = _x_dtype(x, "x")
+    dev, n = x.device, x.shape[0]
+    if x.shape[1] != cols:
+        raise ValueError(f"gemm: x has {x.shape[1]} columns, the matrix {cols}")
+    a = _choice(ACTIVATIONS, act, "act")
+    _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, dev, "gemm")
+    if bias is not None and (bias.numel() != rows or bias.dtype != torch.float32 or not bias.is_contiguous()):
+        raise ValueError("gemm: bias must be a contiguous float32 tensor [rows]")
+    if residual is not None:
+        _check_out(residual, (n, rows), x.dtype, "residual")
+    if out is None:
+        out = torch.empty((n, rows), dtype=x.dtype, device=dev)
+    else:
+        _check_out(out, (n, rows), x.dtype, "out")
+    _same_device(dev, bias=bias, residual=residual, out=out)
+    zf = TCQ_Q8_INT8 if checkpoint is None else _check_packed(checkpoint, n, rows, dev, "checkpoint")
+    cb = cb_dtype_of(codebook)
+    with _on_device(dev):
+        ws = _scratch(workspace, tcq_gemm_workspace_bytes(L, k, T, rows, cols, n, cb), dev, "gemm")
+        _check(tcq_gemm(_ptr(bits), _ptr(start_state), _ptr(scale), _ptr(codebook), cb, L, k, T, rows, cols, _ptr(x),
+                        xt, _ld(x), n, _ptr(bias), a, _ptr(residual), 0 if residual is None else _ld(residual),
+                        _ptr(out), _ld(out), None if checkpoint is None else _ptr(checkpoint.codes),
+                        None if checkpoint is None else _ptr(checkpoint.scales), zf, _ptr(ws), ws.numel(),
+                        _stream_on(dev, stream)), "tcq_gemm")
+    return out
+
+
+def gemm_dgrad(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, cols: int, dz, out=None,
+               workspace=None, stream=None):
+    """dz W for a trellis-coded W [rows, cols] and ``dz`` float16 or bfloat16 [n, rows];
+    [n, cols] of dz's type."""
+    torch = _torch()
+    xt = _x_dtype(dz, "dz")
+    dev, n = dz.device, dz.shape[0]
+    if dz.shape[1] != rows:
+        raise ValueError(f"gemm_dgrad: dz has {dz.shape[1]} columns, the matrix {rows} rows")
+    _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, dev, "gemm_dgrad")
+    if out is None:
+        out = torch.empty((n, cols), dtype=dz.dtype, device=dev)
+    else:
+        _check_out(out, (n, cols), dz.dtype, "out")
+        _same_device(dev, out=out)
+    cb = cb_dtype_of(codebook)
+    with _on_device(dev):
+        ws = _scratch(workspace, tcq_gemm_dgrad_workspace_bytes(L, k, T, rows, cols, n, cb), dev, "gemm_dgrad")
+        _check(tcq_gemm_dgrad(_ptr(bits), _ptr(start_state), _ptr(scale), _ptr(codebook), cb, L, k, T, rows, cols,
+                              _ptr(dz), xt, _ld(dz), n, _ptr(out), _ld(out), _ptr(ws), ws.numel(),
+                              _stream_on(dev, stream)), "tcq_gemm_dgrad")
+    return out
+
+
+def act_grad8(dy, checkpoint, act: str, dbias: bool = True, out=None, workspace=None, stream=None):
+    """(dz, dbias): dy act'(z) in dy's type [n, rows] and its float32 column sums (None
+    unless ``dbias``), from the 8-bit checkpoint of the pre-activation (None for act
+    "none").  ``out`` may be ``dy``."""
+    torch = _torch()
+    xt = _x_dtype(dy, "dy")
+    dev = dy.device
+    n, rows = dy.shape
+    a = _choice(ACTIVATIONS, act, "act")
+    if checkpoint is None and a != TCQ_ACT_NONE:
+        raise ValueError(f"act_grad8: {act!r} needs the checkpoint of the pre-activation")
+    zf = TCQ_Q8_INT8 if checkpoint is None else _check_packed(checkpoint, n, rows, dev, "checkpoint")
+    if out is None:
+        out = torch.empty((n, rows), dtype=dy.dtype, device=dev)
+    else:
+        _check_out(out, (n, rows), dy.dtype, "out")
+        _same_device(dev, out=out)
+    db = torch.empty(rows, dtype=torch.float32, device=dev) if dbias else None
+    with _on_device(dev):
+        ws = _scratch(workspace, tcq_act_grad8_workspace_bytes(n, rows), dev, "act_grad8") if dbias else None
+        _check(tcq_act_grad8(_ptr(dy), xt, _ld(dy), None if checkpoint is None else _ptr(checkpoint.codes),
+                             None if checkpoint is None else _ptr(checkpoint.scales), zf, a, n, rows, _ptr(out),
+                             _ld(out), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), _stream_on(dev, stream)),
+               "tcq_act_grad8")
+    return out, db
+
+
+def wgrad8(dz, packed: Packed8, out=None, accumulate: bool = False, workspace=None, stream=None):
+    """dz^T x, float32 [rows, cols], for ``dz`` float16 or bfloat16 [n, rows] and the
+    8-bit checkpoint of x [n, cols]; added to ``out`` when ``accumulate``."""
+    torch = _torch()
+    xt = _x_dtype(dz, "dz")
+    dev = dz.device
+    n, rows = dz.shape
+    cols = packed.codes.shape[1]
+    fmt = _check_packed(packed, n, cols, dev, "packed")
+    if out is None:
+        if accumulate:
+            raise ValueError("wgrad8: accumulate needs out")
+        out = torch.empty((rows, cols), dtype=torch.float32, device=dev)
+    else:
+        _check_out(out, (rows, cols), torch.float32, "out")
+        _same_device(dev, out=out)
+    with _on_device(dev):
+        ws = _scratch(workspace, tcq_wgrad8_workspace_bytes(rows, cols, n), dev, "wgrad8")
+        _check(tcq_wgrad8(_ptr(dz), xt, _ld(dz), _ptr(packed.codes), _ptr(packed.scales), fmt, n, rows, cols,
+                          _ptr(out), _ld(out), int(accumulate), _ptr(ws), ws.numel(), _stream_on(dev, stream)),
+               "tcq_wgrad8")
     return out
 
 
