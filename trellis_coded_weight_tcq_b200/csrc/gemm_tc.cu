@@ -59,6 +59,7 @@ constexpr int kThreads = 256;
 struct __align__(1024) Smem {
     unsigned char a[kStages][kHalfBytes];
     unsigned char b[kStages][kHalfBytes];
+    float2 cols[2][kTile];  // (power of two, bias) of the columns of a tile, per accumulator set
     unsigned long long full[kStages], empty[kStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int stop;
@@ -74,18 +75,17 @@ struct Shape {
 // them below n.
 template <int KIND, int XT>
 __device__ __forceinline__ void store32_16bit(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                              int count, bool vec, float row_scale)
+                                              int count, bool vec, float row_scale, const float2* cols)
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= row_scale;
     if constexpr (KIND == kGemmForward) {
         if (e.col_scale || e.bias) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (i < count) {
-                    if (e.col_scale) v[i] *= __ldg(e.col_scale + c + i);
-                    if (e.bias) v[i] += __ldg(e.bias + c + i);
-                }
+            for (int i = 0; i < 32; i += 2) {  // two columns per 16-byte read, the same in every lane
+                const float4 p = *reinterpret_cast<const float4*>(cols + i);
+                v[i] = fmaf(v[i], p.x, p.y);
+                v[i + 1] = fmaf(v[i + 1], p.z, p.w);
             }
         }
         if (e.z_codes) {
@@ -175,7 +175,7 @@ __device__ __forceinline__ void store32_16bit(const Epilogue& e, long long r, lo
 // The same for either output type.
 template <int KIND, int XT>
 __device__ __forceinline__ void store32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                        bool vec, float row_scale)
+                                        bool vec, float row_scale, const float2* cols)
 {
     const int count = n - c < 32 ? (int)(n - c) : 32;
     if constexpr (KIND == kGemmWgrad) {
@@ -196,7 +196,7 @@ __device__ __forceinline__ void store32(const Epilogue& e, long long r, long lon
                 if (i < count) o[i] = e.accumulate ? o[i] + v[i] : v[i];
         }
     } else {
-        store32_16bit<KIND, XT>(e, r, c, n, v, count, vec, row_scale);
+        store32_16bit<KIND, XT>(e, r, c, n, v, count, vec, row_scale, cols);
     }
 }
 
@@ -308,6 +308,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         int done = 0;
         for (int t = pair; t < tiles; t += pairs, ++done) {
             const int acc = done & 1;
+            if constexpr (KIND == kGemmForward) {
+                // this tile's columns, while its product still runs; the set's last readers
+                // passed the barrier of the tile between
+                for (int i = threadIdx.x - 128; i < kTile; i += 128) {
+                    const long long c = (long long)(t / p.m_tiles) * kTile + i;
+                    S.cols[acc][i] = make_float2(e.col_scale && c < p.n ? __ldg(e.col_scale + c) : 1.f,
+                                                 e.bias && c < p.n ? __ldg(e.bias + c) : 0.f);
+                }
+                named_barrier(1, 128);
+            }
             bool ok = mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -320,7 +330,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 if (n0 + c >= p.n) break;
                 float v[32];
                 tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * 256 + c, v);
-                if (r < p.m) store32<KIND, XT>(e, r, n0 + c, p.n, v, vec, row_scale);
+                if (r < p.m) store32<KIND, XT>(e, r, n0 + c, p.n, v, vec, row_scale, S.cols[acc] + c);
                 __syncwarp();
             }
             tc_fence_before();
