@@ -36,40 +36,52 @@ __device__ __forceinline__ void stage_table(unsigned char* sm, const void* cb, i
     }
 }
 
-// The states of N consecutive weights whose first is weight t0 of its block (N | t0),
-// from the two stream words that end with the last window (word -1 is the start
-// state).  For N = 8, or 4, and k <= 4 the windows, N k + L - k <= 44 bits, lie in
-// those two words.
-template <int K, int N>
-__device__ __forceinline__ void windows(uint32_t hi, uint32_t lo, int t0, uint32_t mask, uint32_t (&s)[N])
+// Bytes of a table entry.
+__host__ __device__ constexpr int entry_bytes(int code) { return code == kCode16F32 ? 4 : code == kCode16F16 ? 2 : 1; }
+
+// Weight i of N consecutive ones whose windows end with the two words b:a (the last
+// window in a's low bits): the state times the entry size, so that a table look-up
+// needs no further shift.  For N = 8, or 4, and k <= 4 the windows, N k + L - k <= 44
+// bits, lie in the two words.
+template <int K, int N, int CODE>
+__device__ __forceinline__ uint32_t window_offset(uint32_t b, uint32_t a, int i, uint32_t mask)
 {
-    const int down = (32 - ((K * (t0 + N)) & 31)) & 31;  // stream bits behind the last window in lo
+    constexpr int up = CODE == kCode16F32 ? 2 : CODE == kCode16F16 ? 1 : 0;
+    const int sh = (N - 1 - i) * K - up;
+    const uint32_t w = sh < 0 ? a << -sh : sh + up <= 16 ? a >> sh : __funnelshift_r(a, b, sh);
+    return w & (mask << up);
+}
+
+// The codeword at an offset from window_offset.
+template <int CODE>
+__device__ __forceinline__ float codeword_at(const unsigned char* tab, uint32_t offset)
+{
+    if constexpr (CODE == kCode16Mad)
+        return mad_codeword(offset);
+    else if constexpr (CODE == kCode16F16)
+        return __half2float(*reinterpret_cast<const __half*>(tab + offset));
+    else
+        return *reinterpret_cast<const float*>(tab + offset);
+}
+
+// N weights, scale * c[s] rounded once to binary16, in pairs (the first in the low half);
+// `down`: stream bits of lo behind the last window.
+template <int K, int N, int CODE>
+__device__ __forceinline__ void decode_weights(uint32_t hi, uint32_t lo, int down, uint32_t mask,
+                                               const unsigned char* tab, float scale, uint32_t* out)
+{
     const uint32_t a = __funnelshift_r(lo, hi, down), b = hi >> down;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int sh = (N - 1 - i) * K;
-        s[i] = (sh <= 16 ? a >> sh : __funnelshift_r(a, b, sh)) & mask;
+    for (int i = 0; i < N; i += 2) {
+        const float c0 = codeword_at<CODE>(tab, window_offset<K, N, CODE>(b, a, i, mask));
+        const float c1 = codeword_at<CODE>(tab, window_offset<K, N, CODE>(b, a, i + 1, mask));
+        const __half2 h = __floats2half2_rn(c0 * scale, c1 * scale);
+        out[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
     }
 }
 
-// Two weights, scale * c[s] rounded to binary16 (the first in the low half).
-template <int CODE>
-__device__ __forceinline__ uint32_t weight_pair(uint32_t s0, uint32_t s1, const unsigned char* tab, float scale)
-{
-    float c0, c1;
-    if constexpr (CODE == kCode16Mad) {
-        c0 = mad_codeword(s0);
-        c1 = mad_codeword(s1);
-    } else if constexpr (CODE == kCode16F16) {
-        c0 = __half2float(reinterpret_cast<const __half*>(tab)[s0]);
-        c1 = __half2float(reinterpret_cast<const __half*>(tab)[s1]);
-    } else {
-        c0 = reinterpret_cast<const float*>(tab)[s0];
-        c1 = reinterpret_cast<const float*>(tab)[s1];
-    }
-    const __half2 h = __floats2half2_rn(c0 * scale, c1 * scale);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
+// Stream bits of a word behind the window that ends at stream bit `end`.
+__device__ __forceinline__ int bits_behind(int end) { return (32 - (end & 31)) & 31; }
 
 // Bits of |v|, or 0 for an infinity or NaN (magnitudes then compare as integers).
 __device__ __forceinline__ uint32_t finite_magnitude(float v)
@@ -86,11 +98,14 @@ __device__ __forceinline__ int power_above(uint32_t magnitude)
     return p;
 }
 
-// 2^e with e held to the normal range.
+// 2^e with e held to -126 .. 126, so that its inverse is a normal number too.
 __device__ __forceinline__ float pow2_clamped(int e)
 {
-    e = e < -126 ? -126 : e > 127 ? 127 : e;
+    e = e < -126 ? -126 : e > 126 ? 126 : e;
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
+
+// The inverse of such a power.
+__device__ __forceinline__ float inverse_pow2(float p) { return __uint_as_float(0x7f000000u - __float_as_uint(p)); }
 
 }  // namespace tcq

@@ -59,7 +59,8 @@ cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, floa
                             cudaStream_t stream);
 
 // x [n, cols] as binary16 rows over a power of two each (row_pow2[n]); col_pow2
-// (or nullptr) multiplies the columns first.
+// (or nullptr) multiplies the columns first.  Follows launch_decode16 in the stream and
+// runs beside it; col_pow2 may be the row powers that launch wrote.
 cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long long n, long long cols,
                               const float* col_pow2, void* out, long long ldo, float* row_pow2, cudaStream_t stream);
 // 16-bit rows copied to another stride.

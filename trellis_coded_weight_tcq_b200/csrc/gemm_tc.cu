@@ -19,6 +19,7 @@
 #include "q8.cuh"
 #include "tc.cuh"
 #include "decode16.cuh"
+#include "pdl.cuh"
 
 namespace tcq {
 
@@ -380,7 +381,8 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigne
 // ---- operand passes
 // One CTA per row: the row's largest finite magnitude, then the row over the power of
 // two that brings it to [2^14, 2^15).  Memory bound (2 bytes read twice, the second
-// time from L2, and 2 written per element).
+// time from L2, and 2 written per element).  It starts while the matrix is decoded,
+// which is bound by shared-memory lookups: the two run side by side.
 constexpr int kRowThreads = 256;
 
 template <int XT>
@@ -440,6 +442,7 @@ __global__ void __launch_bounds__(kRowThreads) scale_rows_kernel(const uint16_t*
     }
     for (long long c = vcols + threadIdx.x; c < cols; c += kRowThreads)
         o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (col_pow2 ? col_pow2[c] : 1.f) * inv);
+    pdl_wait();  // ends after the decode that it ran beside
 }
 
 __global__ void __launch_bounds__(256) copy16_kernel(const uint16_t* x, long long ldx, long long n, long long cols,
@@ -476,11 +479,9 @@ cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long lon
     const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
     const uint16_t* xi = static_cast<const uint16_t*>(x);
     uint16_t* o = static_cast<uint16_t*>(out);
-    if (xdtype == TCQ_X_BF16)
-        scale_rows_kernel<TCQ_X_BF16><<<(unsigned)n, kRowThreads, 0, stream>>>(xi, ldx, cols, col_pow2, o, ldo, row_pow2, vec);
-    else
-        scale_rows_kernel<TCQ_X_F16><<<(unsigned)n, kRowThreads, 0, stream>>>(xi, ldx, cols, col_pow2, o, ldo, row_pow2, vec);
-    return cudaGetLastError();
+    return launch_pdl(xdtype == TCQ_X_BF16 ? scale_rows_kernel<TCQ_X_BF16> : scale_rows_kernel<TCQ_X_F16>,
+                      dim3((unsigned)n), dim3(kRowThreads), 0, stream, true, xi, ldx, cols, col_pow2, o, ldo, row_pow2,
+                      vec);
 }
 
 cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
