@@ -537,8 +537,8 @@ tcq_status tcq_ub8_decode(const uint32_t* bits, const uint32_t* start_state, con
  *                            targets for its rows and freed its tensor memory;
  *                            the affected blocks then carry non-finite costs.
  *                            The products of tcq_gemm, tcq_gemm_dgrad and
- *                            tcq_wgrad8 stop the same way and leave the outputs
- *                            of the tiles not yet finished unwritten.
+ *                            tcq_wgrad8 stop the same way; the outputs of the
+ *                            call are then unspecified.
  *   TCQ_DEVERR_BOUNDS        an index failed its bounds check and the access
  *                            was skipped (only the TCQ_DEBUG build,
  *                            libtcq_debug.so, checks indices).

@@ -163,12 +163,17 @@ cudaError_t launch_k(const CodedMatrix& w, void* out, long long ldw, const float
 
 }  // namespace
 
+cudaError_t launch_row_pow2(const CodedMatrix& w, float* row_pow2, cudaStream_t stream)
+{
+    row_pow2_kernel<<<(unsigned)((w.rows + 7) / 8), 256, 0, stream>>>(w.scale, w.rows, w.cols / w.T, row_pow2);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, int num_sms,
                             cudaStream_t stream)
 {
     if (w.scale) {
-        row_pow2_kernel<<<(unsigned)((w.rows + 7) / 8), 256, 0, stream>>>(w.scale, w.rows, w.cols / w.T, row_pow2);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_row_pow2(w, row_pow2, stream);
         if (e != cudaSuccess) return e;
     }
     switch (w.cb_f16) {

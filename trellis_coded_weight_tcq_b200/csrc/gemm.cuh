@@ -59,13 +59,28 @@ cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, floa
                             cudaStream_t stream);
 
 // x [n, cols] as binary16 rows over a power of two each (row_pow2[n]); col_pow2
-// (or nullptr) multiplies the columns first.  Follows launch_decode16 in the stream and
-// runs beside it; col_pow2 may be the row powers that launch wrote.
+// (or nullptr) multiplies the columns first.  `early`: the launch before it in the
+// stream is one of this call's (launch_decode16, launch_row_pow2), which it may run
+// beside; col_pow2 may then be the row powers that launch_decode16 read.
 cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long long n, long long cols,
-                              const float* col_pow2, void* out, long long ldo, float* row_pow2, cudaStream_t stream);
+                              const float* col_pow2, void* out, long long ldo, float* row_pow2, bool early,
+                              cudaStream_t stream);
 // 16-bit rows copied to another stride.
 cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
                           int num_sms, cudaStream_t stream);
+
+// The forward product with the decoding inside it, for up to kFusedMaxTokens tokens:
+// x binary16 [n, cols] (ldx a multiple of 8, 16-byte aligned).  `early`: the launch
+// before it in the stream is one of this call's, which it may start beside.
+constexpr long long kFusedMaxTokens = 1024;
+bool fused_shape(int T, long long rows, long long cols, long long n);
+size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms);
+cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx, long long n, int xdtype,
+                              const float* row_pow2, float* partial, const Epilogue& e, int num_sms, unsigned int* err,
+                              bool early, cudaStream_t stream);
+
+// The powers of two of W's rows (launch_decode16 includes it).
+cudaError_t launch_row_pow2(const CodedMatrix& w, float* row_pow2, cudaStream_t stream);
 
 cudaError_t launch_pack8(const void* x, int xdtype, long long ldx, long long n, long long cols, int format,
                          uint8_t* codes, uint8_t* scales, int num_sms, cudaStream_t stream);

@@ -58,28 +58,39 @@ bool matrix_pointers(const uint32_t* bits, const uint32_t* start, const float* s
            (dt == TCQ_MAD || (cb && aligned(cb, dt == TCQ_F16 ? 2 : 4)));
 }
 
+int code_mode(tcq_dtype dt) { return dt == TCQ_F16 ? 1 : dt == TCQ_MAD ? kMadCodebook : 0; }
+
 CodedMatrix matrix(const uint32_t* bits, const uint32_t* start, const float* scale, const void* cb, tcq_dtype dt, int L,
                    int k, int T, int64_t rows, int64_t cols)
 {
-    return {bits, start, scale, cb, dt == TCQ_F16 ? 1 : dt == TCQ_MAD ? kMadCodebook : 0, L, k, T,
+    return {bits, start, scale, cb, code_mode(dt), L, k, T,
             tcq_words_per_block(k, T), rows, cols};
 }
 
 // Workspace of a product: the binary16 matrix, its row powers, the binary16
 // activations (rows of `inner` elements) and theirs.
 struct GemmSpace {
-    size_t weights, row_pow2, x, x_pow2, total;
+    size_t row_pow2, x, x_pow2, total;
 };
 
-GemmSpace gemm_space(int64_t rows, int64_t cols, int64_t n, int64_t inner)
+// `weights`: bytes of the binary16 matrix, or of the partial sums in its place
+GemmSpace gemm_space(size_t weights, int64_t rows, int64_t n, int64_t inner)
 {
     GemmSpace s;
-    s.weights = 0;
-    s.row_pow2 = align256((size_t)rows * round_up(cols, 8) * 2);
+    s.row_pow2 = align256(weights);
     s.x = s.row_pow2 + align256((size_t)rows * 4);
     s.x_pow2 = s.x + align256((size_t)n * round_up(inner, 8) * 2);
     s.total = s.x_pow2 + align256((size_t)n * 4);
     return s;
+}
+
+size_t matrix16_bytes(int64_t rows, int64_t cols) { return (size_t)rows * round_up(cols, 8) * 2; }
+
+GemmSpace forward_space(tcq_dtype dt, int L, int T, int64_t rows, int64_t cols, int64_t n, int num_sms)
+{
+    const bool fused = fused_shape(T, rows, cols, n);
+    return gemm_space(fused ? fused_partial_bytes(code_mode(dt), L, rows, cols, n, num_sms) : matrix16_bytes(rows, cols),
+                      rows, n, cols);
 }
 
 Epilogue plain_epilogue(void* out, int64_t ldo)
@@ -100,7 +111,8 @@ size_t tcq_gemm_workspace_bytes(int L, int k, int T, int64_t rows, int64_t cols,
 {
     if (check_matrix(cb_dtype, L, k, T, rows, cols) != TCQ_OK || !valid_dim(n) || n == 0 || rows == 0 || cols == 0)
         return 0;
-    return gemm_space(rows, cols, n, cols).total;
+    const int num_sms = sms();
+    return forward_space(cb_dtype, L, T, rows, cols, n, num_sms > 0 ? num_sms : 148).total;
 }
 
 tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const float* scale, const void* codebook,
@@ -117,9 +129,9 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
         !valid_rows(y, ldy, rows) || (residual && !valid_rows(residual, ldr, rows)) || (bias && !aligned(bias, 4)) ||
         (z_codes == nullptr) != (z_scales == nullptr) || !workspace || !aligned(workspace, 256))
         return TCQ_ERR_INVALID_ARG;
-    const GemmSpace sp = gemm_space(rows, cols, n, cols);
-    if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
     const int num_sms = sms();
+    const GemmSpace sp = forward_space(cb_dtype, L, T, rows, cols, n, num_sms > 0 ? num_sms : 148);
+    if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
     if (num_sms <= 0) return TCQ_ERR_CUDA;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     unsigned int* err = device_error_word(st);
@@ -129,13 +141,17 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     const CodedMatrix w = matrix(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols);
     const int64_t ldw = round_up(cols, 8);
 
-    cudaError_t e = launch_decode16(w, ws, ldw, row_pow2, num_sms, st);
+    const bool fused = fused_shape(T, rows, cols, n);
+    cudaError_t e = !fused  ? launch_decode16(w, ws, ldw, row_pow2, num_sms, st)
+                    : scale ? launch_row_pow2(w, row_pow2, st)
+                            : cudaSuccess;
     if (e != cudaSuccess) return TCQ_ERR_CUDA;
     GemmProblem p = {x, ldx, ws, ldw, n, rows, cols, 0, xdtype};
     Epilogue ep = plain_epilogue(y, ldy);
     // binary16 rows that TMA can read are used where they are
-    if (xdtype != TCQ_X_F16 || !direct(x, ldx)) {
-        e = launch_scale_rows(x, xdtype, ldx, n, cols, nullptr, ws + sp.x, ldw, x_pow2, st);
+    const bool scaled = xdtype != TCQ_X_F16 || !direct(x, ldx);
+    if (scaled) {
+        e = launch_scale_rows(x, xdtype, ldx, n, cols, nullptr, ws + sp.x, ldw, x_pow2, !fused || scale, st);
         if (e != cudaSuccess) return TCQ_ERR_CUDA;
         p.a = ws + sp.x;
         p.lda = ldw;
@@ -149,6 +165,9 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     ep.z_codes = z_codes;
     ep.z_scales = z_scales;
     ep.z_format = z_format;
+    if (fused)
+        return status(launch_gemm_fused(w, p.a, p.lda, n, xdtype, row_pow2, reinterpret_cast<float*>(ws), ep, num_sms, err,
+                                        scaled || scale, st));
     return status(launch_gemm_tc(kGemmForward, p, ep, num_sms, err, st));
 }
 
@@ -156,7 +175,7 @@ size_t tcq_gemm_dgrad_workspace_bytes(int L, int k, int T, int64_t rows, int64_t
 {
     if (check_matrix(cb_dtype, L, k, T, rows, cols) != TCQ_OK || !valid_dim(n) || n == 0 || rows == 0 || cols == 0)
         return 0;
-    return gemm_space(rows, cols, n, rows).total;
+    return gemm_space(matrix16_bytes(rows, cols), rows, n, rows).total;
 }
 
 tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, const float* scale, const void* codebook,
@@ -174,7 +193,7 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
     if (!matrix_pointers(bits, start_state, scale, codebook, cb_dtype) || !valid_rows(dz, lddz, rows) || !workspace ||
         !aligned(workspace, 256))
         return TCQ_ERR_INVALID_ARG;
-    const GemmSpace sp = gemm_space(rows, cols, n, rows);
+    const GemmSpace sp = gemm_space(matrix16_bytes(rows, cols), rows, n, rows);
     if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
     const int num_sms = sms();
     if (num_sms <= 0) return TCQ_ERR_CUDA;
@@ -192,7 +211,8 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
     // W's rows run along the reduction: their powers go with dZ's columns
     if (xdtype != TCQ_X_F16 || scale || !direct(dz, lddz)) {
         const int64_t ldz = round_up(rows, 8);
-        e = launch_scale_rows(dz, xdtype, lddz, n, rows, scale ? row_pow2 : nullptr, ws + sp.x, ldz, x_pow2, st);
+        e = launch_scale_rows(dz, xdtype, lddz, n, rows, scale ? row_pow2 : nullptr, ws + sp.x, ldz, x_pow2, true,
+                              st);
         if (e != cudaSuccess) return TCQ_ERR_CUDA;
         p.a = ws + sp.x;
         p.lda = ldz;

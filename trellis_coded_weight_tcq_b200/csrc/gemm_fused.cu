@@ -1,0 +1,424 @@
+// gemm_fused.cu -- the forward product for small batches: the matrix is decoded
+// inside the product and never written out.
+//
+// With few tokens the product is bound by decoding (one shared-memory lookup per
+// weight, about 3.5 bank passes per 32 random entries), so every weight is decoded
+// once per 256 tokens and goes straight into a tensor-core operand tile.  The
+// weights take the M side of the MMA: a CTA multiplies 128 rows of W by up to 256
+// tokens, D[row, token] in tensor memory (cta_group::1, 128 x N x 16).
+//
+// 16 warps decode, in four groups: a lane owns one row and turns the stream words of
+// 64 columns (one stage) into eight 16-byte pieces of the swizzled K-major tile, held
+// in registers until the stage is free.  Group g takes stages g, g + 4, ..., so four
+// stages are decoded at a time while the words of the next four are on their way.
+// Warp 16 loads the activations' tiles by TMA, one thread of warp 17 issues the MMAs.
+//
+// Work is split over the SMs evenly, in stages: a CTA takes a contiguous run of
+// (tile, stage) pairs, so a tile's reduction may be cut into pieces; each writes its
+// fp32 sums to the workspace, and a second kernel adds a tile's pieces in order and
+// applies the epilogue.  The split depends on the shape and the SM count only.
+#include "decode16.cuh"
+#include "gemm.cuh"
+#include "pdl.cuh"
+#include "q8.cuh"
+#include "tc.cuh"
+
+namespace tcq {
+
+namespace {
+
+constexpr int kDecodeWarps = 16;
+constexpr int kThreads = (kDecodeWarps + 2) * 32;
+constexpr int kRows = 128;             // rows of W per tile
+constexpr int kDepth = 64;             // columns per stage
+constexpr int kABytes = kRows * kDepth * 2;
+constexpr int kMaxStages = 8;
+constexpr int kSmemBytes = 227 * 1024;
+
+struct Barriers {
+    unsigned long long afull[kMaxStages], bfull[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int stop;
+    int fills[kMaxStages];  // warps that have filled a stage, ever
+};
+
+struct Plan {
+    long long n;          // tokens
+    int np;               // tokens per tile, a multiple of 16
+    int row_tiles, token_tiles;
+    int steps;            // stages of a whole reduction
+    long long units;      // tiles * steps
+    int ctas;
+    int pieces;           // slots per tile in the workspace
+    int stages;           // ring depth
+    int tmem_columns;
+    int table;            // shared-memory bytes of the table, a multiple of 1024
+};
+
+// the CTA that has unit u, and the first unit of a CTA
+__host__ __device__ inline long long first_unit(const Plan& p, long long cta) { return p.units * cta / p.ctas; }
+__host__ __device__ inline int cta_of(const Plan& p, long long u) { return (int)(((u + 1) * p.ctas - 1) / p.units); }
+
+// 2 K stream words of a lane's 64 columns, in the widest loads their alignment allows
+// (`wide`: the stream starts on a 16-byte boundary)
+template <int K>
+__device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[2 * K], bool wide)
+{
+    if (!wide) {
+#pragma unroll
+        for (int i = 0; i < 2 * K; ++i) w[i] = __ldg(p + i);
+    } else if constexpr (K % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * K; i += 4) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + i));
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * K; i += 2) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + i));
+            w[i] = v.x; w[i + 1] = v.y;
+        }
+    }
+}
+
+template <int K, int CODE>
+__global__ void __launch_bounds__(kThreads, 1)
+fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, const float* row_pow2, float* partial,
+             unsigned int* err)
+{
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char* ring = sm + p.table;
+    const int bbytes = p.np * kDepth * 2;
+    const int sbytes = kABytes + bbytes;
+    Barriers& B = *reinterpret_cast<Barriers*>(ring + (size_t)p.stages * sbytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(smem_addr(&B.afull[i]), 4);
+            mbar_init(smem_addr(&B.bfull[i]), 1);
+            mbar_init(smem_addr(&B.empty[i]), 1);
+            B.fills[i] = 0;
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&B.tfull[i]), 1);
+            mbar_init(smem_addr(&B.tempty[i]), kDecodeWarps);
+        }
+        mbar_init(smem_addr(&B.drain), 1);
+        B.stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        tma_prefetch_map(&map_x);
+    }
+    if (warp == kDecodeWarps + 1) tmem_alloc<1>(smem_addr(&B.tmem), p.tmem_columns);
+    stage_table<CODE>(sm, w.cb, w.cb_f16, w.L);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();  // the scaled activations and the row powers
+    pdl_release();
+    const uint32_t tmem = B.tmem;
+    volatile int* stop = &B.stop;
+    const long long u0 = first_unit(p, blockIdx.x), u1 = first_unit(p, blockIdx.x + 1);
+    const int acc_columns = p.tmem_columns / 2;
+
+    if (warp < kDecodeWarps) {
+        const int group = warp >> 2;
+        const int r = (warp & 3) * 32 + lane;  // row of the tile
+        const uint32_t mask = (1u << w.L) - 1u;
+        const int nb = (int)(w.cols / w.T), spb = w.T / kDepth;  // stages per block
+        const long long row_words = (long long)p.steps * 2 * K;
+        const bool wide = (reinterpret_cast<uintptr_t>(w.bits) & 15) == 0;
+        // the words, the word before them and the scale of this lane's part of unit u
+        auto fetch = [&](long long u, uint32_t (&words)[2 * K], uint32_t& prev, float& sc) {
+            const long long tile = u / p.steps;
+            const int ks = (int)(u - tile * p.steps);
+            const long long row = (tile % p.row_tiles) * kRows + r;
+            sc = 0.f;
+            prev = 0u;
+#pragma unroll
+            for (int i = 0; i < 2 * K; ++i) words[i] = 0u;
+            if (row < w.rows) {
+                const uint32_t* q = w.bits + row * row_words + ks * 2 * K;
+                const int j = ks / spb;
+                load_words<K>(q, words, wide);
+                prev = __ldg(ks == j * spb ? w.start_state + row * nb + j : q - 1);
+                sc = w.scale ? __ldg(w.scale + row * nb + j) * inverse_pow2(__ldg(row_pow2 + row)) : 1.f;
+            }
+        };
+        uint32_t words[2 * K], prev;
+        float sc;
+        long long u = u0 + group;
+        if (u < u1) fetch(u, words, prev, sc);
+        bool ok = true;
+        int done = 0;
+        for (long long s0 = u0; s0 < u1 && ok; ++done) {  // segments: runs of one tile's stages
+            const long long tile = s0 / p.steps;
+            const long long s1 = (tile + 1) * p.steps < u1 ? (tile + 1) * p.steps : u1;
+            for (; u < s1; u += 4) {
+                const int it = (int)(u - u0), slot = it % p.stages;
+                uint32_t nwords[2 * K], nprev;
+                float nsc;
+                if (u + 4 < u1) fetch(u + 4, nwords, nprev, nsc);
+                uint32_t v[32];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    constexpr int bits = 8 * K;
+                    const int e = (bits * (q + 1) - 1) >> 5;
+                    decode_weights<K, 8, CODE>(e > 0 ? words[e > 0 ? e - 1 : 0] : prev, words[e],
+                                               bits_behind(bits * (q + 1)), mask, sm, sc, v + 4 * q);
+                }
+                // A barrier's parity tells two neighbouring phases apart.  With four or more
+                // stages the wait four units ago puts this one's phase next; with fewer,
+                // the group must first see the slot's fill before its own.
+                const int round = it / p.stages;
+                if (p.stages < 4) ok = wait_count(&B.fills[slot], 4 * round, stop, err);
+                ok = ok && mbar_wait(smem_addr(&B.empty[slot]), (round & 1) ^ 1, stop, err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                unsigned char* a = ring + (size_t)slot * sbytes + r * 128;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<uint4*>(a + ((q ^ (r & 7)) << 4)) =
+                        make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&B.afull[slot]));
+                    if (p.stages < 4) atomicAdd(&B.fills[slot], 1);
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * K; ++i) words[i] = nwords[i];
+                prev = nprev;
+                sc = nsc;
+            }
+            if (!ok) break;
+            // the segment's sums: lane = row, 16 tokens at a time shared among the groups
+            const int acc = done & 1;
+            ok = mbar_wait(smem_addr(&B.tfull[acc]), (done >> 1) & 1, stop, err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int piece = (int)blockIdx.x - cta_of(p, tile * p.steps);
+            float* out = partial + ((tile * p.pieces + piece) * p.np) * kRows + r;
+            const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * acc_columns;
+            for (int c = 16 * group; c < p.np; c += 64) {
+                float d[16];
+                tmem_load16(lanes + c, d);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) __stcg(out + (long long)(c + i) * kRows, d[i]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&B.tempty[acc]));
+            s0 = s1;
+        }
+    } else if (warp == kDecodeWarps) {
+        if (lane == 0) {
+            bool ok = true;
+            int it = 0;
+            for (long long u = u0; u < u1; ++u, ++it) {
+                const int slot = it % p.stages;
+                ok = mbar_wait(smem_addr(&B.empty[slot]), ((it / p.stages) & 1) ^ 1, stop, err);
+                if (!ok) break;
+                const long long tile = u / p.steps;
+                const int ks = (int)(u - tile * p.steps);
+                mbar_expect_tx(smem_addr(&B.bfull[slot]), bbytes);
+                tma_load_2d(smem_addr(ring + (size_t)slot * sbytes + kABytes), &map_x, smem_addr(&B.bfull[slot]),
+                            ks * kDepth, (int)(tile / p.row_tiles) * p.np);
+            }
+            if (!ok)  // what was loaded last is still waited for
+                for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
+                    mbar_drain(smem_addr(&B.bfull[i % p.stages]), (i / p.stages) & 1);
+        }
+        __syncwarp();
+    } else {
+        if (lane == 0) {
+            const uint32_t idesc = mma_idesc(kRows, p.np, 0, 0, 0);
+            bool ok = true;
+            int done = 0;
+            for (long long s0 = u0; s0 < u1 && ok; ++done) {
+                const long long tile = s0 / p.steps;
+                const long long s1 = (tile + 1) * p.steps < u1 ? (tile + 1) * p.steps : u1;
+                const int acc = done & 1;
+                ok = mbar_wait(smem_addr(&B.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
+                if (!ok) break;
+                tc_fence_after();
+                for (long long u = s0; u < s1; ++u) {
+                    const int it = (int)(u - u0), slot = it % p.stages;
+                    ok = mbar_wait(smem_addr(&B.bfull[slot]), (it / p.stages) & 1, stop, err) &&
+                         mbar_wait(smem_addr(&B.afull[slot]), (it / p.stages) & 1, stop, err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = smem_addr(ring + (size_t)slot * sbytes), b = a + kABytes;
+#pragma unroll
+                    for (int j = 0; j < kDepth / 16; ++j)
+                        mma_f16<1>(tmem + acc * acc_columns, smem_desc_sw128(a + 32 * j, 16),
+                                   smem_desc_sw128(b + 32 * j, 16), idesc, u != s0 || j != 0);
+                    mma_commit<1>(smem_addr(&B.empty[slot]));
+                }
+                if (ok) mma_commit<1>(smem_addr(&B.tfull[acc]));
+                s0 = s1;
+            }
+            if (!ok) {
+                mma_commit<1>(smem_addr(&B.drain));
+                mbar_drain(smem_addr(&B.drain), 0);
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kDecodeWarps + 1) {
+        tc_fence_after();
+        tmem_free<1>(tmem, p.tmem_columns);
+    }
+}
+
+// Adds a tile's pieces in order and applies the epilogue: a warp takes one token of a
+// tile, four rows of W per lane.
+template <int XT>
+__global__ void __launch_bounds__(256) fused_finish_kernel(Plan p, Epilogue e, long long rows, const float* partial,
+                                                           bool vec)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long tile = blockIdx.x;
+    const long long t = (tile / p.row_tiles) * p.np + (long long)blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int local = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (local >= p.np || t >= p.n) return;
+    const long long r = (tile % p.row_tiles) * kRows + 4 * lane;
+    const int pieces = cta_of(p, (tile + 1) * p.steps - 1) - cta_of(p, tile * p.steps) + 1;
+    const float* src = partial + (tile * p.pieces * p.np + local) * kRows + 4 * lane;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < pieces; ++i) {
+        const float4 d = __ldcg(reinterpret_cast<const float4*>(src + (long long)i * p.np * kRows));
+        v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
+    }
+    const int count = rows - r < 4 ? (rows - r > 0 ? (int)(rows - r) : 0) : 4;
+    const float rs = e.row_scale ? __ldg(e.row_scale + t) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] *= rs;
+        if (i < count) v[i] = fmaf(v[i], e.col_scale ? __ldg(e.col_scale + r + i) : 1.f, e.bias ? __ldg(e.bias + r + i) : 0.f);
+    }
+    if (e.z_codes) {  // a group of 32 is eight lanes
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool int8 = e.z_format == TCQ_Q8_INT8;
+        const uint32_t byte = int8 ? q8_scale_byte<TCQ_Q8_INT8>(top) : q8_scale_byte<TCQ_Q8_E4M3>(top);
+        const float inv = q8_inv(byte);
+        if (count > 0 && (lane & 7) == 0) e.z_scales[t * ((rows + 31) / 32) + r / 32] = (uint8_t)byte;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count)
+                e.z_codes[t * rows + r + i] = byte == 255u ? 0 : (uint8_t)(int8 ? q8_encode<TCQ_Q8_INT8>(v[i], inv)
+                                                                              : q8_encode<TCQ_Q8_E4M3>(v[i], inv));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], e.act);
+    uint16_t* out = static_cast<uint16_t*>(e.out) + t * e.ldo + r;
+    const uint16_t* res = e.residual ? static_cast<const uint16_t*>(e.residual) + t * e.ldr + r : nullptr;
+    if (vec && count == 4) {
+        if (res) {
+            const uint2 q = *reinterpret_cast<const uint2*>(res);
+            const float2 a = x_unpack2<XT>(q.x), b = x_unpack2<XT>(q.y);
+            v[0] += a.x; v[1] += a.y; v[2] += b.x; v[3] += b.y;
+        }
+        *reinterpret_cast<uint2*>(out) = make_uint2(x_pack2<XT>(v[0], v[1]), x_pack2<XT>(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) out[i] = x_bits<XT>(res ? v[i] + x_load<XT>(res, i) : v[i]);
+    }
+}
+
+int code_of(const CodedMatrix& w) { return w.cb_f16 == 1 ? kCode16F16 : w.cb_f16 == 0 ? kCode16F32 : kCode16Mad; }
+
+Plan make_plan(int code, int L, long long rows, long long cols, long long n, int num_sms)
+{
+    Plan p;
+    p.n = n;
+    const long long tt = (n + 255) / 256;
+    p.token_tiles = (int)tt;
+    p.np = (int)(((n + tt - 1) / tt + 15) / 16 * 16);
+    p.row_tiles = (int)((rows + kRows - 1) / kRows);
+    p.steps = (int)(cols / kDepth);
+    p.units = (long long)p.row_tiles * p.token_tiles * p.steps;
+    // at least four stages per CTA, one for each group of decoding warps
+    long long ctas = (p.units + 3) / 4;
+    if (ctas > num_sms) ctas = num_sms;
+    p.ctas = (int)ctas;
+    const long long least = p.units / p.ctas;  // a tile meets at most this many CTAs
+    p.pieces = (int)((p.steps + least - 1) / least + 1);
+    if (p.pieces > p.ctas) p.pieces = p.ctas;
+    p.table = (int)((table_bytes(code, L) + 1023) & ~(size_t)1023);
+    p.stages = (kSmemBytes - p.table - (int)sizeof(Barriers)) / (kABytes + p.np * kDepth * 2);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.tmem_columns = 32;
+    while (p.tmem_columns < 2 * p.np) p.tmem_columns *= 2;
+    return p;
+}
+
+template <int K, int CODE>
+cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const Plan& p, const float* row_pow2, float* partial,
+                   unsigned int* err, bool early, cudaStream_t stream)
+{
+    const cudaError_t e = cudaFuncSetAttribute(fused_kernel<K, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const size_t smem = p.table + (size_t)p.stages * (kABytes + p.np * kDepth * 2) + sizeof(Barriers);
+    return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, p, row_pow2,
+                      partial, err);
+}
+
+template <int CODE>
+cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const Plan& p, const float* row_pow2, float* partial,
+                     unsigned int* err, bool early, cudaStream_t stream)
+{
+    switch (w.K) {
+    case 1: return launch<1, CODE>(w, map, p, row_pow2, partial, err, early, stream);
+    case 2: return launch<2, CODE>(w, map, p, row_pow2, partial, err, early, stream);
+    case 3: return launch<3, CODE>(w, map, p, row_pow2, partial, err, early, stream);
+    default: return launch<4, CODE>(w, map, p, row_pow2, partial, err, early, stream);
+    }
+}
+
+}  // namespace
+
+// T a multiple of 64 keeps a stage inside one block and its words together.
+bool fused_shape(int T, long long rows, long long cols, long long n)
+{
+    return T % kDepth == 0 && n <= kFusedMaxTokens && rows / kRows * ((n + 255) / 256) * (cols / kDepth) < (1ll << 30);
+}
+
+size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms)
+{
+    const int code = cb_f16 == 1 ? kCode16F16 : cb_f16 == 0 ? kCode16F32 : kCode16Mad;
+    const Plan p = make_plan(code, L, rows, cols, n, num_sms);
+    return (size_t)p.row_tiles * p.token_tiles * p.pieces * p.np * kRows * sizeof(float);
+}
+
+cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx, long long n, int xdtype,
+                              const float* row_pow2, float* partial, const Epilogue& e, int num_sms, unsigned int* err,
+                              bool early, cudaStream_t stream)
+{
+    const int code = code_of(w);
+    const Plan p = make_plan(code, w.L, w.rows, w.cols, n, num_sms);
+    CUtensorMap map;
+    if (!make_map_16bit(&map, x, n, w.cols, ldx, p.np)) return cudaErrorInvalidValue;
+    cudaError_t st = code == kCode16Mad   ? launch_k<kCode16Mad>(w, map, p, row_pow2, partial, err, early, stream)
+                     : code == kCode16F16 ? launch_k<kCode16F16>(w, map, p, row_pow2, partial, err, early, stream)
+                                          : launch_k<kCode16F32>(w, map, p, row_pow2, partial, err, early, stream);
+    if (st != cudaSuccess) return st;
+    bool vec = (reinterpret_cast<uintptr_t>(e.out) & 7) == 0 && e.ldo % 4 == 0;
+    if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 7) == 0 && e.ldr % 4 == 0;
+    const dim3 grid((unsigned)(p.row_tiles * p.token_tiles), (unsigned)((p.np + 7) / 8));
+    return launch_pdl(xdtype == TCQ_X_BF16 ? fused_finish_kernel<TCQ_X_BF16> : fused_finish_kernel<TCQ_X_F16>, grid,
+                      dim3(256), 0, stream, true, p, e, w.rows, static_cast<const float*>(partial), vec);
+}
+
+}  // namespace tcq

@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(kRowThreads) scale_rows_kernel(const uint16_t*
                                                                  float* row_pow2, bool vec)
 {
     __shared__ uint32_t part[kRowThreads / 32];
+    pdl_release();
     const long long r = blockIdx.x;
     const uint16_t* xr = x + r * ldx;
     uint16_t* o = out + r * ldo;
@@ -474,13 +475,14 @@ cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& 
 }
 
 cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long long n, long long cols,
-                              const float* col_pow2, void* out, long long ldo, float* row_pow2, cudaStream_t stream)
+                              const float* col_pow2, void* out, long long ldo, float* row_pow2, bool early,
+                              cudaStream_t stream)
 {
     const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
     const uint16_t* xi = static_cast<const uint16_t*>(x);
     uint16_t* o = static_cast<uint16_t*>(out);
     return launch_pdl(xdtype == TCQ_X_BF16 ? scale_rows_kernel<TCQ_X_BF16> : scale_rows_kernel<TCQ_X_F16>,
-                      dim3((unsigned)n), dim3(kRowThreads), 0, stream, true, xi, ldx, cols, col_pow2, o, ldo, row_pow2,
+                      dim3((unsigned)n), dim3(kRowThreads), 0, stream, early, xi, ldx, cols, col_pow2, o, ldo, row_pow2,
                       vec);
 }
 

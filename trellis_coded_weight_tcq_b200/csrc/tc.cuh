@@ -75,7 +75,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
-// The same without the stop flag: what was issued before a stop is still waited for.
+// Waits for a shared-memory counter that only grows.
+__device__ __forceinline__ bool wait_count(const volatile int* count, int least, volatile int* stop, unsigned int* err)
+{
+    for (long long i = 0; i < kWaitLimit; ++i) {
+        if (*count >= least) return true;
+        if ((i & 255) == 255 && *stop) return false;
+    }
+    *stop = 1;
+    if (err) atomicOr(err, kDevErrWaitTimeout);
+    return false;
+}
+
+// The same as mbar_wait without the stop flag: what was issued before a stop is still waited for.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
 {
     for (long long i = 0; i < kWaitLimit; ++i)
@@ -212,6 +224,23 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
                  ::"memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 ::"memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // ---- host
