@@ -77,6 +77,12 @@ SHAPES = [  # L, k, T, rows, blocks per row, code, scaled, n, dtype
     (3, 3, 8, 33, 1, "f16", False, 40, "bf16"),         # an eight-entry table, eight columns
     (16, 2, 256, 2048, 16, "f16", True, 512, "bf16"),   # several tiles in every direction
     (12, 3, 64, 4099, 3, "f16", True, 2, "f16"),
+    (16, 2, 256, 3000, 6, "f16", True, 100, "f16"),     # runs of stages that cut tiles, a ring of three
+    (16, 2, 128, 1500, 24, "mad", True, 1000, "bf16"),  # four token tiles, the last one short
+    (14, 1, 64, 2500, 9, "f32", True, 200, "f16"),
+    (16, 4, 256, 20000, 1, "f16", False, 20, "bf16"),   # more row tiles than SMs, few stages each
+    (8, 3, 64, 130, 1, "mad", True, 256, "f16"),        # one stage per tile
+    (16, 2, 256, 520, 8, "f16", True, 1025, "bf16"),    # the first count that decodes ahead
 ]
 
 
