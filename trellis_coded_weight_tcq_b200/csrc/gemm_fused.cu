@@ -7,16 +7,19 @@
 // weights take the M side of the MMA: a CTA multiplies 128 rows of W by up to 256
 // tokens, D[row, token] in tensor memory (cta_group::1, 128 x N x 16).
 //
-// 16 warps decode, in four groups: a lane owns one row and turns the stream words of
-// 64 columns (one stage) into eight 16-byte pieces of the swizzled K-major tile, held
-// in registers until the stage is free.  Group g takes stages g, g + 4, ..., so four
-// stages are decoded at a time while the words of the next four are on their way.
-// Warp 16 loads the activations' tiles by TMA, one thread of warp 17 issues the MMAs.
+// 16 warps decode, in two groups that take turns at units of 128 columns (two stages
+// of the ring): a warp covers 16 rows, lanes 0-15 the first stage's 64 columns of
+// them, lanes 16-31 the second's.  A lane turns its 2 k stream words (16 bytes for k =
+// 2; the warp reads whole 32-byte sectors, half the cache lines that a row per lane
+// would touch, and the second half's preceding word comes from the first by shuffle)
+// into eight 16-byte pieces of the swizzled K-major tile, held in registers until the
+// stage is free.  Warp 16 loads the activations' tiles by TMA, one thread of warp 17
+// issues the MMAs.
 //
-// Work is split over the SMs evenly, in stages: a CTA takes a contiguous run of
-// (tile, stage) pairs, so a tile's reduction may be cut into pieces; each writes its
-// fp32 sums to the workspace, and a second kernel adds a tile's pieces in order and
-// applies the epilogue.  The split depends on the shape and the SM count only.
+// Work is split over the SMs evenly, in units: a CTA takes a contiguous run of (tile,
+// unit) pairs, so a tile's reduction may be cut into pieces; each writes its fp32 sums
+// to the workspace, and a second kernel adds a tile's pieces in order and applies the
+// epilogue.  The split depends on the shape and the SM count only.
 #include "decode16.cuh"
 #include "gemm.cuh"
 #include "pdl.cuh"
@@ -39,18 +42,18 @@ struct Barriers {
     unsigned long long afull[kMaxStages], bfull[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int stop;
-    int fills[kMaxStages];  // warps that have filled a stage, ever
+    int fills[kMaxStages];  // warps that have filled a stage, counted from the start
 };
 
 struct Plan {
     long long n;          // tokens
     int np;               // tokens per tile, a multiple of 16
     int row_tiles, token_tiles;
-    int steps;            // stages of a whole reduction
+    int steps;            // units of 128 columns of a whole reduction
     long long units;      // tiles * steps
     int ctas;
     int pieces;           // slots per tile in the workspace
-    int stages;           // ring depth
+    int stages;           // ring depth, even
     int tmem_columns;
     int table;            // shared-memory bytes of the table, a multiple of 1024
 };
@@ -95,7 +98,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
-            mbar_init(smem_addr(&B.afull[i]), 4);
+            mbar_init(smem_addr(&B.afull[i]), kDecodeWarps / 2);
             mbar_init(smem_addr(&B.bfull[i]), 1);
             mbar_init(smem_addr(&B.empty[i]), 1);
             B.fills[i] = 0;
@@ -122,56 +125,87 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
     const int acc_columns = p.tmem_columns / 2;
 
     if (warp < kDecodeWarps) {
-        const int group = warp >> 2;
-        const int r = (warp & 3) * 32 + lane;  // row of the tile
+        const int group = warp >> 3, half = lane >> 4;
+        const int r = (warp & 7) * 16 + (lane & 15);  // row of the tile
         const uint32_t mask = (1u << w.L) - 1u;
-        const int nb = (int)(w.cols / w.T), spb = w.T / kDepth;  // stages per block
-        const long long row_words = (long long)p.steps * 2 * K;
+        const int T = w.T, cols = (int)w.cols, nb = cols / T;
+        const int tshift = (T & (T - 1)) == 0 ? __ffs(T) - 1 : -1;
         const bool wide = (reinterpret_cast<uintptr_t>(w.bits) & 15) == 0;
-        // the words, the word before them and the scale of this lane's part of unit u
-        auto fetch = [&](long long u, uint32_t (&words)[2 * K], uint32_t& prev, float& sc) {
-            const long long tile = u / p.steps;
-            const int ks = (int)(u - tile * p.steps);
-            const long long row = (tile % p.row_tiles) * kRows + r;
+        const int row_words = cols / 32 * K;
+        // where the group's next unit is: its tile, its place in the reduction, its row
+        long long tile = u0 / p.steps;
+        int ks = (int)(u0 - tile * p.steps);
+        const uint32_t* bits = nullptr;  // this lane's row, or none
+        long long row = 0;
+        float inv = 1.f;
+        auto enter_tile = [&]() {
+            row = (tile % p.row_tiles) * kRows + r;
+            bits = row < w.rows ? w.bits + row * row_words : nullptr;
+            if (bits && w.scale) inv = inverse_pow2(__ldg(row_pow2 + row));
+        };
+        auto advance = [&](int by) {
+            for (ks += by; ks >= p.steps; ks -= p.steps) {
+                ++tile;
+                if (ks - p.steps < p.steps) enter_tile();
+            }
+        };
+        enter_tile();
+        advance(group);
+        // the words of this lane's 64 columns, the word before them, their scale
+        auto fetch = [&](uint32_t (&words)[2 * K], uint32_t& prev, float& sc) {
+            const int c = ks * 128 + half * kDepth;
             sc = 0.f;
             prev = 0u;
 #pragma unroll
             for (int i = 0; i < 2 * K; ++i) words[i] = 0u;
-            if (row < w.rows) {
-                const uint32_t* q = w.bits + row * row_words + ks * 2 * K;
-                const int j = ks / spb;
+            if (bits && c < cols) {
+                const uint32_t* q = bits + c / 32 * K;
+                const int j = tshift >= 0 ? c >> tshift : c / T;
+                const bool first = c == j * T;
                 load_words<K>(q, words, wide);
-                prev = __ldg(ks == j * spb ? w.start_state + row * nb + j : q - 1);
-                sc = w.scale ? __ldg(w.scale + row * nb + j) * inverse_pow2(__ldg(row_pow2 + row)) : 1.f;
+                if (first || !half) prev = __ldg(first ? w.start_state + row * nb + j : q - 1);
+                sc = w.scale ? __ldg(w.scale + row * nb + j) * inv : 1.f;
+                if (half && !first) prev = 0u;
             }
+            return c;
         };
         uint32_t words[2 * K], prev;
         float sc;
+        int c0 = 0;
         long long u = u0 + group;
-        if (u < u1) fetch(u, words, prev, sc);
+        if (u < u1) c0 = fetch(words, prev, sc);
         bool ok = true;
         int done = 0;
-        for (long long s0 = u0; s0 < u1 && ok; ++done) {  // segments: runs of one tile's stages
-            const long long tile = s0 / p.steps;
-            const long long s1 = (tile + 1) * p.steps < u1 ? (tile + 1) * p.steps : u1;
-            for (; u < s1; u += 4) {
-                const int it = (int)(u - u0), slot = it % p.stages;
+        for (long long s0 = u0; s0 < u1 && ok; ++done) {  // segments: runs of one tile's units
+            const long long seg_tile = s0 / p.steps;
+            const long long s1 = (seg_tile + 1) * p.steps < u1 ? (seg_tile + 1) * p.steps : u1;
+            for (; u < s1; u += 2) {
+                const int it = 2 * (int)(u - u0);  // the unit's first stage
                 uint32_t nwords[2 * K], nprev;
                 float nsc;
-                if (u + 4 < u1) fetch(u + 4, nwords, nprev, nsc);
+                int nc0 = 0;
+                if (u + 2 < u1) {
+                    advance(2);
+                    nc0 = fetch(nwords, nprev, nsc);
+                }
+                // the second half's word before it is the first half's last, inside a block
+                const uint32_t other = __shfl_up_sync(0xffffffffu, words[2 * K - 1], 16);
+                const int j0 = tshift >= 0 ? c0 >> tshift : c0 / T;
+                const uint32_t before = half && c0 != j0 * T ? other : prev;
                 uint32_t v[32];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    constexpr int bits = 8 * K;
-                    const int e = (bits * (q + 1) - 1) >> 5;
-                    decode_weights<K, 8, CODE>(e > 0 ? words[e > 0 ? e - 1 : 0] : prev, words[e],
-                                               bits_behind(bits * (q + 1)), mask, sm, sc, v + 4 * q);
+                    constexpr int bits8 = 8 * K;
+                    const int e = (bits8 * (q + 1) - 1) >> 5;
+                    decode_weights<K, 8, CODE>(e > 0 ? words[e > 0 ? e - 1 : 0] : before, words[e],
+                                               bits_behind(bits8 * (q + 1)), mask, sm, sc, v + 4 * q);
                 }
                 // A barrier's parity tells two neighbouring phases apart.  With four or more
-                // stages the wait four units ago puts this one's phase next; with fewer,
-                // the group must first see the slot's fill before its own.
+                // stages the wait one turn ago puts this one's phase next; with two, the
+                // group must first see the other group's fill.
+                const int slot = (it + half) % p.stages;
                 const int round = it / p.stages;
-                if (p.stages < 4) ok = wait_count(&B.fills[slot], 4 * round, stop, err);
+                if (p.stages < 4) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
                 ok = ok && mbar_wait(smem_addr(&B.empty[slot]), (round & 1) ^ 1, stop, err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -182,7 +216,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                         make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) {
+                if ((lane & 15) == 0) {
                     mbar_arrive(smem_addr(&B.afull[slot]));
                     if (p.stages < 4) atomicAdd(&B.fills[slot], 1);
                 }
@@ -190,18 +224,19 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                 for (int i = 0; i < 2 * K; ++i) words[i] = nwords[i];
                 prev = nprev;
                 sc = nsc;
+                c0 = nc0;
             }
             if (!ok) break;
-            // the segment's sums: lane = row, 16 tokens at a time shared among the groups
+            // the segment's sums: lane = row, 16 tokens at a time shared among the warps
             const int acc = done & 1;
             ok = mbar_wait(smem_addr(&B.tfull[acc]), (done >> 1) & 1, stop, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const int piece = (int)blockIdx.x - cta_of(p, tile * p.steps);
-            float* out = partial + ((tile * p.pieces + piece) * p.np) * kRows + r;
+            const int piece = (int)blockIdx.x - cta_of(p, seg_tile * p.steps);
+            float* out = partial + ((seg_tile * p.pieces + piece) * p.np) * kRows + (warp & 3) * 32 + lane;
             const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * acc_columns;
-            for (int c = 16 * group; c < p.np; c += 64) {
+            for (int c = 16 * (warp >> 2); c < p.np; c += 64) {
                 float d[16];
                 tmem_load16(lanes + c, d);
 #pragma unroll
@@ -216,12 +251,12 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
         if (lane == 0) {
             bool ok = true;
             int it = 0;
-            for (long long u = u0; u < u1; ++u, ++it) {
+            for (; it < 2 * (int)(u1 - u0); ++it) {
                 const int slot = it % p.stages;
                 ok = mbar_wait(smem_addr(&B.empty[slot]), ((it / p.stages) & 1) ^ 1, stop, err);
                 if (!ok) break;
-                const long long tile = u / p.steps;
-                const int ks = (int)(u - tile * p.steps);
+                const long long tile = (u0 + it / 2) / p.steps;
+                const int ks = 2 * (int)(u0 + it / 2 - tile * p.steps) + (it & 1);
                 mbar_expect_tx(smem_addr(&B.bfull[slot]), bbytes);
                 tma_load_2d(smem_addr(ring + (size_t)slot * sbytes + kABytes), &map_x, smem_addr(&B.bfull[slot]),
                             ks * kDepth, (int)(tile / p.row_tiles) * p.np);
@@ -243,8 +278,9 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                 ok = mbar_wait(smem_addr(&B.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
                 if (!ok) break;
                 tc_fence_after();
-                for (long long u = s0; u < s1; ++u) {
-                    const int it = (int)(u - u0), slot = it % p.stages;
+                const int first = 2 * (int)(s0 - u0);
+                for (int it = first; it < 2 * (int)(s1 - u0); ++it) {
+                    const int slot = it % p.stages;
                     ok = mbar_wait(smem_addr(&B.bfull[slot]), (it / p.stages) & 1, stop, err) &&
                          mbar_wait(smem_addr(&B.afull[slot]), (it / p.stages) & 1, stop, err);
                     if (!ok) break;
@@ -253,7 +289,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
 #pragma unroll
                     for (int j = 0; j < kDepth / 16; ++j)
                         mma_f16<1>(tmem + acc * acc_columns, smem_desc_sw128(a + 32 * j, 16),
-                                   smem_desc_sw128(b + 32 * j, 16), idesc, u != s0 || j != 0);
+                                   smem_desc_sw128(b + 32 * j, 16), idesc, it != first || j != 0);
                     mma_commit<1>(smem_addr(&B.empty[slot]));
                 }
                 if (ok) mma_commit<1>(smem_addr(&B.tfull[acc]));
@@ -346,10 +382,10 @@ Plan make_plan(int code, int L, long long rows, long long cols, long long n, int
     p.token_tiles = (int)tt;
     p.np = (int)(((n + tt - 1) / tt + 15) / 16 * 16);
     p.row_tiles = (int)((rows + kRows - 1) / kRows);
-    p.steps = (int)(cols / kDepth);
+    p.steps = (int)((cols + 127) / 128);
     p.units = (long long)p.row_tiles * p.token_tiles * p.steps;
-    // at least four stages per CTA, one for each group of decoding warps
-    long long ctas = (p.units + 3) / 4;
+    // at least two units per CTA, one for each group of decoding warps
+    long long ctas = (p.units + 1) / 2;
     if (ctas > num_sms) ctas = num_sms;
     p.ctas = (int)ctas;
     const long long least = p.units / p.ctas;  // a tile meets at most this many CTAs
@@ -357,7 +393,7 @@ Plan make_plan(int code, int L, long long rows, long long cols, long long n, int
     if (p.pieces > p.ctas) p.pieces = p.ctas;
     p.table = (int)((table_bytes(code, L) + 1023) & ~(size_t)1023);
     p.stages = (kSmemBytes - p.table - (int)sizeof(Barriers)) / (kABytes + p.np * kDepth * 2);
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.stages = p.stages > kMaxStages ? kMaxStages : p.stages / 2 * 2;
     p.tmem_columns = 32;
     while (p.tmem_columns < 2 * p.np) p.tmem_columns *= 2;
     return p;
@@ -392,7 +428,7 @@ cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const Plan& p
 // T a multiple of 64 keeps a stage inside one block and its words together.
 bool fused_shape(int T, long long rows, long long cols, long long n)
 {
-    return T % kDepth == 0 && n <= kFusedMaxTokens && rows / kRows * ((n + 255) / 256) * (cols / kDepth) < (1ll << 30);
+    return T % kDepth == 0 && n <= kFusedMaxTokens && (rows / kRows + 1) * ((n + 255) / 256) * (cols / 128 + 1) < (1ll << 30);
 }
 
 size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms)
