@@ -36,6 +36,9 @@ __device__ __forceinline__ void stage_table(unsigned char* sm, const void* cb, i
     }
 }
 
+// Stream bits of a word behind the window that ends at stream bit `end`.
+__device__ __forceinline__ int bits_behind(int end) { return (32 - (end & 31)) & 31; }
+
 // Bytes of a table entry.
 __host__ __device__ constexpr int entry_bytes(int code) { return code == kCode16F32 ? 4 : code == kCode16F16 ? 2 : 1; }
 
@@ -80,8 +83,35 @@ __device__ __forceinline__ void decode_weights(uint32_t hi, uint32_t lo, int dow
     }
 }
 
-// Stream bits of a word behind the window that ends at stream bit `end`.
-__device__ __forceinline__ int bits_behind(int end) { return (32 - (end & 31)) & 31; }
+// 64 weights from their 2 K stream words and the word before them, the look-ups of 16
+// weights in flight while the 16 before are converted.
+template <int K, int CODE>
+__device__ __forceinline__ void decode_64(const uint32_t (&words)[2 * K], uint32_t before, uint32_t mask,
+                                          const unsigned char* tab, float scale, uint32_t (&out)[32])
+{
+    float c[2][16];
+    auto look_up = [&](int step, float (&f)[16]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int q = 2 * step + h;
+            const int e = (8 * K * (q + 1) - 1) >> 5, down = bits_behind(8 * K * (q + 1));
+            const uint32_t lo = words[e], hi = e > 0 ? words[e > 0 ? e - 1 : 0] : before;
+            const uint32_t a = __funnelshift_r(lo, hi, down), b = hi >> down;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[8 * h + i] = codeword_at<CODE>(tab, window_offset<K, 8, CODE>(b, a, i, mask));
+        }
+    };
+    look_up(0, c[0]);
+#pragma unroll
+    for (int step = 0; step < 4; ++step) {
+        if (step < 3) look_up(step + 1, c[(step + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const __half2 h = __floats2half2_rn(c[step & 1][i] * scale, c[step & 1][i + 1] * scale);
+            out[8 * step + i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+}
 
 // Bits of |v|, or 0 for an infinity or NaN (magnitudes then compare as integers).
 __device__ __forceinline__ uint32_t finite_magnitude(float v)

@@ -35,14 +35,14 @@ constexpr int kThreads = (kDecodeWarps + 2) * 32;
 constexpr int kRows = 128;             // rows of W per tile
 constexpr int kDepth = 64;             // columns per stage
 constexpr int kABytes = kRows * kDepth * 2;
-constexpr int kMaxStages = 8;
+constexpr int kMaxSlots = 8;
 constexpr int kSmemBytes = 227 * 1024;
 
 struct Barriers {
-    unsigned long long afull[kMaxStages], bfull[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+    unsigned long long full[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int stop;
-    int fills[kMaxStages];  // warps that have filled a stage, counted from the start
+    int fills[kMaxSlots];  // warps that have filled a slot, counted from the start
 };
 
 struct Plan {
@@ -53,7 +53,8 @@ struct Plan {
     long long units;      // tiles * steps
     int ctas;
     int pieces;           // slots per tile in the workspace
-    int stages;           // ring depth, even
+    int slots;            // ring depth
+    int per;              // stages per slot: 2 (a unit), or 1 where only two stages fit
     int tmem_columns;
     int table;            // shared-memory bytes of the table, a multiple of 1024
 };
@@ -93,13 +94,12 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char* ring = sm + p.table;
     const int bbytes = p.np * kDepth * 2;
-    const int sbytes = kABytes + bbytes;
-    Barriers& B = *reinterpret_cast<Barriers*>(ring + (size_t)p.stages * sbytes);
+    const int sbytes = p.per * (kABytes + bbytes);  // a slot: its A stages, then its B stages
+    Barriers& B = *reinterpret_cast<Barriers*>(ring + (size_t)p.slots * sbytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < p.stages; ++i) {
-            mbar_init(smem_addr(&B.afull[i]), kDecodeWarps / 2);
-            mbar_init(smem_addr(&B.bfull[i]), 1);
+        for (int i = 0; i < p.slots; ++i) {
+            mbar_init(smem_addr(&B.full[i]), kDecodeWarps / 2 + 1);  // a group's warps, and the TMA thread
             mbar_init(smem_addr(&B.empty[i]), 1);
             B.fills[i] = 0;
         }
@@ -137,11 +137,11 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
         int ks = (int)(u0 - tile * p.steps);
         const uint32_t* bits = nullptr;  // this lane's row, or none
         long long row = 0;
-        float inv = 1.f;
+        float inv = 1.f;  // the row's power
         auto enter_tile = [&]() {
             row = (tile % p.row_tiles) * kRows + r;
             bits = row < w.rows ? w.bits + row * row_words : nullptr;
-            if (bits && w.scale) inv = inverse_pow2(__ldg(row_pow2 + row));
+            if (bits && w.scale) inv = __ldg(row_pow2 + row);
         };
         auto advance = [&](int by) {
             for (ks += by; ks >= p.steps; ks -= p.steps) {
@@ -151,11 +151,14 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
         };
         enter_tile();
         advance(group);
-        // the words of this lane's 64 columns, the word before them, their scale
-        auto fetch = [&](uint32_t (&words)[2 * K], uint32_t& prev, float& sc) {
+        // The words of this lane's 64 columns, the word before them, their scale, the row's
+        // inverse power.  Nothing here depends on what was loaded, so that the loads stay
+        // in flight over the decoding of the unit before.
+        auto fetch = [&](uint32_t (&words)[2 * K], uint32_t& prev, float& sc, float& in) {
             const int c = ks * 128 + half * kDepth;
             sc = 0.f;
             prev = 0u;
+            in = inv;
 #pragma unroll
             for (int i = 0; i < 2 * K; ++i) words[i] = 0u;
             if (bits && c < cols) {
@@ -164,16 +167,15 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                 const bool first = c == j * T;
                 load_words<K>(q, words, wide);
                 if (first || !half) prev = __ldg(first ? w.start_state + row * nb + j : q - 1);
-                sc = w.scale ? __ldg(w.scale + row * nb + j) * inv : 1.f;
-                if (half && !first) prev = 0u;
+                sc = w.scale ? __ldg(w.scale + row * nb + j) : 1.f;
             }
             return c;
         };
         uint32_t words[2 * K], prev;
-        float sc;
+        float sc, pw;
         int c0 = 0;
         long long u = u0 + group;
-        if (u < u1) c0 = fetch(words, prev, sc);
+        if (u < u1) c0 = fetch(words, prev, sc, pw);
         bool ok = true;
         int done = 0;
         for (long long s0 = u0; s0 < u1 && ok; ++done) {  // segments: runs of one tile's units
@@ -182,48 +184,43 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
             for (; u < s1; u += 2) {
                 const int it = 2 * (int)(u - u0);  // the unit's first stage
                 uint32_t nwords[2 * K], nprev;
-                float nsc;
+                float nsc, npw;
                 int nc0 = 0;
                 if (u + 2 < u1) {
                     advance(2);
-                    nc0 = fetch(nwords, nprev, nsc);
+                    nc0 = fetch(nwords, nprev, nsc, npw);
                 }
                 // the second half's word before it is the first half's last, inside a block
                 const uint32_t other = __shfl_up_sync(0xffffffffu, words[2 * K - 1], 16);
                 const int j0 = tshift >= 0 ? c0 >> tshift : c0 / T;
                 const uint32_t before = half && c0 != j0 * T ? other : prev;
                 uint32_t v[32];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    constexpr int bits8 = 8 * K;
-                    const int e = (bits8 * (q + 1) - 1) >> 5;
-                    decode_weights<K, 8, CODE>(e > 0 ? words[e > 0 ? e - 1 : 0] : before, words[e],
-                                               bits_behind(bits8 * (q + 1)), mask, sm, sc, v + 4 * q);
-                }
+                decode_64<K, CODE>(words, before, mask, sm, sc * inverse_pow2(pw), v);
                 // A barrier's parity tells two neighbouring phases apart.  With four or more
                 // stages the wait one turn ago puts this one's phase next; with two, the
                 // group must first see the other group's fill.
-                const int slot = (it + half) % p.stages;
-                const int round = it / p.stages;
-                if (p.stages < 4) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
+                const int step = (it + half) / p.per, sub = (it + half) % p.per;
+                const int slot = step % p.slots, round = step / p.slots;
+                if (p.per == 1) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
                 ok = ok && mbar_wait(smem_addr(&B.empty[slot]), (round & 1) ^ 1, stop, err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                unsigned char* a = ring + (size_t)slot * sbytes + r * 128;
+                unsigned char* a = ring + (size_t)slot * sbytes + sub * kABytes + r * 128;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     *reinterpret_cast<uint4*>(a + ((q ^ (r & 7)) << 4)) =
                         make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if ((lane & 15) == 0) {
-                    mbar_arrive(smem_addr(&B.afull[slot]));
-                    if (p.stages < 4) atomicAdd(&B.fills[slot], 1);
+                if (lane == 0 || (p.per == 1 && lane == 16)) {
+                    mbar_arrive(smem_addr(&B.full[slot]));
+                    if (p.per == 1) atomicAdd(&B.fills[slot], 1);
                 }
 #pragma unroll
                 for (int i = 0; i < 2 * K; ++i) words[i] = nwords[i];
                 prev = nprev;
                 sc = nsc;
+                pw = npw;
                 c0 = nc0;
             }
             if (!ok) break;
@@ -250,20 +247,28 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
     } else if (warp == kDecodeWarps) {
         if (lane == 0) {
             bool ok = true;
-            int it = 0;
-            for (; it < 2 * (int)(u1 - u0); ++it) {
-                const int slot = it % p.stages;
-                ok = mbar_wait(smem_addr(&B.empty[slot]), ((it / p.stages) & 1) ^ 1, stop, err);
+            int i = 0;
+            const int fills = 2 / p.per * (int)(u1 - u0);
+            long long tile = u0 / p.steps;
+            int ks = 2 * (int)(u0 - tile * p.steps);  // in stages
+            for (; i < fills; ++i) {
+                const int slot = i % p.slots;
+                const uint32_t full = smem_addr(&B.full[slot]);
+                ok = mbar_wait(smem_addr(&B.empty[slot]), ((i / p.slots) & 1) ^ 1, stop, err);
                 if (!ok) break;
-                const long long tile = (u0 + it / 2) / p.steps;
-                const int ks = 2 * (int)(u0 + it / 2 - tile * p.steps) + (it & 1);
-                mbar_expect_tx(smem_addr(&B.bfull[slot]), bbytes);
-                tma_load_2d(smem_addr(ring + (size_t)slot * sbytes + kABytes), &map_x, smem_addr(&B.bfull[slot]),
-                            ks * kDepth, (int)(tile / p.row_tiles) * p.np);
+                mbar_expect_tx(full, p.per * bbytes);
+                for (int h = 0; h < p.per; ++h)
+                    tma_load_2d(smem_addr(ring + (size_t)slot * sbytes + p.per * kABytes + h * bbytes), &map_x, full,
+                                (ks + h) * kDepth, (int)(tile / p.row_tiles) * p.np);
+                ks += p.per;
+                if (ks == 2 * p.steps) {
+                    ks = 0;
+                    ++tile;
+                }
             }
-            if (!ok)  // what was loaded last is still waited for
-                for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
-                    mbar_drain(smem_addr(&B.bfull[i % p.stages]), (i / p.stages) & 1);
+            if (!ok)  // what was loaded last is still waited for (unless its decoders stopped)
+                for (int j = i > p.slots ? i - p.slots : 0; j < i; ++j)
+                    mbar_drain(smem_addr(&B.full[j % p.slots]), (j / p.slots) & 1);
         }
         __syncwarp();
     } else {
@@ -278,18 +283,19 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                 ok = mbar_wait(smem_addr(&B.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
                 if (!ok) break;
                 tc_fence_after();
-                const int first = 2 * (int)(s0 - u0);
-                for (int it = first; it < 2 * (int)(s1 - u0); ++it) {
-                    const int slot = it % p.stages;
-                    ok = mbar_wait(smem_addr(&B.bfull[slot]), (it / p.stages) & 1, stop, err) &&
-                         mbar_wait(smem_addr(&B.afull[slot]), (it / p.stages) & 1, stop, err);
+                const int first = 2 / p.per * (int)(s0 - u0), last = 2 / p.per * (int)(s1 - u0);
+                for (int i = first; i < last; ++i) {
+                    const int slot = i % p.slots;
+                    ok = mbar_wait(smem_addr(&B.full[slot]), (i / p.slots) & 1, stop, err);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = smem_addr(ring + (size_t)slot * sbytes), b = a + kABytes;
+                    uint32_t a = smem_addr(ring + (size_t)slot * sbytes), b = a + p.per * kABytes;
+                    for (int h = 0; h < p.per; ++h, a += kABytes, b += bbytes) {
 #pragma unroll
-                    for (int j = 0; j < kDepth / 16; ++j)
-                        mma_f16<1>(tmem + acc * acc_columns, smem_desc_sw128(a + 32 * j, 16),
-                                   smem_desc_sw128(b + 32 * j, 16), idesc, it != first || j != 0);
+                        for (int j = 0; j < kDepth / 16; ++j)
+                            mma_f16<1>(tmem + acc * acc_columns, smem_desc_sw128(a + 32 * j, 16),
+                                       smem_desc_sw128(b + 32 * j, 16), idesc, i != first || h != 0 || j != 0);
+                    }
                     mma_commit<1>(smem_addr(&B.empty[slot]));
                 }
                 if (ok) mma_commit<1>(smem_addr(&B.tfull[acc]));
@@ -392,8 +398,13 @@ Plan make_plan(int code, int L, long long rows, long long cols, long long n, int
     p.pieces = (int)((p.steps + least - 1) / least + 1);
     if (p.pieces > p.ctas) p.pieces = p.ctas;
     p.table = (int)((table_bytes(code, L) + 1023) & ~(size_t)1023);
-    p.stages = (kSmemBytes - p.table - (int)sizeof(Barriers)) / (kABytes + p.np * kDepth * 2);
-    p.stages = p.stages > kMaxStages ? kMaxStages : p.stages / 2 * 2;
+    // slots of a whole unit, one barrier and one commit for 128 columns, where two of them
+    // fit beside the table (the barriers of a slot share the pipe that the look-ups fill,
+    // about 300 cycles each); slots of a stage otherwise
+    const int room = kSmemBytes - p.table - (int)sizeof(Barriers), stage = kABytes + p.np * kDepth * 2;
+    p.per = room >= 4 * stage ? 2 : 1;
+    p.slots = p.per == 2 ? room / (2 * stage) : 2;
+    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
     p.tmem_columns = 32;
     while (p.tmem_columns < 2 * p.np) p.tmem_columns *= 2;
     return p;
@@ -406,7 +417,7 @@ cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const Plan& p, 
     const cudaError_t e = cudaFuncSetAttribute(fused_kernel<K, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemBytes);
     if (e != cudaSuccess) return e;
-    const size_t smem = p.table + (size_t)p.stages * (kABytes + p.np * kDepth * 2) + sizeof(Barriers);
+    const size_t smem = p.table + (size_t)p.slots * p.per * (kABytes + p.np * kDepth * 2) + sizeof(Barriers);
     return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, p, row_pow2,
                       partial, err);
 }
