@@ -10,7 +10,6 @@ computing anything itself.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -591,124 +590,154 @@ class Packed8:
     format: str = "int8"
 
 
+# These calls can be shorter than their checks, so the checks are few and plain: torch
+# sizes compare with tuples, addresses and streams go to ctypes as integers.
 def _x_dtype(t, what: str) -> int:
     """TCQ_X_* of a 2-D 16-bit CUDA tensor with unit-stride rows."""
     torch = _torch()
     if t.dim() != 2 or not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel()):
         raise ValueError(f"{what} must be a 2-D CUDA tensor with unit-stride rows")
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype == torch.bfloat16:
         return TCQ_X_BF16
-    if t.dtype == torch.float16:
+    if dtype == torch.float16:
         return TCQ_X_F16
-    raise TypeError(f"{what} must be float16 or bfloat16, got {t.dtype}")
+    raise TypeError(f"{what} must be float16 or bfloat16, got {dtype}")
 
 
 def _ld(t) -> int:
     """Row stride in elements (that of one row, or of none, does not matter)."""
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] else max(t.shape[1], 1)
-
-
-def _on_device(device):
-    """The tensors' device made current for the call, if it is not."""
-    torch = _torch()
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t is not MAD and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, x on {device}")
+    n, cols = t.shape
+    return t.stride(0) if n > 1 and cols else max(cols, 1)
 
 
 def _choice(table, name, what):
-    if name not in table:
-        raise ValueError(f"{what} must be one of {', '.join(table)}; got {name!r}")
-    return table[name]
+    try:
+        return table[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"{what} must be one of {', '.join(table)}; got {name!r}") from None
 
 
-def _check_out(out, shape, dtype, what):
-    if tuple(out.shape) != shape or out.dtype != dtype or (out.stride(1) != 1 and shape[1] > 1 and out.numel()):
+def _check_out(out, shape, dtype, device, what):
+    if out.shape != shape or out.dtype != dtype or (out.stride(1) != 1 and shape[1] > 1 and out.numel()):
         raise ValueError(f"{what} must be a {dtype} tensor {list(shape)} with unit-stride rows")
     if shape[0] > 1 and out.numel() and out.stride(0) < shape[1]:
         raise ValueError(f"{what}: rows overlap")
+    _check_device(out, device, what)
+
+
+def _check_device(t, device, what):
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
 
 
 def _check_packed(p, n, cols, device, what):
     torch = _torch()
     fmt = _choice(Q8_FORMATS, p.format, f"{what}.format")
-    if (tuple(p.codes.shape) != (n, cols) or p.codes.element_size() != 1 or not p.codes.is_contiguous() or
-            tuple(p.scales.shape) != (n, -(-cols // 32)) or p.scales.dtype != torch.uint8 or
-            not p.scales.is_contiguous()):
-        raise ValueError(f"{what} must hold contiguous 8-bit codes [{n}, {cols}] and uint8 scales "
-                         f"[{n}, {-(-cols // 32)}]")
-    _same_device(device, **{f"{what}.codes": p.codes, f"{what}.scales": p.scales})
+    codes, scales = p.codes, p.scales
+    groups = (cols + 31) // 32
+    if (codes.shape != (n, cols) or codes.element_size() != 1 or not codes.is_contiguous() or
+            scales.shape != (n, groups) or scales.dtype != torch.uint8 or not scales.is_contiguous()):
+        raise ValueError(f"{what} must hold contiguous 8-bit codes [{n}, {cols}] and uint8 scales [{n}, {groups}]")
+    _check_device(codes, device, what)
+    _check_device(scales, device, what)
     return fmt
 
 
 def _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, device, what):
     torch = _torch()
-    nb = rows * (cols // T) if T > 0 else 0
     W = tcq_words_per_block(k, T)
     if W < 0:
         raise TCQError(TCQ_ERR_UNSUPPORTED, "tcq_words_per_block")
-    if bits.numel() < nb * W or start_state.numel() < nb or (scale is not None and scale.numel() < nb):
+    nb = rows * (cols // T)
+    if bits.numel() < nb * W or start_state.numel() < nb:
         raise ValueError(f"{what}: tensors too small for a {rows} x {cols} matrix of T={T} blocks")
     if (bits.element_size() != 4 or start_state.element_size() != 4 or not bits.is_contiguous() or
-            not start_state.is_contiguous() or
-            (scale is not None and (scale.dtype != torch.float32 or not scale.is_contiguous()))):
-        raise ValueError(f"{what}: bits and start_state are contiguous 32-bit words, scale contiguous float32")
-    if codebook is not MAD and (codebook.numel() < (1 << L) or not codebook.is_contiguous()):
-        raise ValueError(f"{what}: codebook must hold 2^L contiguous entries")
-    _same_device(device, bits=bits, start_state=start_state, scale=scale, codebook=codebook)
+            not start_state.is_contiguous()):
+        raise ValueError(f"{what}: bits and start_state are contiguous 32-bit words")
+    _check_device(bits, device, "bits")
+    _check_device(start_state, device, "start_state")
+    if scale is not None:
+        if scale.numel() < nb or scale.dtype != torch.float32 or not scale.is_contiguous():
+            raise ValueError(f"{what}: scale must hold a contiguous float32 value per block")
+        _check_device(scale, device, "scale")
+    if codebook is not MAD:
+        if codebook.numel() < (1 << L) or not codebook.is_contiguous():
+            raise ValueError(f"{what}: codebook must hold 2^L contiguous entries")
+        _check_device(codebook, device, "codebook")
 
 
-def _scratch(workspace, nbytes, device, what):
-    torch = _torch()
+def _scratch(workspace, nbytes, like, what):
     if workspace is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        return like.new_empty(nbytes or 1, dtype=_torch().uint8)
+    if workspace.device != like.device or workspace.dtype != _torch().uint8 or not workspace.is_contiguous():
         raise ValueError(f"{what}: workspace must be a contiguous uint8 tensor on x's device")
     return workspace
 
 
-def _stream_on(device, stream):
+def _addr(t):
+    return None if t is None or t is MAD else t.data_ptr()
+
+
+def _launch(what, device, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current, on the given stream or on
+    that device's current one."""
     torch = _torch()
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    index = device.index
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status != TCQ_OK:
+        raise TCQError(status, what)
+
+
+def _sized(device, fn, *args):
+    """A workspace query, which counts the multiprocessors of the tensors' device."""
+    torch = _torch()
+    if device.index == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(device.index):
+        return fn(*args)
 
 
 def pack8(x, format: str = "int8", out: Packed8 | None = None, stream=None) -> Packed8:
     """8-bit checkpoint of ``x`` (float16 or bfloat16 CUDA [n, cols], unit-stride rows)."""
-    torch = _torch()
+    torch, lib = _torch(), load_library()
     xt = _x_dtype(x, "x")
     n, cols = x.shape
     if out is None:
         fmt = _choice(Q8_FORMATS, format, "format")
-        out = Packed8(torch.empty((n, cols), dtype=torch.int8, device=x.device),
-                      torch.empty((n, -(-cols // 32)), dtype=torch.uint8, device=x.device), format)
+        out = Packed8(x.new_empty((n, cols), dtype=torch.int8),
+                      x.new_empty((n, (cols + 31) // 32), dtype=torch.uint8), format)
     else:
         fmt = _check_packed(out, n, cols, x.device, "out")
-    with _on_device(x.device):
-        _check(tcq_pack8(_ptr(x), xt, _ld(x), n, cols, fmt, _ptr(out.codes), _ptr(out.scales),
-                         _stream_on(x.device, stream)), "tcq_pack8")
+    _launch("tcq_pack8", x.device, stream, lib.tcq_pack8, x.data_ptr(), xt, _ld(x), n, cols, fmt,
+            out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
 
 def unpack8(packed: Packed8, dtype=None, out=None, stream=None):
     """The values of an 8-bit checkpoint, as ``dtype`` (bfloat16 when not given) [n, cols]."""
-    torch = _torch()
-    n, cols = packed.codes.shape
-    dev = packed.codes.device
+    torch, lib = _torch(), load_library()
+    codes = packed.codes
+    if codes.dim() != 2 or not codes.is_cuda:
+        raise ValueError("packed must hold CUDA tensors [n, cols]")
+    n, cols = codes.shape
+    dev = codes.device
     fmt = _check_packed(packed, n, cols, dev, "packed")
     if out is None:
-        out = torch.empty((n, cols), dtype=dtype or torch.bfloat16, device=dev)
+        out = codes.new_empty((n, cols), dtype=dtype or torch.bfloat16)
     else:
-        _check_out(out, (n, cols), dtype or out.dtype, "out")
-        _same_device(dev, out=out)
+        _check_out(out, (n, cols), dtype or out.dtype, dev, "out")
     xt = _x_dtype(out, "out")
-    with _on_device(dev):
-        _check(tcq_unpack8(_ptr(packed.codes), _ptr(packed.scales), fmt, n, cols, _ptr(out), xt, _ld(out),
-                           _stream_on(dev, stream)), "tcq_unpack8")
+    _launch("tcq_unpack8", dev, stream, lib.tcq_unpack8, codes.data_ptr(), packed.scales.data_ptr(), fmt, n, cols,
+            out.data_ptr(), xt, _ld(out))
     return out
 
 
@@ -720,31 +749,35 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
     ``bias`` float32 [rows]; ``residual`` like the result; ``checkpoint`` a Packed8 of
     [n, rows] that receives the pre-activation in 8 bits.  ``workspace`` (uint8, at
     least tcq_gemm_workspace_bytes) and ``out`` are allocated when not given."""
-    torch = _torch()
+    torch, lib = _torch(), load_library()
     xt = _x_dtype(x, "x")
-    dev, n = x.device, x.shape[0]
+    dev, dtype, n = x.device, x.dtype, x.shape[0]
     if x.shape[1] != cols:
         raise ValueError(f"gemm: x has {x.shape[1]} columns, the matrix {cols}")
     a = _choice(ACTIVATIONS, act, "act")
     _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, dev, "gemm")
-    if bias is not None and (bias.numel() != rows or bias.dtype != torch.float32 or not bias.is_contiguous()):
-        raise ValueError("gemm: bias must be a contiguous float32 tensor [rows]")
+    if bias is not None:
+        if bias.numel() != rows or bias.dtype != torch.float32 or not bias.is_contiguous():
+            raise ValueError("gemm: bias must be a contiguous float32 tensor [rows]")
+        _check_device(bias, dev, "bias")
+    ldr = 0
     if residual is not None:
-        _check_out(residual, (n, rows), x.dtype, "residual")
+        _check_out(residual, (n, rows), dtype, dev, "residual")
+        ldr = _ld(residual)
     if out is None:
-        out = torch.empty((n, rows), dtype=x.dtype, device=dev)
+        out = x.new_empty((n, rows))
     else:
-        _check_out(out, (n, rows), x.dtype, "out")
-    _same_device(dev, bias=bias, residual=residual, out=out)
-    zf = TCQ_Q8_INT8 if checkpoint is None else _check_packed(checkpoint, n, rows, dev, "checkpoint")
+        _check_out(out, (n, rows), dtype, dev, "out")
+    zc = zs = None
+    zf = TCQ_Q8_INT8
+    if checkpoint is not None:
+        zf = _check_packed(checkpoint, n, rows, dev, "checkpoint")
+        zc, zs = checkpoint.codes.data_ptr(), checkpoint.scales.data_ptr()
     cb = cb_dtype_of(codebook)
-    with _on_device(dev):
-        ws = _scratch(workspace, tcq_gemm_workspace_bytes(L, k, T, rows, cols, n, cb), dev, "gemm")
-        _check(tcq_gemm(_ptr(bits), _ptr(start_state), _ptr(scale), _ptr(codebook), cb, L, k, T, rows, cols, _ptr(x),
-                        xt, _ld(x), n, _ptr(bias), a, _ptr(residual), 0 if residual is None else _ld(residual),
-                        _ptr(out), _ld(out), None if checkpoint is None else _ptr(checkpoint.codes),
-                        None if checkpoint is None else _ptr(checkpoint.scales), zf, _ptr(ws), ws.numel(),
-                        _stream_on(dev, stream)), "tcq_gemm")
+    ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_workspace_bytes, L, k, T, rows, cols, n, cb), x, "gemm")
+    _launch("tcq_gemm", dev, stream, lib.tcq_gemm, bits.data_ptr(), start_state.data_ptr(), _addr(scale),
+            _addr(codebook), cb, L, k, T, rows, cols, x.data_ptr(), xt, _ld(x), n, _addr(bias), a, _addr(residual),
+            ldr, out.data_ptr(), _ld(out), zc, zs, zf, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -752,23 +785,22 @@ def gemm_dgrad(bits, start_state, scale, codebook, L: int, k: int, T: int, rows:
                workspace=None, stream=None):
     """dz W for a trellis-coded W [rows, cols] and ``dz`` float16 or bfloat16 [n, rows];
     [n, cols] of dz's type."""
-    torch = _torch()
+    lib = load_library()
     xt = _x_dtype(dz, "dz")
     dev, n = dz.device, dz.shape[0]
     if dz.shape[1] != rows:
         raise ValueError(f"gemm_dgrad: dz has {dz.shape[1]} columns, the matrix {rows} rows")
     _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, dev, "gemm_dgrad")
     if out is None:
-        out = torch.empty((n, cols), dtype=dz.dtype, device=dev)
+        out = dz.new_empty((n, cols))
     else:
-        _check_out(out, (n, cols), dz.dtype, "out")
-        _same_device(dev, out=out)
+        _check_out(out, (n, cols), dz.dtype, dev, "out")
     cb = cb_dtype_of(codebook)
-    with _on_device(dev):
-        ws = _scratch(workspace, tcq_gemm_dgrad_workspace_bytes(L, k, T, rows, cols, n, cb), dev, "gemm_dgrad")
-        _check(tcq_gemm_dgrad(_ptr(bits), _ptr(start_state), _ptr(scale), _ptr(codebook), cb, L, k, T, rows, cols,
-                              _ptr(dz), xt, _ld(dz), n, _ptr(out), _ld(out), _ptr(ws), ws.numel(),
-                              _stream_on(dev, stream)), "tcq_gemm_dgrad")
+    ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_dgrad_workspace_bytes, L, k, T, rows, cols, n, cb), dz,
+                  "gemm_dgrad")
+    _launch("tcq_gemm_dgrad", dev, stream, lib.tcq_gemm_dgrad, bits.data_ptr(), start_state.data_ptr(), _addr(scale),
+            _addr(codebook), cb, L, k, T, rows, cols, dz.data_ptr(), xt, _ld(dz), n, out.data_ptr(), _ld(out),
+            ws.data_ptr(), ws.numel())
     return out
 
 
@@ -776,33 +808,36 @@ def act_grad8(dy, checkpoint, act: str, dbias: bool = True, out=None, workspace=
     """(dz, dbias): dy act'(z) in dy's type [n, rows] and its float32 column sums (None
     unless ``dbias``), from the 8-bit checkpoint of the pre-activation (None for act
     "none").  ``out`` may be ``dy``."""
-    torch = _torch()
+    torch, lib = _torch(), load_library()
     xt = _x_dtype(dy, "dy")
     dev = dy.device
     n, rows = dy.shape
     a = _choice(ACTIVATIONS, act, "act")
-    if checkpoint is None and a != TCQ_ACT_NONE:
+    zc = zs = None
+    zf = TCQ_Q8_INT8
+    if checkpoint is not None:
+        zf = _check_packed(checkpoint, n, rows, dev, "checkpoint")
+        zc, zs = checkpoint.codes.data_ptr(), checkpoint.scales.data_ptr()
+    elif a != TCQ_ACT_NONE:
         raise ValueError(f"act_grad8: {act!r} needs the checkpoint of the pre-activation")
-    zf = TCQ_Q8_INT8 if checkpoint is None else _check_packed(checkpoint, n, rows, dev, "checkpoint")
     if out is None:
-        out = torch.empty((n, rows), dtype=dy.dtype, device=dev)
+        out = dy.new_empty((n, rows))
     else:
-        _check_out(out, (n, rows), dy.dtype, "out")
-        _same_device(dev, out=out)
-    db = torch.empty(rows, dtype=torch.float32, device=dev) if dbias else None
-    with _on_device(dev):
-        ws = _scratch(workspace, tcq_act_grad8_workspace_bytes(n, rows), dev, "act_grad8") if dbias else None
-        _check(tcq_act_grad8(_ptr(dy), xt, _ld(dy), None if checkpoint is None else _ptr(checkpoint.codes),
-                             None if checkpoint is None else _ptr(checkpoint.scales), zf, a, n, rows, _ptr(out),
-                             _ld(out), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), _stream_on(dev, stream)),
-               "tcq_act_grad8")
+        _check_out(out, (n, rows), dy.dtype, dev, "out")
+    db, dp, wp, wb = None, None, None, 0
+    if dbias:
+        db = dy.new_empty(rows, dtype=torch.float32)
+        ws = _scratch(workspace, lib.tcq_act_grad8_workspace_bytes(n, rows), dy, "act_grad8")
+        dp, wp, wb = db.data_ptr(), ws.data_ptr(), ws.numel()
+    _launch("tcq_act_grad8", dev, stream, lib.tcq_act_grad8, dy.data_ptr(), xt, _ld(dy), zc, zs, zf, a, n, rows,
+            out.data_ptr(), _ld(out), dp, wp, wb)
     return out, db
 
 
 def wgrad8(dz, packed: Packed8, out=None, accumulate: bool = False, workspace=None, stream=None):
     """dz^T x, float32 [rows, cols], for ``dz`` float16 or bfloat16 [n, rows] and the
     8-bit checkpoint of x [n, cols]; added to ``out`` when ``accumulate``."""
-    torch = _torch()
+    torch, lib = _torch(), load_library()
     xt = _x_dtype(dz, "dz")
     dev = dz.device
     n, rows = dz.shape
@@ -811,15 +846,13 @@ def wgrad8(dz, packed: Packed8, out=None, accumulate: bool = False, workspace=No
     if out is None:
         if accumulate:
             raise ValueError("wgrad8: accumulate needs out")
-        out = torch.empty((rows, cols), dtype=torch.float32, device=dev)
+        out = dz.new_empty((rows, cols), dtype=torch.float32)
     else:
-        _check_out(out, (rows, cols), torch.float32, "out")
-        _same_device(dev, out=out)
-    with _on_device(dev):
-        ws = _scratch(workspace, tcq_wgrad8_workspace_bytes(rows, cols, n), dev, "wgrad8")
-        _check(tcq_wgrad8(_ptr(dz), xt, _ld(dz), _ptr(packed.codes), _ptr(packed.scales), fmt, n, rows, cols,
-                          _ptr(out), _ld(out), int(accumulate), _ptr(ws), ws.numel(), _stream_on(dev, stream)),
-               "tcq_wgrad8")
+        _check_out(out, (rows, cols), torch.float32, dev, "out")
+    ws = _scratch(workspace, lib.tcq_wgrad8_workspace_bytes(rows, cols, n), dz, "wgrad8")
+    _launch("tcq_wgrad8", dev, stream, lib.tcq_wgrad8, dz.data_ptr(), xt, _ld(dz), packed.codes.data_ptr(),
+            packed.scales.data_ptr(), fmt, n, rows, cols, out.data_ptr(), _ld(out), int(accumulate), ws.data_ptr(),
+            ws.numel())
     return out
 
 
