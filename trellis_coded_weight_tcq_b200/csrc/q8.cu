@@ -2,11 +2,12 @@
 // through an activation from a packed pre-activation (format: q8.cuh).
 //
 // All three are bound by memory: 3 + 1/32 bytes per element to pack or unpack, 5 + 1/32
-// for the gradient.  Rows of a multiple of 8 elements with 16-byte aligned 16-bit
-// rows move 8 elements per thread (16- and 8-byte accesses), four neighbouring lanes
-// sharing a group; other shapes take one element per lane, a warp per group, which
-// needs no alignment at all.
+// for the gradient.  Rows of a multiple of 16 elements (8 for the gradient) with
+// 16-byte aligned 16-bit rows move whole 16-byte vectors; other shapes take one element
+// per lane, a warp per group, which needs no alignment at all.  Rows that follow one
+// another without gaps and hold whole groups are one long row.
 #include "gemm.cuh"
+#include "pdl.cuh"
 #include "q8.cuh"
 
 namespace tcq {
@@ -15,30 +16,8 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t max3(uint32_t a, uint32_t b, uint32_t c) { return max(a, max(b, c)); }
-
-// the codes of eight elements
-template <int FMT>
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv)
-{
-    uint32_t c[2] = {0u, 0u};
-    if (inv != 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i / 4] |= q8_encode<FMT>(f[i], inv) << (8 * (i & 3));
-    }
-    return make_uint2(c[0], c[1]);
-}
-
-template <int FMT>
-__device__ __forceinline__ void decode8(uint2 codes, float scale, float (&f)[8])
-{
-    const uint32_t c[2] = {codes.x, codes.y};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = q8_decode<FMT>((c[i / 4] >> (8 * (i & 3))) & 0xffu, scale);
-}
-
 template <int XT>
-__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8])
+__device__ __forceinline__ void load8(const uint16_t* p, float* f)
 {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -51,7 +30,7 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8])
 }
 
 template <int XT>
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8])
+__device__ __forceinline__ void store8(uint16_t* p, const float* f)
 {
     *reinterpret_cast<uint4*>(p) = make_uint4(x_pack2<XT>(f[0], f[1]), x_pack2<XT>(f[2], f[3]),
                                               x_pack2<XT>(f[4], f[5]), x_pack2<XT>(f[6], f[7]));
@@ -65,83 +44,111 @@ __device__ __forceinline__ float in_range(float v)
     return v;
 }
 
-// ---- pack
+// Rows of a grid: CTAs take rows blockIdx.x, + gridDim.x, ... and pieces of a row
+// blockIdx.y, + gridDim.y, ...
+
+// ---- pack: 16 elements per thread, two neighbouring lanes per group
 template <int XT, int FMT>
-__global__ void __launch_bounds__(kThreads) pack8_vec_kernel(const uint16_t* x, long long ldx, long long n, int cols,
-                                                             int groups, uint8_t* codes, uint8_t* scales)
+__global__ void __launch_bounds__(kThreads) pack8_vec_kernel(const uint16_t* x, long long ldx, long long n,
+                                                             long long cols, uint8_t* codes, uint8_t* scales)
 {
-    // four lanes per group; the last group's lanes behind the row's end hold nothing
-    const int per_row = 4 * groups;
-    const long long total = n * per_row;
-    const long long stride = (long long)gridDim.x * kThreads;
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i - threadIdx.x % 32 < total; i += stride) {
-        const long long r = i / per_row;
-        const int c = (int)(i - r * per_row) * 8;
-        const bool in = i < total && c < cols;
-        float f[8] = {};
-        uint32_t top = 0u;
-        if (in) {
-            load8<XT>(x + r * ldx + c, f);
+    const long long groups = (cols + 31) / 32;
+    for (long long r = blockIdx.x; r < n; r += gridDim.x) {
+        const uint16_t* xr = x + r * ldx;
+        uint8_t* cr = codes + r * cols;
+        uint8_t* sr = scales + r * groups;
+        // the last group's second lane may hold nothing
+        for (long long i = (long long)blockIdx.y * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < 2 * groups;
+             i += (long long)gridDim.y * blockDim.x) {
+            const long long c = 16 * i;
+            const bool in = c < cols;
+            uint32_t w[8] = {};
+            if (in) {
+                const uint4 a = *reinterpret_cast<const uint4*>(xr + c), b = *reinterpret_cast<const uint4*>(xr + c + 8);
+                w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+                w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+            }
+            // magnitudes order as integers in either 16-bit type, infinities and NaN on top
+            uint32_t top = 0u;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (in) {
-            const uint32_t byte = q8_scale_byte<FMT>(top);
-            *reinterpret_cast<uint2*>(codes + r * cols + c) = encode8<FMT>(f, q8_inv(byte));
-            if ((c & 31) == 0) scales[r * groups + c / 32] = (uint8_t)byte;
+            for (int j = 0; j < 8; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            const float2 tops = x_unpack2<XT>(top);
+            const uint32_t byte = q8_scale_byte<FMT>(max(__float_as_uint(tops.x), __float_as_uint(tops.y)));
+            const float inv = q8_inv(byte);
+            uint32_t code[4] = {};
+            if (byte != 255u) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 p = x_unpack2<XT>(w[2 * j]), q = x_unpack2<XT>(w[2 * j + 1]);
+                    const float f[4] = {p.x, p.y, q.x, q.y};
+                    code[j] = q8_encode4<FMT>(f, inv);
+                }
+            }
+            if (in) {
+                *reinterpret_cast<uint4*>(cr + c) = make_uint4(code[0], code[1], code[2], code[3]);
+                if ((i & 1) == 0) sr[i / 2] = (uint8_t)byte;
+            }
         }
     }
 }
 
 template <int XT, int FMT>
-__global__ void __launch_bounds__(kThreads) pack8_kernel(const uint16_t* x, long long ldx, long long n, int cols,
-                                                         int groups, uint8_t* codes, uint8_t* scales)
+__global__ void __launch_bounds__(kThreads) pack8_kernel(const uint16_t* x, long long ldx, long long n, long long cols,
+                                                         uint8_t* codes, uint8_t* scales)
 {
-    const int lane = threadIdx.x & 31;
-    const long long total = n * groups, stride = (long long)gridDim.x * (kThreads / 32);
-    for (long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5; i < total; i += stride) {
-        const long long r = i / groups;
-        const int g = (int)(i - r * groups), c = 32 * g + lane;
-        const float v = c < cols ? x_load<XT>(x, r * ldx + c) : 0.f;
-        uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
-        const uint32_t byte = q8_scale_byte<FMT>(top);
-        const float inv = q8_inv(byte);
-        if (c < cols) codes[r * cols + c] = inv != 0.f ? (uint8_t)q8_encode<FMT>(v, inv) : (uint8_t)0;
-        if (lane == 0) scales[i] = (uint8_t)byte;
+    const long long groups = (cols + 31) / 32;
+    for (long long r = blockIdx.x; r < n; r += gridDim.x) {
+        for (long long g = (long long)blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32; g < groups;
+             g += (long long)gridDim.y * (blockDim.x / 32)) {
+            const long long c = 32 * g + (threadIdx.x & 31);
+            const float v = c < cols ? x_load<XT>(x, r * ldx + c) : 0.f;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
+            const uint32_t byte = q8_scale_byte<FMT>(top);
+            const float inv = q8_inv(byte);
+            if (c < cols) codes[r * cols + c] = inv != 0.f ? (uint8_t)q8_encode<FMT>(v, inv) : (uint8_t)0;
+            if ((threadIdx.x & 31) == 0) scales[r * groups + g] = (uint8_t)byte;
+        }
     }
 }
 
 // ---- unpack
 template <int XT, int FMT>
 __global__ void __launch_bounds__(kThreads) unpack8_vec_kernel(const uint8_t* codes, const uint8_t* scales, long long n,
-                                                               int cols, int groups, uint16_t* x, long long ldx)
+                                                               long long cols, uint16_t* x, long long ldx)
 {
-    const int per_row = cols / 8;
-    const long long total = n * per_row;
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < total; i += (long long)gridDim.x * kThreads) {
-        const long long r = i / per_row;
-        const int c = (int)(i - r * per_row) * 8;
-        float f[8];
-        decode8<FMT>(*reinterpret_cast<const uint2*>(codes + r * cols + c), q8_scale(scales[r * groups + c / 32]), f);
+    const long long groups = (cols + 31) / 32, pieces = cols / 16;
+    for (long long r = blockIdx.x; r < n; r += gridDim.x) {
+        const uint8_t* cr = codes + r * cols;
+        const uint8_t* sr = scales + r * groups;
+        uint16_t* xr = x + r * ldx;
+        for (long long i = (long long)blockIdx.y * blockDim.x + threadIdx.x; i < pieces;
+             i += (long long)gridDim.y * blockDim.x) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(cr) + i);
+            const float s = q8_scale(__ldg(sr + i / 2));
+            float f[16];
+            q8_codes4<FMT>(w.x, f);
+            q8_codes4<FMT>(w.y, f + 4);
+            q8_codes4<FMT>(w.z, f + 8);
+            q8_codes4<FMT>(w.w, f + 12);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = in_range<XT>(f[j]);
-        store8<XT>(x + r * ldx + c, f);
+            for (int j = 0; j < 16; ++j) f[j] = in_range<XT>(f[j] * s);
+            store8<XT>(xr + 16 * i, f);
+            store8<XT>(xr + 16 * i + 8, f + 8);
+        }
     }
 }
 
 template <int XT, int FMT>
 __global__ void __launch_bounds__(kThreads) unpack8_kernel(const uint8_t* codes, const uint8_t* scales, long long n,
-                                                           int cols, int groups, uint16_t* x, long long ldx)
+                                                           long long cols, uint16_t* x, long long ldx)
 {
-    const int lane = threadIdx.x & 31;
-    const long long total = n * groups, stride = (long long)gridDim.x * (kThreads / 32);
-    for (long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5; i < total; i += stride) {
-        const long long r = i / groups;
-        const int g = (int)(i - r * groups), c = 32 * g + lane;
-        if (c < cols)
-            x[r * ldx + c] = x_bits<XT>(in_range<XT>(q8_decode<FMT>(codes[r * cols + c], q8_scale(scales[i]))));
+    const long long groups = (cols + 31) / 32;
+    for (long long r = blockIdx.x; r < n; r += gridDim.x) {
+        for (long long c = (long long)blockIdx.y * blockDim.x + threadIdx.x; c < cols;
+             c += (long long)gridDim.y * blockDim.x)
+            x[r * ldx + c] = x_bits<XT>(
+                in_range<XT>(q8_decode<FMT>(codes[r * cols + c], q8_scale(__ldg(scales + r * groups + c / 32)))));
     }
 }
 
@@ -151,62 +158,68 @@ __global__ void __launch_bounds__(kThreads) unpack8_kernel(const uint8_t* codes,
 // partial sum per column and range.  A second kernel adds the ranges in order.
 constexpr int kRowThreads = 8;
 
-template <int XT, int FMT, int CPT>
-__global__ void __launch_bounds__(kThreads) act_grad8_kernel(ActGradArgs a, int groups)
+template <int XT, int FMT, int ACT, int CPT>
+__global__ void __launch_bounds__(kThreads) act_grad8_kernel(ActGradArgs a)
 {
     __shared__ float part[kRowThreads][32 * CPT + 1];
     const int ct = threadIdx.x & 31, rt = threadIdx.x >> 5;
     const long long c = ((long long)blockIdx.x * 32 + ct) * CPT;
     const long long r0 = a.n * blockIdx.y / gridDim.y, r1 = a.n * (blockIdx.y + 1) / gridDim.y;
-    const uint16_t* dy = static_cast<const uint16_t*>(a.dy);
-    uint16_t* dz = static_cast<uint16_t*>(a.dz);
-    float sum[CPT];
+    const long long groups = (a.rows + 31) / 32;
+    constexpr int P = CPT == 1 ? 1 : CPT / 2;  // pairs of columns
+    F2 sum[P];
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) sum[i] = 0.f;
+    for (int i = 0; i < P; ++i) sum[i] = f2(0.f, 0.f);
     if (c < a.rows) {
+        const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + (r0 + rt) * a.lddy + c;
+        uint16_t* dz = static_cast<uint16_t*>(a.dz) + (r0 + rt) * a.lddz + c;
+        const uint8_t* zc = ACT == TCQ_ACT_NONE ? nullptr : a.z_codes + (r0 + rt) * a.rows + c;
+        const uint8_t* zs = ACT == TCQ_ACT_NONE ? nullptr : a.z_scales + (r0 + rt) * groups + c / 32;
 #pragma unroll 2
         for (long long r = r0 + rt; r < r1; r += kRowThreads) {
-            float g[CPT], z[CPT];
+            float g[CPT < 2 ? 2 : CPT], z[CPT < 2 ? 2 : CPT];
+            g[1] = z[1] = 0.f;
+            float s = 0.f;
             if constexpr (CPT == 8) {
-                load8<XT>(dy + r * a.lddy + c, g);
-                if (a.act != TCQ_ACT_NONE)
-                    decode8<FMT>(*reinterpret_cast<const uint2*>(a.z_codes + r * a.rows + c),
-                                 q8_scale(a.z_scales[r * groups + c / 32]), z);
+                load8<XT>(dy, g);
+                if constexpr (ACT != TCQ_ACT_NONE) {
+                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(zc));
+                    q8_codes4<FMT>(w.x, z);
+                    q8_codes4<FMT>(w.y, z + 4);
+                }
             } else {
-                g[0] = x_load<XT>(dy, r * a.lddy + c);
-                if (a.act != TCQ_ACT_NONE)
-                    z[0] = q8_decode<FMT>(a.z_codes[r * a.rows + c], q8_scale(a.z_scales[r * groups + c / 32]));
+                g[0] = x_load<XT>(dy, 0);
+                if constexpr (ACT != TCQ_ACT_NONE) z[0] = q8_decode<FMT>(__ldg(zc), 1.f);
             }
-            switch (a.act) {
-            case TCQ_ACT_RELU:
+            if constexpr (ACT != TCQ_ACT_NONE) s = q8_slope_scale<FMT>(__ldg(zs));
 #pragma unroll
-                for (int i = 0; i < CPT; ++i) g[i] *= act_slope(z[i], TCQ_ACT_RELU);
-                break;
-            case TCQ_ACT_SILU:
-#pragma unroll
-                for (int i = 0; i < CPT; ++i) g[i] *= act_slope(z[i], TCQ_ACT_SILU);
-                break;
-            case TCQ_ACT_GELU:
-#pragma unroll
-                for (int i = 0; i < CPT; ++i) g[i] *= act_slope(z[i], TCQ_ACT_GELU);
-                break;
-            case TCQ_ACT_GELU_TANH:
-#pragma unroll
-                for (int i = 0; i < CPT; ++i) g[i] *= act_slope(z[i], TCQ_ACT_GELU_TANH);
-                break;
-            default: break;
+            for (int i = 0; i < P; ++i) {
+                F2 t = f2(g[2 * i], g[2 * i + 1]);
+                if constexpr (ACT != TCQ_ACT_NONE)
+                    t = f2_mul(t, act_slope2<ACT>(f2_mul(f2(z[2 * i], z[2 * i + 1]), f2(s, s))));
+                sum[i] = f2_add(sum[i], t);
+                f2_split(t, g[2 * i], g[2 * i + 1]);
             }
-#pragma unroll
-            for (int i = 0; i < CPT; ++i) sum[i] += g[i];
             if constexpr (CPT == 8)
-                store8<XT>(dz + r * a.lddz + c, g);
+                store8<XT>(dz, g);
             else
-                dz[r * a.lddz + c] = x_bits<XT>(g[0]);
+                *dz = x_bits<XT>(g[0]);
+            dy += kRowThreads * a.lddy;
+            dz += kRowThreads * a.lddz;
+            if constexpr (ACT != TCQ_ACT_NONE) {
+                zc += kRowThreads * a.rows;
+                zs += kRowThreads * groups;
+            }
         }
     }
     if (!a.partial) return;  // the same in every thread
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) part[rt][ct * CPT + i] = sum[i];
+    for (int i = 0; i < P; ++i) {
+        float u, v;
+        f2_split(sum[i], u, v);
+        part[rt][ct * CPT + 2 * i] = u;
+        if (CPT > 1) part[rt][ct * CPT + 2 * i + 1] = v;
+    }
     __syncthreads();
     for (int j = threadIdx.x; j < 32 * CPT; j += kThreads) {
         const long long col = (long long)blockIdx.x * 32 * CPT + j;
@@ -218,29 +231,60 @@ __global__ void __launch_bounds__(kThreads) act_grad8_kernel(ActGradArgs a, int 
     }
 }
 
+// 32 columns per CTA, the ranges shared among eight threads each, then joined in order.
 __global__ void __launch_bounds__(kThreads) sum_ranges_kernel(const float* partial, int ranges, long long rows, float* out)
 {
-    const long long c = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= rows) return;
+    __shared__ float part[kRowThreads][32];
+    pdl_wait();
+    const int ct = threadIdx.x & 31, rt = threadIdx.x >> 5;
+    const long long c = (long long)blockIdx.x * 32 + ct;
     float s = 0.f;
-    for (int i = 0; i < ranges; ++i) s += partial[i * rows + c];
-    out[c] = s;
+    if (c < rows) {
+#pragma unroll 4
+        for (int i = rt; i < ranges; i += kRowThreads) s += partial[(long long)i * rows + c];
+    }
+    part[rt][ct] = s;
+    __syncthreads();
+    if (rt == 0 && c < rows) {
+#pragma unroll
+        for (int k = 1; k < kRowThreads; ++k) s += part[k][ct];
+        out[c] = s;
+    }
 }
+
+// (rows, columns) of a grid over [n, cols] with `per` columns per thread
+dim3 row_grid(long long n, long long cols, int per, int threads, int num_sms)
+{
+    const long long most = 16ll * num_sms;
+    long long y = (cols + (long long)per * threads - 1) / ((long long)per * threads);
+    if (y > most) y = most;
+    long long x = (most + y - 1) / y;
+    if (x > n) x = n;
+    return dim3((unsigned)x, (unsigned)y);
+}
+
+// threads for rows of `items` items
+int row_threads(long long items) { return items >= kThreads ? kThreads : (int)((items + 31) / 32 * 32); }
 
 template <int XT, int FMT>
 cudaError_t pack_as(const void* x, long long ldx, long long n, long long cols, uint8_t* codes, uint8_t* scales,
                     int num_sms, cudaStream_t stream)
 {
     const uint16_t* xi = static_cast<const uint16_t*>(x);
-    const int groups = (int)((cols + 31) / 32);
-    const bool vec = cols % 8 == 0 && ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0 &&
-                     (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
-    long long grid = (n * groups * (vec ? 4 : 32) + kThreads - 1) / kThreads;
-    if (grid > 32ll * num_sms) grid = 32ll * num_sms;
-    if (vec)
-        pack8_vec_kernel<XT, FMT><<<(int)grid, kThreads, 0, stream>>>(xi, ldx, n, (int)cols, groups, codes, scales);
-    else
-        pack8_kernel<XT, FMT><<<(int)grid, kThreads, 0, stream>>>(xi, ldx, n, (int)cols, groups, codes, scales);
+    if (cols % 32 == 0 && (ldx == cols || n == 1)) {
+        cols *= n;
+        n = 1;
+        ldx = cols;
+    }
+    if (cols % 16 == 0 && ldx % 8 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(codes)) & 15) == 0) {
+        const int threads = row_threads(cols / 16);
+        pack8_vec_kernel<XT, FMT><<<row_grid(n, cols, 16, threads, num_sms), threads, 0, stream>>>(xi, ldx, n, cols, codes,
+                                                                                                 scales);
+    } else {
+        const int threads = row_threads(cols);
+        pack8_kernel<XT, FMT><<<row_grid(n, cols, 1, threads, num_sms), threads, 0, stream>>>(xi, ldx, n, cols, codes,
+                                                                                            scales);
+    }
     return cudaGetLastError();
 }
 
@@ -249,35 +293,49 @@ cudaError_t unpack_as(const uint8_t* codes, const uint8_t* scales, long long n, 
                       int num_sms, cudaStream_t stream)
 {
     uint16_t* xo = static_cast<uint16_t*>(x);
-    const int groups = (int)((cols + 31) / 32);
-    const bool vec = cols % 8 == 0 && ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0 &&
-                     (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
-    long long grid = (n * groups * (vec ? 4 : 32) + kThreads - 1) / kThreads;
-    if (grid > 32ll * num_sms) grid = 32ll * num_sms;
-    if (vec)
-        unpack8_vec_kernel<XT, FMT><<<(int)grid, kThreads, 0, stream>>>(codes, scales, n, (int)cols, groups, xo, ldx);
-    else
-        unpack8_kernel<XT, FMT><<<(int)grid, kThreads, 0, stream>>>(codes, scales, n, (int)cols, groups, xo, ldx);
+    if (cols % 32 == 0 && (ldx == cols || n == 1)) {
+        cols *= n;
+        n = 1;
+        ldx = cols;
+    }
+    if (cols % 16 == 0 && ldx % 8 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(codes)) & 15) == 0) {
+        const int threads = row_threads(cols / 16);
+        unpack8_vec_kernel<XT, FMT><<<row_grid(n, cols, 16, threads, num_sms), threads, 0, stream>>>(codes, scales, n, cols,
+                                                                                                   xo, ldx);
+    } else {
+        const int threads = row_threads(cols);
+        unpack8_kernel<XT, FMT><<<row_grid(n, cols, 1, threads, num_sms), threads, 0, stream>>>(codes, scales, n, cols, xo,
+                                                                                              ldx);
+    }
     return cudaGetLastError();
 }
 
-template <int XT, int FMT>
-cudaError_t act_grad_as(const ActGradArgs& a, cudaStream_t stream)
+template <int XT, int FMT, int ACT>
+void act_grad_launch(const ActGradArgs& a, cudaStream_t stream)
 {
-    const int groups = (int)((a.rows + 31) / 32);
     const bool vec = a.rows % 8 == 0 && a.lddy % 8 == 0 && a.lddz % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.dz)) & 15) == 0 &&
                      (reinterpret_cast<uintptr_t>(a.z_codes) & 7) == 0;
     const dim3 grid((unsigned)((a.rows + (vec ? 255 : 31)) / (vec ? 256 : 32)), (unsigned)a.splits);
     if (vec)
-        act_grad8_kernel<XT, FMT, 8><<<grid, kThreads, 0, stream>>>(a, groups);
+        act_grad8_kernel<XT, FMT, ACT, 8><<<grid, kThreads, 0, stream>>>(a);
     else
-        act_grad8_kernel<XT, FMT, 1><<<grid, kThreads, 0, stream>>>(a, groups);
-    cudaError_t e = cudaGetLastError();
+        act_grad8_kernel<XT, FMT, ACT, 1><<<grid, kThreads, 0, stream>>>(a);
+}
+
+template <int XT, int FMT>
+cudaError_t act_grad_as(const ActGradArgs& a, cudaStream_t stream)
+{
+    switch (a.act) {
+    case TCQ_ACT_RELU: act_grad_launch<XT, FMT, TCQ_ACT_RELU>(a, stream); break;
+    case TCQ_ACT_SILU: act_grad_launch<XT, FMT, TCQ_ACT_SILU>(a, stream); break;
+    case TCQ_ACT_GELU: act_grad_launch<XT, FMT, TCQ_ACT_GELU>(a, stream); break;
+    case TCQ_ACT_GELU_TANH: act_grad_launch<XT, FMT, TCQ_ACT_GELU_TANH>(a, stream); break;
+    default: act_grad_launch<XT, FMT, TCQ_ACT_NONE>(a, stream); break;
+    }
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.dbias) return e;
-    sum_ranges_kernel<<<(unsigned)((a.rows + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a.partial, a.splits,
-                                                                                              a.rows, a.dbias);
-    return cudaGetLastError();
+    return launch_pdl(sum_ranges_kernel, dim3((unsigned)((a.rows + 31) / 32)), dim3(kThreads), 0, stream, true, static_cast<const float*>(a.partial), a.splits, a.rows, a.dbias);
 }
 
 }  // namespace
@@ -300,12 +358,12 @@ cudaError_t launch_unpack8(const uint8_t* codes, const uint8_t* scales, int form
     return TCQ_BY_TYPES(unpack_as, xdtype, format, codes, scales, n, cols, x, ldx, num_sms, stream);
 }
 
-// Row ranges of the gradient's sums: about 1024 CTAs of 256 columns (so that every
-// SM holds several), at least 32 rows each.  A function of the shape alone, so that
+// Row ranges of the gradient's sums: about 4096 CTAs of 256 columns (several rounds of
+// what the SMs hold), at least 32 rows each.  A function of the shape alone, so that
 // a sum's order is the same on every device.
 int act_grad8_splits(long long n, long long rows)
 {
-    long long s = 1024 / ((rows + 255) / 256);
+    long long s = 4096 / ((rows + 255) / 256);
     if (s > n / 32) s = n / 32;
     return s < 1 ? 1 : (int)s;
 }

@@ -38,12 +38,30 @@ __device__ __forceinline__ uint32_t q8_scale_byte(uint32_t amax_bits)
     return e > 0 ? (uint32_t)e : 0u;
 }
 
-// A code from v with inv = 2^-e of its group.
+// Four codes in one word from v with inv = 2^-e of their group.  int8: adding 1.5 *
+// 2^23 rounds the (exact) quotient to nearest even and leaves it in the last byte; no
+// conversion instruction (they run at a quarter of the rate).
+template <int FMT>
+__device__ __forceinline__ uint32_t q8_encode4(const float* v, float inv)
+{
+    if constexpr (FMT == TCQ_Q8_INT8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(fmaf(v[i], inv, 12582912.f));
+        return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+}
+
+// One code.
 template <int FMT>
 __device__ __forceinline__ uint32_t q8_encode(float v, float inv)
 {
     if constexpr (FMT == TCQ_Q8_INT8)
-        return (uint32_t)__float2int_rn(v * inv) & 0xffu;
+        return __float_as_uint(fmaf(v, inv, 12582912.f)) & 0xffu;
     else
         return (uint32_t)__nv_cvt_float_to_fp8(v * inv, __NV_SATFINITE, __NV_E4M3);
 }
@@ -57,9 +75,41 @@ __device__ __forceinline__ float q8_decode(uint32_t code, float scale)
         return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3))) * scale;
 }
 
+// Four codes of one word, unscaled.  int8: the byte with its sign bit flipped, placed
+// in the last bits of 2^23, is 2^23 + 128 + q; no conversion instruction (they run at
+// a quarter of the rate).
+template <int FMT>
+__device__ __forceinline__ void q8_codes4(uint32_t word, float* f)
+{
+    if constexpr (FMT == TCQ_Q8_INT8) {
+        const uint32_t w = word ^ 0x80808080u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + i)) - 8388736.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(word >> (8 * i)), __NV_E4M3);
+            const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            f[i] = t.x;
+            f[i + 1] = t.y;
+        }
+    }
+}
+
 __device__ __forceinline__ float q8_scale(uint32_t byte)
 {
     return byte == 255u ? __int_as_float(0x7fffffff) : pow2f((int)byte - 127);
+}
+
+// The scale of a pre-activation whose only use is an activation's slope: held so that
+// far values stay far (a nonzero code at the limit is at least 64, where every slope is
+// 0 or 1) and z^2 stays finite.
+template <int FMT>
+__device__ __forceinline__ float q8_slope_scale(uint32_t byte)
+{
+    constexpr uint32_t most = FMT == TCQ_Q8_INT8 ? 127 + 6 : 127 + 15;
+    return q8_scale(byte == 255u || byte < most ? byte : most);
 }
 
 // inv for q8_encode; 0 for a group of NaNs, whose codes are then 0
@@ -125,24 +175,96 @@ __device__ __forceinline__ float act_value(float z, int act)
     }
 }
 
-// The activation's derivative (0 at z = 0 for relu).
-__device__ __forceinline__ float act_slope(float z, int act)
+// ---- two fp32 operations in one instruction (each rounds like the scalar one)
+struct F2 {
+    unsigned long long v;
+};
+
+__device__ __forceinline__ F2 f2(float a, float b)
 {
-    switch (act) {
-    case TCQ_ACT_RELU: return z > 0.f ? 1.f : (z != z ? z : 0.f);
-    case TCQ_ACT_SILU: {
-        const float s = sigmoidf(z);
-        return s * (1.f + z * (1.f - s));
-    }
-    case TCQ_ACT_GELU:
-        return 0.5f * (1.f + erff(z * 0.7071067811865476f)) + z * __expf(-0.5f * z * z) * 0.3989422804014327f;
-    case TCQ_ACT_GELU_TANH: {
-        // the slope is 0 or 1 long before +-64, and z^2 below must not overflow
-        z = z > 64.f ? 64.f : z < -64.f ? -64.f : z;
-        const float s = sigmoidf(2.f * kGeluA * (z + kGeluB * z * z * z));
-        return s + z * s * (1.f - s) * (2.f * kGeluA) * (1.f + 3.f * kGeluB * z * z);
-    }
-    default: return 1.f;
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void f2_split(F2 p, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / (1 + 2^t) of both
+__device__ __forceinline__ F2 f2_logistic2(F2 t)
+{
+    float a, b;
+    f2_split(t, a, b);
+    const F2 d = f2_add(f2(ex2(a), ex2(b)), f2(1.f, 1.f));
+    f2_split(d, a, b);
+    return f2(rcp(a), rcp(b));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// An activation's derivative at two finite z below 2^33 (0 at 0 for relu).  With s the
+// logistic function: silu' = s + z s (1 - s); gelu_tanh' = s + z s (1 - s) 2 u', s at 2 u.
+template <int ACT>
+__device__ __forceinline__ F2 act_slope2(F2 z)
+{
+    if constexpr (ACT == TCQ_ACT_SILU) {
+        const F2 s = f2_logistic2(f2_mul(z, f2(-kLog2e, -kLog2e)));
+        const F2 m = f2_fma(f2_mul(s, f2(-1.f, -1.f)), s, s);
+        return f2_fma(m, z, s);
+    } else if constexpr (ACT == TCQ_ACT_GELU_TANH) {
+        constexpr float a0 = -2.f * kGeluA * kLog2e, a1 = a0 * kGeluB, b0 = 2.f * kGeluA, b1 = 3.f * b0 * kGeluB;
+        const F2 zz = f2_mul(z, z);
+        const F2 s = f2_logistic2(f2_mul(z, f2_fma(zz, f2(a1, a1), f2(a0, a0))));
+        const F2 m = f2_fma(f2_mul(s, f2(-1.f, -1.f)), s, s);
+        return f2_fma(m, f2_mul(z, f2_fma(zz, f2(b1, b1), f2(b0, b0))), s);
+    } else {
+        float a, b;
+        f2_split(z, a, b);
+        if constexpr (ACT == TCQ_ACT_RELU) {
+            return f2(a > 0.f ? 1.f : (a != a ? a : 0.f), b > 0.f ? 1.f : (b != b ? b : 0.f));
+        } else {
+            auto gelu = [](float x) {
+                return 0.5f * (1.f + erff(x * 0.7071067811865476f)) + x * ex2(x * x * (-0.5f * kLog2e)) * 0.3989422804014327f;
+            };
+            return f2(gelu(a), gelu(b));
+        }
     }
 }
 
