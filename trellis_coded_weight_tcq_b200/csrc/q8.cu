@@ -2,8 +2,7 @@
 // through an activation from a packed pre-activation (format: q8.cuh).
 //
 // All three are bound by memory: 3 + 1/32 bytes per element to pack or unpack, 5 + 1/32
-// for the gradient.  Rows of a multiple of 16 elements (8 for the gradient) with
-// 16-byte aligned 16-bit rows move whole 16-byte vectors; other shapes take one element
+// for the gradient.  Rows of a multiple of 8 elements (16 to pack) with 16-byte aligned 16-bit rows move whole 16-byte vectors; other shapes take one element
 // per lane, a warp per group, which needs no alignment at all.  Rows that follow one
 // another without gaps and hold whole groups are one long row.
 #include "gemm.cuh"
@@ -113,28 +112,39 @@ __global__ void __launch_bounds__(kThreads) pack8_kernel(const uint16_t* x, long
 }
 
 // ---- unpack
+// Eight elements per thread and step, so that a warp's stores are one run; two steps'
+// loads in flight.
 template <int XT, int FMT>
 __global__ void __launch_bounds__(kThreads) unpack8_vec_kernel(const uint8_t* codes, const uint8_t* scales, long long n,
                                                                long long cols, uint16_t* x, long long ldx)
 {
-    const long long groups = (cols + 31) / 32, pieces = cols / 16;
+    const long long groups = (cols + 31) / 32, pieces = cols / 8;
+    const long long step = blockDim.x;
     for (long long r = blockIdx.x; r < n; r += gridDim.x) {
-        const uint8_t* cr = codes + r * cols;
+        const uint2* cr = reinterpret_cast<const uint2*>(codes + r * cols);
         const uint8_t* sr = scales + r * groups;
         uint16_t* xr = x + r * ldx;
-        for (long long i = (long long)blockIdx.y * blockDim.x + threadIdx.x; i < pieces;
-             i += (long long)gridDim.y * blockDim.x) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(cr) + i);
-            const float s = q8_scale(__ldg(sr + i / 2));
-            float f[16];
-            q8_codes4<FMT>(w.x, f);
-            q8_codes4<FMT>(w.y, f + 4);
-            q8_codes4<FMT>(w.z, f + 8);
-            q8_codes4<FMT>(w.w, f + 12);
+        for (long long i = (long long)blockIdx.y * 2 * step + threadIdx.x; i < pieces; i += (long long)gridDim.y * 2 * step) {
+            const bool two = i + step < pieces;
+            uint2 w[2];
+            uint32_t byte[2];
+            w[0] = __ldg(cr + i);
+            byte[0] = __ldg(sr + i / 4);
+            if (two) {
+                w[1] = __ldg(cr + i + step);
+                byte[1] = __ldg(sr + (i + step) / 4);
+            }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = in_range<XT>(f[j] * s);
-            store8<XT>(xr + 16 * i, f);
-            store8<XT>(xr + 16 * i + 8, f + 8);
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1 && !two) break;
+                const float s = q8_scale(byte[h]);
+                float f[8];
+                q8_codes4<FMT>(w[h].x, f);
+                q8_codes4<FMT>(w[h].y, f + 4);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = in_range<XT>(f[j] * s);
+                store8<XT>(xr + 8 * (i + h * step), f);
+            }
         }
     }
 }
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) unpack8_kernel(const uint8_t* codes,
 constexpr int kRowThreads = 8;
 
 template <int XT, int FMT, int ACT, int CPT>
-__global__ void __launch_bounds__(kThreads) act_grad8_kernel(ActGradArgs a)
+__global__ void __launch_bounds__(kThreads, 3) act_grad8_kernel(ActGradArgs a)
 {
     __shared__ float part[kRowThreads][32 * CPT + 1];
     const int ct = threadIdx.x & 31, rt = threadIdx.x >> 5;
@@ -171,45 +181,68 @@ __global__ void __launch_bounds__(kThreads) act_grad8_kernel(ActGradArgs a)
 #pragma unroll
     for (int i = 0; i < P; ++i) sum[i] = f2(0.f, 0.f);
     if (c < a.rows) {
-        const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + (r0 + rt) * a.lddy + c;
-        uint16_t* dz = static_cast<uint16_t*>(a.dz) + (r0 + rt) * a.lddz + c;
-        const uint8_t* zc = ACT == TCQ_ACT_NONE ? nullptr : a.z_codes + (r0 + rt) * a.rows + c;
-        const uint8_t* zs = ACT == TCQ_ACT_NONE ? nullptr : a.z_scales + (r0 + rt) * groups + c / 32;
-#pragma unroll 2
-        for (long long r = r0 + rt; r < r1; r += kRowThreads) {
-            float g[CPT < 2 ? 2 : CPT], z[CPT < 2 ? 2 : CPT];
-            g[1] = z[1] = 0.f;
-            float s = 0.f;
-            if constexpr (CPT == 8) {
-                load8<XT>(dy, g);
+        // a row's loads, two rows ahead of their use
+        struct Row {
+            uint4 d;
+            uint2 z;
+            uint32_t byte;
+        };
+        const long long first = r0 + rt;
+        int rows = first < r1 ? (int)((r1 - first + kRowThreads - 1) / kRowThreads) : 0, ahead = rows;
+        const uint16_t* dy = static_cast<const uint16_t*>(a.dy) + first * a.lddy + c;
+        const uint8_t* zc = ACT == TCQ_ACT_NONE ? nullptr : a.z_codes + first * a.rows + c;
+        const uint8_t* zs = ACT == TCQ_ACT_NONE ? nullptr : a.z_scales + first * groups + c / 32;
+        auto fetch = [&]() {
+            Row v = {};
+            if (ahead-- > 0) {
+                if constexpr (CPT == 8)
+                    v.d = *reinterpret_cast<const uint4*>(dy);
+                else
+                    v.d.x = *dy;
+                dy += kRowThreads * a.lddy;
                 if constexpr (ACT != TCQ_ACT_NONE) {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(zc));
-                    q8_codes4<FMT>(w.x, z);
-                    q8_codes4<FMT>(w.y, z + 4);
+                    if constexpr (CPT == 8)
+                        v.z = __ldg(reinterpret_cast<const uint2*>(zc));
+                    else
+                        v.z.x = __ldg(zc);
+                    v.byte = __ldg(zs);
+                    zc += kRowThreads * a.rows;
+                    zs += kRowThreads * groups;
                 }
-            } else {
-                g[0] = x_load<XT>(dy, 0);
-                if constexpr (ACT != TCQ_ACT_NONE) z[0] = q8_decode<FMT>(__ldg(zc), 1.f);
             }
-            if constexpr (ACT != TCQ_ACT_NONE) s = q8_slope_scale<FMT>(__ldg(zs));
+            return v;
+        };
+        uint16_t* dz = static_cast<uint16_t*>(a.dz) + first * a.lddz + c;
+        Row now = fetch(), next = fetch();
+        for (; rows > 0; --rows) {
+            const Row after = fetch();
+            float z[8];
+            float s = 0.f;
+            if constexpr (ACT != TCQ_ACT_NONE) {
+                s = q8_slope_scale<FMT>(now.byte);
+                q8_codes4<FMT>(now.z.x, z);
+                if constexpr (CPT == 8) q8_codes4<FMT>(now.z.y, z + 4);
+            }
+            const uint32_t d[4] = {now.d.x, now.d.y, now.d.z, now.d.w};
+            uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                F2 t = f2(g[2 * i], g[2 * i + 1]);
+                const float2 g = x_unpack2<XT>(d[i]);
+                F2 t = f2(g.x, g.y);
                 if constexpr (ACT != TCQ_ACT_NONE)
                     t = f2_mul(t, act_slope2<ACT>(f2_mul(f2(z[2 * i], z[2 * i + 1]), f2(s, s))));
                 sum[i] = f2_add(sum[i], t);
-                f2_split(t, g[2 * i], g[2 * i + 1]);
+                float u, v;
+                f2_split(t, u, v);
+                o[i] = x_pack2<XT>(u, v);
             }
             if constexpr (CPT == 8)
-                store8<XT>(dz, g);
+                *reinterpret_cast<uint4*>(dz) = make_uint4(o[0], o[1], o[2], o[3]);
             else
-                *dz = x_bits<XT>(g[0]);
-            dy += kRowThreads * a.lddy;
+                *dz = (uint16_t)o[0];
             dz += kRowThreads * a.lddz;
-            if constexpr (ACT != TCQ_ACT_NONE) {
-                zc += kRowThreads * a.rows;
-                zs += kRowThreads * groups;
-            }
+            now = next;
+            next = after;
         }
     }
     if (!a.partial) return;  // the same in every thread
@@ -298,8 +331,9 @@ cudaError_t unpack_as(const uint8_t* codes, const uint8_t* scales, long long n, 
         n = 1;
         ldx = cols;
     }
-    if (cols % 16 == 0 && ldx % 8 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(codes)) & 15) == 0) {
-        const int threads = row_threads(cols / 16);
+    if (cols % 8 == 0 && ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0 &&
+        (reinterpret_cast<uintptr_t>(codes) & 7) == 0) {
+        const int threads = row_threads(cols / 8);
         unpack8_vec_kernel<XT, FMT><<<row_grid(n, cols, 16, threads, num_sms), threads, 0, stream>>>(codes, scales, n, cols,
                                                                                                    xo, ldx);
     } else {
