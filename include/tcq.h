@@ -382,7 +382,8 @@ tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 forma
  * scales for a binary16 table and the computed code), relative to a power of two
  * per row of W; a bfloat16 row of X is scaled to binary16 by a power of two of its
  * own, exactly for elements above 2^-32 of the row's largest and within 2^-39 of
- * that largest for the others.  Sums are fp32.
+ * that largest for the others.  Sums are fp32.  A single token (n == 1, no checkpoint
+ * of Z) takes tcq_gemv's kernels, with both operands in fp32.
  *
  *   bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols  as tcq_gemv
  *               (T % 4 == 0, cols % T == 0, a binary16 table when L >= 15; the
@@ -396,7 +397,8 @@ tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 forma
  *               and [n, ceil(rows / 32)] scale bytes), or both NULL.
  *   workspace   device scratch, 256-byte aligned, at least tcq_gemm_workspace_bytes
  *               of the same shape (else TCQ_ERR_WORKSPACE).  Contents on entry do not
- *               matter; calls that may overlap need a workspace each.
+ *               matter; calls that may overlap need a workspace each.  A single token
+ *               without a checkpoint of Z needs none (NULL).
  * 16-bit arrays 2-byte aligned, fp32 arrays 4-byte aligned (16 bytes and row strides
  * that are multiples of 8 elements run faster).  n == 0 or rows == 0 is a no-op;
  * cols == 0 is TCQ_ERR_INVALID_ARG.  A row of X with an infinity or a NaN affects only its

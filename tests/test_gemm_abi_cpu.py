@@ -51,6 +51,15 @@ def test_gemm_refusals(over, status):
     assert _gemm(**over) == status
 
 
+def test_gemm_single_token_needs_no_workspace():
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("passes the checks: with a GPU there it would run on the made-up addresses")
+    assert _gemm(n=1, ws=None, wsb=0) not in (INVALID, WORKSPACE)
+    assert _gemm(n=1, ws=None, wsb=0, zc=FAKE, zs=FAKE) == INVALID
+
+
 def test_gemm_without_work():
     assert _gemm(n=0, x=None, y=None, ws=None, wsb=0) == OK
     assert _gemm(rows=0, bits=None, st=None, x=None, y=None, ws=None, wsb=0) == OK

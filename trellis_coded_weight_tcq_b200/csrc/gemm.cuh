@@ -33,6 +33,15 @@ struct Epilogue {
     int accumulate;          // fp32 outputs: add to what is there
 };
 
+// One token of the forward product (gemv.cu): the matrix-vector kernels on a 16-bit
+// vector, weights in fp32, with the epilogue's bias, activation and residual.
+struct GemvLayerArgs : GemvArgs {
+    const void* x16;
+    bool x_vec;  // 8-byte aligned
+    Epilogue e;
+};
+cudaError_t launch_gemv_layer(const GemvLayerArgs& a, int xdtype, int num_sms, cudaStream_t stream);
+
 enum GemmKind { kGemmForward = 0, kGemmDgrad = 1, kGemmWgrad = 2 };
 
 // out[m, n] = epilogue(sum_k a b), 16-bit operands (fmt 0 binary16, 1 bfloat16):

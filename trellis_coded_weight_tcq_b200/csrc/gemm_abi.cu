@@ -127,18 +127,32 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     if (n == 0 || rows == 0) return TCQ_OK;
     if (cols == 0 || !matrix_pointers(bits, start_state, scale, codebook, cb_dtype) || !valid_rows(x, ldx, cols) ||
         !valid_rows(y, ldy, rows) || (residual && !valid_rows(residual, ldr, rows)) || (bias && !aligned(bias, 4)) ||
-        (z_codes == nullptr) != (z_scales == nullptr) || !workspace || !aligned(workspace, 256))
+        (z_codes == nullptr) != (z_scales == nullptr))
         return TCQ_ERR_INVALID_ARG;
     const int num_sms = sms();
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const CodedMatrix w = matrix(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols);
+    if (n == 1 && !z_codes) {
+        if (num_sms <= 0) return TCQ_ERR_CUDA;
+        GemvLayerArgs g;
+        static_cast<GemvArgs&>(g) = {w.bits, w.start_state, w.scale, w.cb, w.cb_f16, L, k, T, w.W, rows, cols, nullptr,
+                                     nullptr};
+        g.x16 = x;
+        g.x_vec = aligned(x, 8);
+        g.e = plain_epilogue(y, ldy);
+        g.e.bias = bias;
+        g.e.act = act;
+        g.e.residual = residual;
+        return status(launch_gemv_layer(g, xdtype, num_sms, st));
+    }
+    if (!workspace || !aligned(workspace, 256)) return TCQ_ERR_INVALID_ARG;
     const GemmSpace sp = forward_space(cb_dtype, L, T, rows, cols, n, num_sms > 0 ? num_sms : 148);
     if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
     if (num_sms <= 0) return TCQ_ERR_CUDA;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     unsigned int* err = device_error_word(st);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     float* row_pow2 = reinterpret_cast<float*>(ws + sp.row_pow2);
     float* x_pow2 = reinterpret_cast<float*>(ws + sp.x_pow2);
-    const CodedMatrix w = matrix(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols);
     const int64_t ldw = round_up(cols, 8);
 
     const bool fused = fused_shape(T, rows, cols, n);

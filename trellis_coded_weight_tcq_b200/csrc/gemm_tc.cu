@@ -11,8 +11,18 @@
 // tensor memory; two sets of them let the four epilogue warps store a tile while the
 // next one is multiplied.  The grid is persistent, one pair per two SMs.
 //
+// Outputs that TMA can address (16-byte aligned base and rows) leave through shared
+// memory: a warp writes 32 rows of 128 bytes to a swizzled box and stores it as whole
+// lines (a lane's own 16-byte stores would each touch half a sector of 32 different
+// rows); other outputs are stored by the lanes.
+//
+// The tensor core's running fp32 sum loses about 1e-7 of a sum per square root of its
+// steps.  That does not show in 16-bit outputs; the weight gradient, fp32 and summed over
+// all tokens, takes its sums out of tensor memory every 1024 tokens and adds them in
+// registers (error against float64 at 4096 tokens: 1.6e-6 without, 8e-7 with).
+//
 // Roles: warp 0 TMA, warp 1 MMA (first CTA of the pair only), warp 2 tensor memory,
-// warps 4-7 epilogue.  Barriers: full (both CTAs' loads of a stage landed; in the
+// warps 4 and up epilogue.  Barriers: full (both CTAs' loads of a stage landed; in the
 // first CTA), empty (the MMAs that read a stage are done; in both, by a commit to
 // both), tfull / tempty (an accumulator set is complete / has been read).
 #include "gemm.cuh"
@@ -23,7 +33,12 @@
 
 namespace tcq {
 
-bool make_map_16bit(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld, int box_rows)
+namespace {
+
+// A tensor map of a row-major matrix with the 128-byte swizzle, boxes of box_rows x
+// 128 bytes; elements of 2 or 4 bytes.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, int element, const void* base, long long rows, long long cols,
+              long long ld, int box_rows)
 {
     typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -40,13 +55,26 @@ bool make_map_16bit(CUtensorMap* map, const void* base, long long rows, long lon
     }();
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * element};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / element), (cuuint32_t)box_rows};
     const cuuint32_t step[2] = {1u, 1u};
-    // the element type only matters for the fill, which is zero in both
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map_out(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld, int element)
+{
+    return make_map(map, element == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, element, base,
+                    rows, cols, ld, 32);
+}
+
+}  // namespace
+
+bool make_map_16bit(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld, int box_rows)
+{
+    // the element type only matters for the fill, which is zero in both
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, rows, cols, ld, box_rows);
 }
 
 namespace {
@@ -55,16 +83,25 @@ constexpr int kStages = 6;
 constexpr int kTile = 256;            // rows and columns of a pair's tile
 constexpr int kDepth = 64;            // reduction depth of a stage
 constexpr int kHalfBytes = 128 * kDepth * 2;  // one CTA's half of one operand's stage
-constexpr int kThreads = 256;
+constexpr int kBoxBytes = 32 * 128;   // a warp's box of the output: 32 rows of 128 bytes
+constexpr int kSegment = 16;          // stages (1024 deep) that the weight gradient sums in tensor memory
+
+// Four epilogue warps, two boxes each; the weight gradient has eight with one box, a
+// half of the tile's columns each, because they hold their sums in registers.
+__host__ __device__ constexpr int epilogue_warps(int kind) { return kind == kGemmWgrad ? 8 : 4; }
+__host__ __device__ constexpr int gemm_threads(int kind) { return 128 + 32 * epilogue_warps(kind); }
 
 struct __align__(1024) Smem {
     unsigned char a[kStages][kHalfBytes];
     unsigned char b[kStages][kHalfBytes];
-    float2 cols[2][kTile];  // (power of two, bias) of the columns of a tile, per accumulator set
+    unsigned char box[8][kBoxBytes];
+    float2 cols[kTile];  // (power of two, bias) of a tile's columns
     unsigned long long full[kStages], empty[kStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int stop;
 };
+
+static_assert(sizeof(Smem) <= 227 * 1024, "shared memory");
 
 struct Shape {
     long long m, n, k;
@@ -72,11 +109,11 @@ struct Shape {
     int fmt;
 };
 
-// 32 consecutive 16-bit outputs of one row: row r, columns c .. c + 31, `count` of
-// them below n.
+// 32 values of one row through the epilogue: row r, columns c .. c + 31, `count` of them
+// below n.
 template <int KIND, int XT>
-__device__ __forceinline__ void store32_16bit(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                              int count, bool vec, float row_scale, const float2* cols)
+__device__ __forceinline__ void apply32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
+                                        int count, bool vec, float row_scale, const float2* cols)
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= row_scale;
@@ -159,6 +196,13 @@ __device__ __forceinline__ void store32_16bit(const Epilogue& e, long long r, lo
             }
         }
     }
+}
+
+// 32 16-bit outputs of a row by its lane.
+template <int XT>
+__device__ __forceinline__ void store32(const Epilogue& e, long long r, long long c, const float (&v)[32], int count,
+                                        bool vec)
+{
     uint16_t* o = static_cast<uint16_t*>(e.out) + r * e.ldo + c;
     if (vec && count == 32) {
 #pragma unroll
@@ -173,40 +217,24 @@ __device__ __forceinline__ void store32_16bit(const Epilogue& e, long long r, lo
     }
 }
 
-// The same for either output type.
-template <int KIND, int XT>
-__device__ __forceinline__ void store32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                        bool vec, float row_scale, const float2* cols)
+// 64 bytes of a lane's row of a swizzled box: 32 16-bit values, the first or second half.
+template <int XT>
+__device__ __forceinline__ void box32(unsigned char* row, int lane, int half, const float (&v)[32])
 {
-    const int count = n - c < 32 ? (int)(n - c) : 32;
-    if constexpr (KIND == kGemmWgrad) {
-        float* o = static_cast<float*>(e.out) + r * e.ldo + c;
-        if (vec && count == 32) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                float4 t = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                if (e.accumulate) {
-                    const float4 old = *reinterpret_cast<const float4*>(o + i);
-                    t.x += old.x; t.y += old.y; t.z += old.z; t.w += old.w;
-                }
-                *reinterpret_cast<float4*>(o + i) = t;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < count) o[i] = e.accumulate ? o[i] + v[i] : v[i];
-        }
-    } else {
-        store32_16bit<KIND, XT>(e, r, c, n, v, count, vec, row_scale, cols);
-    }
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(row + (((4 * half + i) ^ (lane & 7)) << 4)) =
+            make_uint4(x_pack2<XT>(v[8 * i], v[8 * i + 1]), x_pack2<XT>(v[8 * i + 2], v[8 * i + 3]),
+                       x_pack2<XT>(v[8 * i + 4], v[8 * i + 5]), x_pack2<XT>(v[8 * i + 6], v[8 * i + 7]));
 }
 
 template <int KIND, int XT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Shape p, Epilogue e,
-            bool vec, unsigned int* err)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND), 1)
+gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+            const __grid_constant__ CUtensorMap map_out, Shape p, Epilogue e, bool vec, bool tma_out, unsigned int* err)
 {
-    constexpr int AMN = KIND == kGemmWgrad, BMN = KIND != kGemmForward;
+    constexpr int AMN = KIND == kGemmWgrad, BMN = KIND != kGemmForward, EW = epilogue_warps(KIND);
+    const int segment = KIND == kGemmWgrad ? kSegment : p.k_steps;  // stages between two accumulator sets
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem& S = *reinterpret_cast<Smem*>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -220,7 +248,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&S.tfull[i]), 1);
-            mbar_init(smem_addr(&S.tempty[i]), 8);  // four epilogue warps in each CTA
+            mbar_init(smem_addr(&S.tempty[i]), 2 * EW);  // the epilogue warps of both CTAs
         }
         mbar_init(smem_addr(&S.drain), 1);
         S.stop = 0;
@@ -276,27 +304,30 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const uint32_t idesc = mma_idesc(256, 256, p.fmt, AMN, BMN);
             int it = 0, done = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs, ++done) {
-                const int acc = done & 1;
-                ok = mbar_wait(smem_addr(&S.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
-                if (!ok) break;
-                tc_fence_after();
-                for (int ks = 0; ks < p.k_steps; ++ks, ++it) {
-                    const int s = it % kStages;
-                    ok = mbar_wait(smem_addr(&S.full[s]), (it / kStages) & 1, stop, err);
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                for (int k0 = 0; k0 < p.k_steps && ok; k0 += segment, ++done) {
+                    const int acc = done & 1;
+                    ok = mbar_wait(smem_addr(&S.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = smem_addr(S.a[s]), b = smem_addr(S.b[s]);
-#pragma unroll
-                    for (int j = 0; j < kDepth / 16; ++j) {
+                    const int k1 = k0 + segment < p.k_steps ? k0 + segment : p.k_steps;
+                    for (int ks = k0; ks < k1; ++ks, ++it) {
+                        const int s = it % kStages;
+                        ok = mbar_wait(smem_addr(&S.full[s]), (it / kStages) & 1, stop, err);
+                        if (!ok) break;
+                        tc_fence_after();
                         // 16 deep: 32 bytes along a K-major row, 16 rows of 128 bytes otherwise
-                        const unsigned long long da = smem_desc_sw128(a + j * (AMN ? 2048 : 32), kHalfBytes / 2);
-                        const unsigned long long db = smem_desc_sw128(b + j * (BMN ? 2048 : 32), kHalfBytes / 2);
-                        mma_f16<2>(tmem + acc * 256, da, db, idesc, (ks | j) != 0);
+                        // (a descriptor counts in 16 bytes)
+                        const unsigned long long da = smem_desc_sw128(smem_addr(S.a[s]), kHalfBytes / 2);
+                        const unsigned long long db = smem_desc_sw128(smem_addr(S.b[s]), kHalfBytes / 2);
+#pragma unroll
+                        for (int j = 0; j < kDepth / 16; ++j)
+                            mma_f16<2>(tmem + acc * 256, da + j * (AMN ? 128 : 2), db + j * (BMN ? 128 : 2), idesc,
+                                       ks != k0 || j != 0);
+                        mma_commit<2>(smem_addr(&S.empty[s]));
                     }
-                    mma_commit<2>(smem_addr(&S.empty[s]));
+                    if (ok) mma_commit<2>(smem_addr(&S.tfull[acc]));
                 }
-                if (ok) mma_commit<2>(smem_addr(&S.tfull[acc]));
             }
             if (*stop) {  // nothing issued may still run when the tensor memory is freed
                 mma_commit<2>(smem_addr(&S.drain));
@@ -306,38 +337,121 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         __syncwarp();
     } else if (warp >= 4) {
         const int quarter = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         int done = 0;
-        for (int t = pair; t < tiles; t += pairs, ++done) {
-            const int acc = done & 1;
-            if constexpr (KIND == kGemmForward) {
-                // this tile's columns, while its product still runs; the set's last readers
-                // passed the barrier of the tile between
-                for (int i = threadIdx.x - 128; i < kTile; i += 128) {
-                    const long long c = (long long)(t / p.m_tiles) * kTile + i;
-                    S.cols[acc][i] = make_float2(e.col_scale && c < p.n ? __ldg(e.col_scale + c) : 1.f,
-                                                 e.bias && c < p.n ? __ldg(e.bias + c) : 0.f);
-                }
-                named_barrier(1, 128);
-            }
-            bool ok = mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            const long long r = (long long)(t % p.m_tiles) * kTile + rank * 128 + quarter * 32 + lane;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            const long long r0 = (long long)(t % p.m_tiles) * kTile + rank * 128 + quarter * 32, r = r0 + lane;
             const long long n0 = (long long)(t / p.m_tiles) * kTile;
-            const float row_scale = e.row_scale && r < p.m ? __ldg(e.row_scale + r) : 1.f;
+            if constexpr (KIND == kGemmWgrad) {
+                const int half = (warp - 4) >> 2;
+                unsigned char* box = S.box[warp - 4];
+                float sum[128];
+                for (int k0 = 0; k0 < p.k_steps && ok; k0 += segment, ++done) {
+                    const int acc = done & 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float v[16];
+                        tmem_load16(lanes + acc * 256 + 128 * half + 16 * j, v);
+                        if (k0 == 0) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[16 * j + i] = v[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[16 * j + i] += v[i];
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_addr(&S.tempty[acc]), 0));
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const long long c = n0 + 128 * half + 32 * j;
+                    if (c >= p.n || r0 >= p.m) break;  // the same in every lane
+                    if (tma_out) {
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                                make_float4(sum[32 * j + 4 * i], sum[32 * j + 4 * i + 1], sum[32 * j + 4 * i + 2],
+                                            sum[32 * j + 4 * i + 3]);
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (e.accumulate)
+                                tma_add_2d(&map_out, smem_addr(box), (int)c, (int)r0);
+                            else
+                                tma_store_2d(&map_out, smem_addr(box), (int)c, (int)r0);
+                            bulk_commit();
+                        }
+                    } else if (r < p.m) {
+                        float* o = static_cast<float*>(e.out) + r * e.ldo + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < p.n) o[i] = e.accumulate ? o[i] + sum[32 * j + i] : sum[32 * j + i];
+                    }
+                }
+            } else {
+                const int acc = done & 1;
+                if constexpr (KIND == kGemmForward) {
+                    // this tile's columns, while its product still runs
+                    named_barrier(1, 128);  // the last tile's have been read
+                    for (int i = threadIdx.x - 128; i < kTile; i += 128) {
+                        const long long c = n0 + i;
+                        S.cols[i] = make_float2(e.col_scale && c < p.n ? __ldg(e.col_scale + c) : 1.f,
+                                                     e.bias && c < p.n ? __ldg(e.bias + c) : 0.f);
+                    }
+                    named_barrier(1, 128);
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
+                if (!ok) break;
+                tc_fence_after();
+                const float row_scale = e.row_scale && r < p.m ? __ldg(e.row_scale + r) : 1.f;
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                if (n0 + c >= p.n) break;
-                float v[32];
-                tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + acc * 256 + c, v);
-                if (r < p.m) store32<KIND, XT>(e, r, n0 + c, p.n, v, vec, row_scale, S.cols[acc] + c);
+                for (int c = 0; c < kTile; c += 64) {
+                    if (n0 + c >= p.n || r0 >= p.m) break;  // the same in every lane
+                    unsigned char* box = S.box[2 * quarter + ((c >> 6) & 1)];
+                    if (tma_out) {
+                        if (lane == 0) bulk_wait_read<1>();  // the box's last store, two ago, has been read
+                        __syncwarp();
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const long long ch = n0 + c + 32 * h;
+                        if (ch >= p.n) break;
+                        float v[32];
+                        tmem_load32(lanes + acc * 256 + c + 32 * h, v);
+                        const int count = p.n - ch < 32 ? (int)(p.n - ch) : 32;
+                        if (r < p.m) {
+                            apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale, S.cols + c + 32 * h);
+                            if (!tma_out) store32<XT>(e, r, ch, v, count, vec);
+                        }
+                        if (tma_out) box32<XT>(box + lane * 128, lane, h, v);
+                        __syncwarp();
+                    }
+                    if (tma_out) {
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&map_out, smem_addr(box), (int)(n0 + c), (int)r0);
+                            bulk_commit();
+                        }
+                    }
+                }
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_addr(&S.tempty[acc]), 0));
+                ++done;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_addr(&S.tempty[acc]), 0));
         }
+        if (lane == 0) bulk_wait_all();  // the boxes are read and the outputs written
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -351,7 +465,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 template <int KIND, int XT>
 cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigned int* err, cudaStream_t stream)
 {
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mo;
     const bool ok = (KIND == kGemmWgrad ? make_map_16bit(&ma, g.a, g.k, g.m, g.lda, 64)
                                         : make_map_16bit(&ma, g.a, g.m, g.k, g.lda, 128)) &&
                     (KIND == kGemmForward ? make_map_16bit(&mb, g.b, g.n, g.k, g.ldb, 128)
@@ -367,6 +481,11 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigne
     s.fmt = g.fmt;
     const int es = KIND == kGemmWgrad ? 4 : 2;
     bool vec = (reinterpret_cast<uintptr_t>(e.out) & 15) == 0 && e.ldo * es % 16 == 0;
+    const bool tma_out = vec;
+    if (!tma_out)
+        mo = ma;  // not used
+    else if (!make_map_out(&mo, e.out, g.m, g.n, e.ldo, es))
+        return cudaErrorInvalidValue;
     if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 15) == 0 && e.ldr % 8 == 0;
     cudaError_t st = cudaFuncSetAttribute(gemm_kernel<KIND, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)sizeof(Smem));
@@ -374,7 +493,7 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigne
     const long long tiles = (long long)s.m_tiles * s.n_tiles;
     if (tiles > INT32_MAX - num_sms) return cudaErrorInvalidValue;
     const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    gemm_kernel<KIND, XT><<<2 * pairs, kThreads, sizeof(Smem), stream>>>(ma, mb, s, e, vec, err);
+    gemm_kernel<KIND, XT><<<2 * pairs, gemm_threads(KIND), sizeof(Smem), stream>>>(ma, mb, mo, s, e, vec, tma_out, err);
     return cudaGetLastError();
 }
 

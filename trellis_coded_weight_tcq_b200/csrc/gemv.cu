@@ -18,10 +18,46 @@
 // shared-memory bank conflicts bound the kernel), a widening and an FMA; the
 // bits are k/8 bytes per weight from HBM.
 #include "codes.cuh"
+#include "gemm.cuh"
+#include "q8.cuh"
 
 namespace tcq {
 
 namespace {
+
+// Where the vector comes from and what happens to a row's sum: fp32 in and out
+// (tcq_gemv), or one token of tcq_gemm, a 16-bit vector widened as it is staged and the
+// layer's epilogue on the sum.
+struct VectorF32 {
+    typedef GemvArgs Args;
+    static __device__ __forceinline__ float load(const Args& a, long long i) { return a.x[i]; }
+    static __device__ __forceinline__ float4 load4(const Args& a, long long q)
+    {
+        return __ldg(reinterpret_cast<const float4*>(a.x) + q);
+    }
+    static __device__ __forceinline__ void store(const Args& a, long long r, float v) { a.y[r] = v; }
+};
+
+template <int XT>
+struct VectorLayer {
+    typedef GemvLayerArgs Args;
+    static __device__ __forceinline__ float load(const Args& a, long long i) { return x_load<XT>(a.x16, i); }
+    static __device__ __forceinline__ float4 load4(const Args& a, long long q)
+    {
+        if (a.x_vec) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.x16) + q);
+            const float2 l = x_unpack2<XT>(v.x), h = x_unpack2<XT>(v.y);
+            return make_float4(l.x, l.y, h.x, h.y);
+        }
+        return make_float4(load(a, 4 * q), load(a, 4 * q + 1), load(a, 4 * q + 2), load(a, 4 * q + 3));
+    }
+    static __device__ __forceinline__ void store(const Args& a, long long r, float v)
+    {
+        v = act_value(a.e.bias ? v + __ldg(a.e.bias + r) : v, a.e.act);
+        if (a.e.residual) v += x_load<XT>(a.e.residual, r);
+        static_cast<uint16_t*>(a.e.out)[r] = x_bits<XT>(v);
+    }
+};
 
 constexpr int kGemvThreads = 1024;
 constexpr int kGemvUnroll = 4;
@@ -30,8 +66,8 @@ constexpr int kGemvUnroll = 4;
 // binary16) or kCodeMad (the computed code, no table).
 enum GemvCode { kCodeF32 = 0, kCodeF16 = 1, kCodeMad = 2 };
 
-template <int CODE, bool XSMEM>
-__global__ void __launch_bounds__(kGemvThreads, 1) gemv_kernel(GemvArgs a)
+template <int CODE, bool XSMEM, typename IO>
+__global__ void __launch_bounds__(kGemvThreads, 1) gemv_kernel(typename IO::Args a)
 {
     constexpr bool CB16 = CODE == kCodeF16;
     extern __shared__ __align__(16) unsigned char gsm[];
@@ -41,7 +77,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_kernel(GemvArgs a)
     // stage the codebook (16-byte copies when possible) and x
     if constexpr (CODE == kCodeMad) {
         if constexpr (XSMEM)
-            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = a.x[i];
+            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = IO::load(a, i);
     } else {
         const unsigned char* src = reinterpret_cast<const unsigned char*>(a.cb);
         if (CB16 || !a.cb_f16) {  // same representation in and out
@@ -58,7 +94,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_kernel(GemvArgs a)
                 tab[i] = load_codeword(a.cb, 1, (uint32_t)i);
         }
         if constexpr (XSMEM)
-            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = a.x[i];
+            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = IO::load(a, i);
     }
     __syncthreads();
 
@@ -121,7 +157,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_kernel(GemvArgs a)
             if constexpr (XSMEM)
                 xv = reinterpret_cast<const float4*>(xs)[g];
             else
-                xv = __ldg(reinterpret_cast<const float4*>(a.x) + g);
+                xv = IO::load4(a, g);
             // align the window: (hi:lo) << off puts the first state's bits at the
             // top; the four windows then start at bits e k <= 12 of the aligned
             // pair and end before bit 12 + L <= 28 of its high word's range + 32
@@ -162,7 +198,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_kernel(GemvArgs a)
         if (itn == 0) {  // row r complete
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            if (lane == 0 && TCQ_IN_BOUNDS(r, a.rows)) a.y[r] = acc;
+            if (lane == 0 && TCQ_IN_BOUNDS(r, a.rows)) IO::store(a, r, acc);
             acc = 0.f;
         }
         r = rn;
@@ -175,8 +211,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_kernel(GemvArgs a)
 // state windows all lie in the high word of the 64-bit read once it is aligned
 // to the first window, (N-1)k + L <= 32, so a state is one shift and one mask.
 // Everything else as gemv_kernel; each item's sum runs as two FMA chains.
-template <int L, int K, int N, int CODE, bool XSMEM>
-__global__ void __launch_bounds__(kGemvThreads, 1) gemv_fast_kernel(GemvArgs a)
+template <int L, int K, int N, int CODE, bool XSMEM, typename IO>
+__global__ void __launch_bounds__(kGemvThreads, 1) gemv_fast_kernel(typename IO::Args a)
 {
     static_assert((N - 1) * K + L <= 32 && N % 4 == 0, "item windows must share one word");
     constexpr bool CB16 = CODE == kCodeF16;
@@ -188,7 +224,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_fast_kernel(GemvArgs a)
     float* xs = reinterpret_cast<float*>(gsm + ((tab_bytes + 15) & ~(size_t)15));
     if constexpr (CODE == kCodeMad) {
         if constexpr (XSMEM)
-            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = a.x[i];
+            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = IO::load(a, i);
     } else {
         const unsigned char* src = reinterpret_cast<const unsigned char*>(a.cb);
         if (CB16 || !a.cb_f16) {
@@ -205,7 +241,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_fast_kernel(GemvArgs a)
                 tab[i] = load_codeword(a.cb, 1, (uint32_t)i);
         }
         if constexpr (XSMEM)
-            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = a.x[i];
+            for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = IO::load(a, i);
     }
     __syncthreads();
 
@@ -276,7 +312,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_fast_kernel(GemvArgs a)
                 if constexpr (XSMEM)
                     v = reinterpret_cast<const float4*>(xs)[(i * N + e) >> 2];
                 else
-                    v = __ldg(reinterpret_cast<const float4*>(a.x) + ((i * N + e) >> 2));
+                    v = IO::load4(a, (i * N + e) >> 2);
                 xv[e] = v.x;
                 xv[e + 1] = v.y;
                 xv[e + 2] = v.z;
@@ -310,7 +346,7 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_fast_kernel(GemvArgs a)
         if (itn == 0) {
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            if (lane == 0 && TCQ_IN_BOUNDS(r, a.rows)) a.y[r] = acc;
+            if (lane == 0 && TCQ_IN_BOUNDS(r, a.rows)) IO::store(a, r, acc);
             acc = 0.f;
         }
         r = rn;
@@ -335,8 +371,8 @@ __global__ void __launch_bounds__(kGemvThreads, 1) gemv_fast_kernel(GemvArgs a)
 constexpr int kMadRowsChunk = 8;  // blocks per fetch of gemv_rows_kernel
 constexpr int kMadRowsThreads = 512;
 
-template <int L, int K, int N, int T, int CODE>
-__global__ void __launch_bounds__(kMadRowsThreads, 1) gemv_rows_kernel(GemvArgs a)
+template <int L, int K, int N, int T, int CODE, typename IO>
+__global__ void __launch_bounds__(kMadRowsThreads, 1) gemv_rows_kernel(typename IO::Args a)
 {
     constexpr int IPB = T / N;  // items per block
     static_assert(IPB % 32 == 0 && (N - 1) * K + L <= 32 && N % 4 == 0, "shape");
@@ -355,7 +391,7 @@ __global__ void __launch_bounds__(kMadRowsThreads, 1) gemv_rows_kernel(GemvArgs 
         float* tab = reinterpret_cast<float*>(gsm);
         for (int i = threadIdx.x; i < (1 << L); i += blockDim.x) tab[i] = load_codeword(a.cb, a.cb_f16, (uint32_t)i);
     }
-    for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = a.x[i];
+    for (long long i = threadIdx.x; i < a.cols; i += blockDim.x) xs[i] = IO::load(a, i);
     __syncthreads();
 
     const int lane = threadIdx.x & 31;
@@ -448,7 +484,7 @@ __global__ void __launch_bounds__(kMadRowsThreads, 1) gemv_rows_kernel(GemvArgs 
     auto finish_row = [&](long long row) {
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-        if (lane == 0 && TCQ_IN_BOUNDS(row, a.rows)) a.y[row] = acc;
+        if (lane == 0 && TCQ_IN_BOUNDS(row, a.rows)) IO::store(a, row, acc);
         acc = 0.f;
     };
     while (r < a.rows) {  // r and c are the same in every lane of the warp
@@ -630,8 +666,8 @@ __device__ __forceinline__ void word_dot(uint32_t hi, uint32_t lo, const float* 
     }
 }
 
-template <int CODE, int R>
-__global__ void __launch_bounds__(kPairThreads, 1) gemv_pair_kernel(GemvArgs a)
+template <int CODE, int R, typename IO>
+__global__ void __launch_bounds__(kPairThreads, 1) gemv_pair_kernel(typename IO::Args a)
 {
     constexpr int kPairRows = R;  // rows per warp item
     constexpr int T = 256, W = 16;
@@ -650,7 +686,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemv_pair_kernel(GemvArgs a)
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     for (int i = threadIdx.x; i < (int)(a.cols / 4); i += blockDim.x) {
-        const float4 v = reinterpret_cast<const float4*>(a.x)[i];
+        const float4 v = IO::load4(a, i);
         *reinterpret_cast<float4*>(xs + xpad(4 * i)) = v;
     }
 
@@ -769,7 +805,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemv_pair_kernel(GemvArgs a)
             }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0 && TCQ_IN_BOUNDS(r, a.rows)) a.y[r] = v;
+            if (lane == 0 && TCQ_IN_BOUNDS(r, a.rows)) IO::store(a, r, v);
         }
     }
 
@@ -784,7 +820,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemv_pair_kernel(GemvArgs a)
                 float v = row[i];
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0 && TCQ_IN_BOUNDS(r0 + i, a.rows)) a.y[r0 + i] = v;
+                if (lane == 0 && TCQ_IN_BOUNDS(r0 + i, a.rows)) IO::store(a, r0 + i, v);
                 row[i] = 0.f;
             }
         };
@@ -802,64 +838,64 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemv_pair_kernel(GemvArgs a)
 
 }
 
-cudaError_t launch_gemv_pair(const GemvArgs& a, int num_sms, cudaStream_t stream, bool mad)
+template <typename IO>
+cudaError_t launch_gemv_pair(const typename IO::Args& a, int num_sms, cudaStream_t stream, bool mad)
 {
     const size_t tab = mad ? 0 : ((size_t)1 << 16) * 2;
     // x padded, then phase B's two floats per stream word of a row (cols / 16 words)
     const size_t smem = tab + (size_t)(a.cols + (a.cols / 128) * 4) * 4 + (size_t)(a.cols / 16) * 2 * 4;
     int grid = num_sms;  // one CTA of 16 warps per SM
     const bool three = a.rows >= (long long)kPairRowsMax * grid * kPairWarps;
-    const void* fn = mad ? (three ? reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeMad, 3>)
-                                  : reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeMad, 1>))
-                         : (three ? reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeF16, 3>)
-                                  : reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeF16, 1>));
+    const void* fn = mad ? (three ? reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeMad, 3, IO>)
+                                  : reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeMad, 1, IO>))
+                         : (three ? reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeF16, 3, IO>)
+                                  : reinterpret_cast<const void*>(&gemv_pair_kernel<kCodeF16, 1, IO>));
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (mad && three)
-        gemv_pair_kernel<kCodeMad, 3><<<grid, kPairThreads, smem, stream>>>(a);
+        gemv_pair_kernel<kCodeMad, 3, IO><<<grid, kPairThreads, smem, stream>>>(a);
     else if (mad)
-        gemv_pair_kernel<kCodeMad, 1><<<grid, kPairThreads, smem, stream>>>(a);
+        gemv_pair_kernel<kCodeMad, 1, IO><<<grid, kPairThreads, smem, stream>>>(a);
     else if (three)
-        gemv_pair_kernel<kCodeF16, 3><<<grid, kPairThreads, smem, stream>>>(a);
+        gemv_pair_kernel<kCodeF16, 3, IO><<<grid, kPairThreads, smem, stream>>>(a);
     else
-        gemv_pair_kernel<kCodeF16, 1><<<grid, kPairThreads, smem, stream>>>(a);
+        gemv_pair_kernel<kCodeF16, 1, IO><<<grid, kPairThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
-template <int L, int K, int N, int T, int CODE>
-cudaError_t launch_gemv_rows(const GemvArgs& a, int grid, cudaStream_t stream)
+template <int L, int K, int N, int T, int CODE, typename IO>
+cudaError_t launch_gemv_rows(const typename IO::Args& a, int grid, cudaStream_t stream)
 {
     const size_t tab = CODE == kCodeMad ? 0 : (((size_t)1 << L) * (CODE == kCodeF16 ? 2 : 4) + 15) & ~(size_t)15;
     const size_t smem = tab + (size_t)a.cols * 4;
-    cudaError_t e = cudaFuncSetAttribute(gemv_rows_kernel<L, K, N, T, CODE>,
+    cudaError_t e = cudaFuncSetAttribute(gemv_rows_kernel<L, K, N, T, CODE, IO>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    gemv_rows_kernel<L, K, N, T, CODE><<<grid, kMadRowsThreads, smem, stream>>>(a);
+    gemv_rows_kernel<L, K, N, T, CODE, IO><<<grid, kMadRowsThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int L, int K, int N, int CODE, bool XSMEM>
-cudaError_t launch_gemv_fast_t(const GemvArgs& a, int grid, size_t smem, cudaStream_t stream)
+template <int L, int K, int N, int CODE, bool XSMEM, typename IO>
+cudaError_t launch_gemv_fast_t(const typename IO::Args& a, int grid, size_t smem, cudaStream_t stream)
 {
-    cudaError_t e = cudaFuncSetAttribute(gemv_fast_kernel<L, K, N, CODE, XSMEM>,
+    cudaError_t e = cudaFuncSetAttribute(gemv_fast_kernel<L, K, N, CODE, XSMEM, IO>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    gemv_fast_kernel<L, K, N, CODE, XSMEM><<<grid, kGemvThreads, smem, stream>>>(a);
+    gemv_fast_kernel<L, K, N, CODE, XSMEM, IO><<<grid, kGemvThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <int CODE, bool XSMEM>
-cudaError_t launch_gemv_t(const GemvArgs& a, int grid, size_t smem, cudaStream_t stream)
+template <int CODE, bool XSMEM, typename IO>
+cudaError_t launch_gemv_t(const typename IO::Args& a, int grid, size_t smem, cudaStream_t stream)
 {
-    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<CODE, XSMEM>,
+    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<CODE, XSMEM, IO>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    gemv_kernel<CODE, XSMEM><<<grid, kGemvThreads, smem, stream>>>(a);
+    gemv_kernel<CODE, XSMEM, IO><<<grid, kGemvThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream)
+template <typename IO>
+cudaError_t launch_gemv_as(const typename IO::Args& a, int num_sms, cudaStream_t stream)
 {
     const size_t entries = (size_t)1 << a.L;
     const bool mad = a.cb_f16 == kMadCodebook;
@@ -881,11 +917,11 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream)
         (reinterpret_cast<uintptr_t>(a.bits) & 15) == 0 &&
         (code == kCodeMad || (reinterpret_cast<uintptr_t>(a.cb) & 15) == 0) &&
         (code == kCodeMad ? 0 : 131072) + (size_t)(a.cols + a.cols / 32) * 4 + (size_t)(a.cols / 8) * 4 <= 220 * 1024)
-        return launch_gemv_pair(a, num_sms, stream, code == kCodeMad);
+        return launch_gemv_pair<IO>(a, num_sms, stream, code == kCodeMad);
     // T = 256: whole rows per warp, constant per-lane offsets
     const bool rows_ok = xsmem && a.T == 256 && (a.cols / 256) % kMadRowsChunk == 0;
 #define TCQ_GEMV_ROWS(LL, KK, NN, CC) \
-    if (rows_ok && a.L == LL && a.K == KK && code == CC) return launch_gemv_rows<LL, KK, NN, 256, CC>(a, (int)grid, stream);
+    if (rows_ok && a.L == LL && a.K == KK && code == CC) return launch_gemv_rows<LL, KK, NN, 256, CC, IO>(a, (int)grid, stream);
     TCQ_GEMV_ROWS(16, 2, 8, kCodeMad)
     TCQ_GEMV_ROWS(16, 3, 4, kCodeMad)
     TCQ_GEMV_ROWS(16, 2, 8, kCodeF16)
@@ -895,8 +931,8 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream)
     // specialised (L, k): compile-time shifts and masks, 8 or 4 weights per item
 #define TCQ_GEMV_FAST(LL, KK, NN, CC)                                                         \
     if (a.L == LL && a.K == KK && code == CC && a.T % NN == 0)                                 \
-        return xsmem ? launch_gemv_fast_t<LL, KK, NN, CC, true>(a, (int)grid, smem, stream) \
-                     : launch_gemv_fast_t<LL, KK, NN, CC, false>(a, (int)grid, smem, stream);
+        return xsmem ? launch_gemv_fast_t<LL, KK, NN, CC, true, IO>(a, (int)grid, smem, stream) \
+                     : launch_gemv_fast_t<LL, KK, NN, CC, false, IO>(a, (int)grid, smem, stream);
     TCQ_GEMV_FAST(16, 2, 8, kCodeF16)
     TCQ_GEMV_FAST(16, 3, 4, kCodeF16)
     TCQ_GEMV_FAST(12, 2, 8, kCodeF32)
@@ -905,13 +941,26 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream)
     TCQ_GEMV_FAST(16, 3, 4, kCodeMad)
 #undef TCQ_GEMV_FAST
     if (mad)
-        return xsmem ? launch_gemv_t<kCodeMad, true>(a, (int)grid, smem, stream)
-                     : launch_gemv_t<kCodeMad, false>(a, (int)grid, smem, stream);
+        return xsmem ? launch_gemv_t<kCodeMad, true, IO>(a, (int)grid, smem, stream)
+                     : launch_gemv_t<kCodeMad, false, IO>(a, (int)grid, smem, stream);
     if (cb16)
-        return xsmem ? launch_gemv_t<kCodeF16, true>(a, (int)grid, smem, stream)
-                     : launch_gemv_t<kCodeF16, false>(a, (int)grid, smem, stream);
-    return xsmem ? launch_gemv_t<kCodeF32, true>(a, (int)grid, smem, stream)
-                 : launch_gemv_t<kCodeF32, false>(a, (int)grid, smem, stream);
+        return xsmem ? launch_gemv_t<kCodeF16, true, IO>(a, (int)grid, smem, stream)
+                     : launch_gemv_t<kCodeF16, false, IO>(a, (int)grid, smem, stream);
+    return xsmem ? launch_gemv_t<kCodeF32, true, IO>(a, (int)grid, smem, stream)
+                 : launch_gemv_t<kCodeF32, false, IO>(a, (int)grid, smem, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream)
+{
+    return launch_gemv_as<VectorF32>(a, num_sms, stream);
+}
+
+cudaError_t launch_gemv_layer(const GemvLayerArgs& a, int xdtype, int num_sms, cudaStream_t stream)
+{
+    return xdtype == TCQ_X_BF16 ? launch_gemv_as<VectorLayer<TCQ_X_BF16>>(a, num_sms, stream)
+                                : launch_gemv_as<VectorLayer<TCQ_X_F16>>(a, num_sms, stream);
 }
 
 }  // namespace tcq

@@ -774,10 +774,13 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
         zf = _check_packed(checkpoint, n, rows, dev, "checkpoint")
         zc, zs = checkpoint.codes.data_ptr(), checkpoint.scales.data_ptr()
     cb = cb_dtype_of(codebook)
-    ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_workspace_bytes, L, k, T, rows, cols, n, cb), x, "gemm")
+    wp, wb = None, 0
+    if n != 1 or zc is not None:
+        ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_workspace_bytes, L, k, T, rows, cols, n, cb), x, "gemm")
+        wp, wb = ws.data_ptr(), ws.numel()
     _launch("tcq_gemm", dev, stream, lib.tcq_gemm, bits.data_ptr(), start_state.data_ptr(), _addr(scale),
             _addr(codebook), cb, L, k, T, rows, cols, x.data_ptr(), xt, _ld(x), n, _addr(bias), a, _addr(residual),
-            ldr, out.data_ptr(), _ld(out), zc, zs, zf, ws.data_ptr(), ws.numel())
+            ldr, out.data_ptr(), _ld(out), zc, zs, zf, wp, wb)
     return out
 
 
