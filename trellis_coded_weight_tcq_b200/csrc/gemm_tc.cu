@@ -341,37 +341,34 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         int done = 0;
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
-            const long long r0 = (long long)(t % p.m_tiles) * kTile + rank * 128 + quarter * 32, r = r0 + lane;
-            const long long n0 = (long long)(t / p.m_tiles) * kTile;
             if constexpr (KIND == kGemmWgrad) {
                 const int half = (warp - 4) >> 2;
                 unsigned char* box = S.box[warp - 4];
                 float sum[128];
+#pragma unroll
+                for (int i = 0; i < 128; ++i) sum[i] = 0.f;
                 for (int k0 = 0; k0 < p.k_steps && ok; k0 += segment, ++done) {
                     const int acc = done & 1;
                     ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float v[16];
-                        tmem_load16(lanes + acc * 256 + 128 * half + 16 * j, v);
-                        if (k0 == 0) {
+                    for (int j = 0; j < 16; ++j) {  // eight at a time: registers are full
+                        float v[8];
+                        tmem_load8(lanes + acc * 256 + 128 * half + 8 * j, v);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[16 * j + i] = v[i];
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[16 * j + i] += v[i];
-                        }
+                        for (int i = 0; i < 8; ++i) sum[8 * j + i] += v[i];
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_addr(&S.tempty[acc]), 0));
                 }
                 if (!ok) break;
+                const int r0 = (t % p.m_tiles) * kTile + (int)rank * 128 + quarter * 32;
+                const int c0 = (t / p.m_tiles) * kTile + 128 * half;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const long long c = n0 + 128 * half + 32 * j;
+                    const int c = c0 + 32 * j;
                     if (c >= p.n || r0 >= p.m) break;  // the same in every lane
                     if (tma_out) {
                         if (lane == 0) bulk_wait_read<0>();
@@ -385,19 +382,21 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         __syncwarp();
                         if (lane == 0) {
                             if (e.accumulate)
-                                tma_add_2d(&map_out, smem_addr(box), (int)c, (int)r0);
+                                tma_add_2d(&map_out, smem_addr(box), c, r0);
                             else
-                                tma_store_2d(&map_out, smem_addr(box), (int)c, (int)r0);
+                                tma_store_2d(&map_out, smem_addr(box), c, r0);
                             bulk_commit();
                         }
-                    } else if (r < p.m) {
-                        float* o = static_cast<float*>(e.out) + r * e.ldo + c;
+                    } else if (r0 + lane < p.m) {
+                        float* o = static_cast<float*>(e.out) + (long long)(r0 + lane) * e.ldo + c;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (c + i < p.n) o[i] = e.accumulate ? o[i] + sum[32 * j + i] : sum[32 * j + i];
                     }
                 }
             } else {
+                const long long r0 = (long long)(t % p.m_tiles) * kTile + rank * 128 + quarter * 32, r = r0 + lane;
+                const long long n0 = (long long)(t / p.m_tiles) * kTile;
                 const int acc = done & 1;
                 if constexpr (KIND == kGemmForward) {
                     // this tile's columns, while its product still runs

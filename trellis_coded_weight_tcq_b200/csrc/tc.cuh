@@ -10,7 +10,7 @@
 
 namespace tcq {
 
-constexpr long long kWaitLimit = 1ll << 26;
+constexpr int kWaitLimit = 1 << 26;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p)
 {
@@ -66,7 +66,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 // Waits for the phase of this parity to complete.  `stop` is the CTA's stop flag.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop, unsigned int* err)
 {
-    for (long long i = 0; i < kWaitLimit; ++i) {
+    for (int i = 0; i < kWaitLimit; ++i) {
         if (mbar_try(bar, parity)) return true;
         if ((i & 255) == 255 && *stop) return false;
     }
@@ -78,7 +78,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // Waits for a shared-memory counter that only grows.
 __device__ __forceinline__ bool wait_count(const volatile int* count, int least, volatile int* stop, unsigned int* err)
 {
-    for (long long i = 0; i < kWaitLimit; ++i) {
+    for (int i = 0; i < kWaitLimit; ++i) {
         if (*count >= least) return true;
         if ((i & 255) == 255 && *stop) return false;
     }
@@ -90,7 +90,7 @@ __device__ __forceinline__ bool wait_count(const volatile int* count, int least,
 // The same as mbar_wait without the stop flag: what was issued before a stop is still waited for.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
 {
-    for (long long i = 0; i < kWaitLimit; ++i)
+    for (int i = 0; i < kWaitLimit; ++i)
         if (mbar_try(bar, parity)) return;
 }
 
@@ -269,6 +269,20 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16])
                  ::"memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same for 8 columns.
+__device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 ::"memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // ---- host
