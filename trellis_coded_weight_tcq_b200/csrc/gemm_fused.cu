@@ -183,6 +183,16 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
             const long long s1 = (seg_tile + 1) * p.steps < u1 ? (seg_tile + 1) * p.steps : u1;
             for (; u < s1; u += 2) {
                 const int it = 2 * (int)(u - u0);  // the unit's first stage
+                // Where the unit's stages go.  A barrier's parity tells two neighbouring phases
+                // apart.  With four or more stages the wait one turn ago puts this one's
+                // phase next; with two, the group must first see the other group's fill.
+                // The slot is usually free by now: asked here, the answer is there after the
+                // decoding, while an answer waited for takes hundreds of cycles in the queue
+                // of the look-ups.
+                const int step = (it + half) / p.per, sub = (it + half) % p.per;
+                const int slot = step % p.slots, round = step / p.slots;
+                const uint32_t empty = smem_addr(&B.empty[slot]);
+                const bool ready = p.per == 2 && mbar_test(empty, (round & 1) ^ 1);
                 uint32_t nwords[2 * K], nprev;
                 float nsc, npw;
                 int nc0 = 0;
@@ -196,15 +206,12 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                 const uint32_t before = half && c0 != j0 * T ? other : prev;
                 uint32_t v[32];
                 decode_64<K, CODE>(words, before, mask, sm, sc * inverse_pow2(pw), v);
-                // A barrier's parity tells two neighbouring phases apart.  With four or more
-                // stages the wait one turn ago puts this one's phase next; with two, the
-                // group must first see the other group's fill.
-                const int step = (it + half) / p.per, sub = (it + half) % p.per;
-                const int slot = step % p.slots, round = step / p.slots;
-                if (p.per == 1) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
-                ok = ok && mbar_wait(smem_addr(&B.empty[slot]), (round & 1) ^ 1, stop, err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                if (!__all_sync(0xffffffffu, ready)) {
+                    if (p.per == 1) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
+                    ok = ok && mbar_wait(empty, (round & 1) ^ 1, stop, err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
                 unsigned char* a = ring + (size_t)slot * sbytes + sub * kABytes + r * 128;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -274,6 +281,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
     } else {
         if (lane == 0) {
             const uint32_t idesc = mma_idesc(kRows, p.np, 0, 0, 0);
+            const unsigned long long desc0 = smem_desc_sw128(smem_addr(ring), 16);
             bool ok = true;
             int done = 0;
             for (long long s0 = u0; s0 < u1 && ok; ++done) {
@@ -289,12 +297,13 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                     ok = mbar_wait(smem_addr(&B.full[slot]), (i / p.slots) & 1, stop, err);
                     if (!ok) break;
                     tc_fence_after();
-                    uint32_t a = smem_addr(ring + (size_t)slot * sbytes), b = a + p.per * kABytes;
-                    for (int h = 0; h < p.per; ++h, a += kABytes, b += bbytes) {
+                    // descriptors count in 16 bytes
+                    unsigned long long a = desc0 + (unsigned)(slot * sbytes >> 4), b = a + (unsigned)(p.per * kABytes >> 4);
+                    for (int h = 0; h < p.per; ++h, a += kABytes >> 4, b += (unsigned)(bbytes >> 4)) {
 #pragma unroll
                         for (int j = 0; j < kDepth / 16; ++j)
-                            mma_f16<1>(tmem + acc * acc_columns, smem_desc_sw128(a + 32 * j, 16),
-                                       smem_desc_sw128(b + 32 * j, 16), idesc, i != first || h != 0 || j != 0);
+                            mma_f16<1>(tmem + acc * acc_columns, a + 2 * j, b + 2 * j, idesc,
+                                       i != first || h != 0 || j != 0);
                     }
                     mma_commit<1>(smem_addr(&B.empty[slot]));
                 }

@@ -404,11 +404,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     for (int i = threadIdx.x - 128; i < kTile; i += 128) {
                         const long long c = n0 + i;
                         S.cols[i] = make_float2(e.col_scale && c < p.n ? __ldg(e.col_scale + c) : 1.f,
-                                                     e.bias && c < p.n ? __ldg(e.bias + c) : 0.f);
+                                                e.bias && c < p.n ? __ldg(e.bias + c) : 0.f);
                     }
-                    named_barrier(1, 128);
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
+                // the columns are there; after a wait that gave up all warps stop together, or
+                // the others would wait at the next barrier
+                if constexpr (KIND == kGemmForward) ok = named_all(1, 128, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const float row_scale = e.row_scale && r < p.m ? __ldg(e.row_scale + r) : 1.f;

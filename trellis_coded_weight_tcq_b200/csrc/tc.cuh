@@ -63,6 +63,16 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
+// Whether it has, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.b32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
 // Waits for the phase of this parity to complete.  `stop` is the CTA's stop flag.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop, unsigned int* err)
 {
@@ -92,6 +102,16 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
 {
     for (int i = 0; i < kWaitLimit; ++i)
         if (mbar_try(bar, parity)) return;
+}
+
+// Named barrier over `count` threads that also tells whether the flag is set in all.
+__device__ __forceinline__ bool named_all(int id, int count, bool flag)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %3, 0;\n\tbarrier.cta.red.and.aligned.pred p, %1, %2, q;\n\t"
+                 "selp.b32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"(id), "r"(count), "r"((uint32_t)flag) : "memory");
+    return r != 0;
 }
 
 // ---- clusters
