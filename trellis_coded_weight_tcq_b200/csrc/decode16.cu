@@ -9,9 +9,9 @@
 // computed codeword is stored as it is.
 //
 // A warp takes 256 columns of a row at a time, eight per lane: their windows lie in
-// two stream words, one 16-byte store per lane; each warp has a contiguous run.  Table lookups at random
-// shared-memory addresses bound it (as in the decoder), then the 2 bytes per weight
-// written.
+// two stream words, one 16-byte store per lane; each warp has a contiguous run.  Table
+// lookups at random shared-memory addresses bound it (as in the decoder, about 3.6 bank
+// passes per 32), then the 2 bytes per weight written.
 #include "codes.cuh"
 #include "decode16.cuh"
 #include "gemm.cuh"
@@ -25,30 +25,93 @@ constexpr int kThreads = 768;  // leaves registers for the pass over the activat
 constexpr int kUnit = 256;  // columns per warp step
 constexpr int kAhead = 4;   // steps whose words are loaded together
 
-// Powers of two of the rows: one warp per row over its scales.
-__global__ void __launch_bounds__(256) row_pow2_kernel(const float* scale, long long rows, long long nb, float* row_pow2)
+// Blocks of whole 32s: a row's stream words follow one another without gaps, so a lane's
+// words lie 8 k apart from unit to unit and its window offset never changes.  The next
+// four units' words load while the current four are decoded.
+template <int K, int CODE>
+__global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix w, uint16_t* out, long long ldw,
+                                                                    const float* row_pow2)
 {
-    pdl_release();
-    const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    uint32_t top = 0u;
-    for (long long j = threadIdx.x & 31; j < nb; j += 32) top = max(top, finite_magnitude(__ldg(scale + r * nb + j)));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) row_pow2[r] = pow2_clamped(power_above(top));
+    extern __shared__ __align__(16) unsigned char sm[];
+    stage_table<CODE>(sm, w.cb, w.cb_f16, w.L);
+    pdl_wait();     // row_pow2
+    pdl_release();  // the pass over the activations may run beside this one (and read row_pow2)
+    const int lane = threadIdx.x & 31;
+    const int cols = (int)w.cols, T = w.T, nb = cols / T;
+    const int upr = (cols + kUnit - 1) / kUnit;
+    const long long units = upr * w.rows;
+    const long long nwarps = ((long long)gridDim.x * blockDim.x) >> 5;
+    const long long me = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const uint32_t mask = (1u << w.L) - 1u;
+    const int tshift = (T & (T - 1)) == 0 ? __ffs(T) - 1 : -1;
+    const long long u0 = units * me / nwarps;
+    int left = (int)(units * (me + 1) / nwarps - u0);
+    long long row = u0 / upr;
+    int at = (int)(u0 - row * upr);
+    const int word = ((8 * lane + 8) * K - 1) >> 5;  // the last window's word in a unit
+    const int down = bits_behind((8 * lane + 8) * K);
+    __syncthreads();
+    struct Four {
+        uint32_t hi[kAhead], lo[kAhead];
+        float sc[kAhead];
+    };
+    // units at .. at + kAhead - 1 of a row
+    auto fetch = [&](Four& f, long long r, int a) {
+        const uint32_t* p = w.bits + r * (cols / 32 * K) + word;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = (a + i) * kUnit + 8 * lane;
+            f.hi[i] = f.lo[i] = 0u;
+            f.sc[i] = 0.f;
+            if (c < cols && TCQ_IN_BOUNDS(r * (cols / 32 * K) + word + (a + i) * 8 * K, w.rows * (cols / 32 * K))) {
+                const int j = tshift >= 0 ? c >> tshift : (int)((unsigned)c / (unsigned)T);
+                const int e = (a + i) * 8 * K;
+                f.lo[i] = __ldg(p + e);
+                f.hi[i] = __ldg((c - j * T + 8) * K > 32 ? p + e - 1 : w.start_state + r * nb + j);
+                f.sc[i] = w.scale ? __ldg(w.scale + r * nb + j) : 1.f;
+            }
+        }
+    };
+    Four cur, nxt;
+    if (left > 0) fetch(cur, row, at);
+    while (left > 0) {  // the same in every lane
+        int n = upr - at < kAhead ? upr - at : kAhead;
+        if (n > left) n = left;
+        const long long r = row;
+        const int a = at;
+        at += n;
+        left -= n;
+        if (at == upr) {
+            at = 0;
+            ++row;
+        }
+        if (left > 0) fetch(nxt, row, at);
+        const float inv = w.scale ? inverse_pow2(__ldg(row_pow2 + r)) : 1.f;
+        uint16_t* dst = out + r * ldw + a * kUnit + 8 * lane;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (i >= n) break;
+            uint32_t v[4];
+            decode_weights<K, 8, CODE>(cur.hi[i], cur.lo[i], down, mask, sm, cur.sc[i] * inv, v);
+            // ldw is cols rounded up to 8: a lane's eight columns are all stored or none is
+            if ((a + i) * kUnit + 8 * lane < cols && TCQ_IN_BOUNDS(dst - out + i * kUnit + 7, w.rows * ldw))
+                *reinterpret_cast<uint4*>(dst + i * kUnit) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        cur = nxt;
+    }
 }
 
-// N = 8: blocks of whole eights; 4: any block of whole quads (two reads per lane).
-// T32: T is a multiple of 32, so that a row's stream words follow one another without
-// gaps and a lane's word index needs no division.
-template <int K, int CODE, int N, bool T32>
+// Any block of whole quads; N = 8: whole eights, 4: two reads per lane.
+template <int K, int CODE, int N>
 __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, uint16_t* out, long long ldw,
                                                                const float* row_pow2)
 {
     constexpr int H = 8 / N;  // reads per lane and unit
     extern __shared__ __align__(16) unsigned char sm[];
     stage_table<CODE>(sm, w.cb, w.cb_f16, w.L);
-    pdl_wait();     // row_pow2
-    pdl_release();  // the pass over the activations may run beside this one (and read row_pow2)
+    pdl_wait();
+    pdl_release();
+    __syncthreads();
     const int lane = threadIdx.x & 31;
     const int cols = (int)w.cols, T = w.T, W = w.W, nb = cols / T;
     const int upr = (cols + kUnit - 1) / kUnit;
@@ -56,89 +119,57 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
     const long long nwarps = ((long long)gridDim.x * blockDim.x) >> 5;
     const long long me = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const uint32_t mask = (1u << w.L) - 1u;
-    const int tshift = (T & (T - 1)) == 0 ? __ffs(T) - 1 : -1;
-    // contiguous runs of units; (row, unit in the row) advance without divisions
-    const long long u1 = units * (me + 1) / nwarps;
-    long long u = units * me / nwarps;
-    long long row = u / upr;
-    int at = (int)(u - row * upr);
-    const uint32_t* bits = w.bits + row * nb * W;
-    const uint32_t* start = w.start_state + row * nb;
-    const float* scale = w.scale ? w.scale + row * nb : nullptr;
-    uint16_t* dst = out + row * ldw;
-    float inv = scale && u < u1 ? inverse_pow2(__ldg(row_pow2 + row)) : 1.f;
-    int left = (int)(u1 - u);
-    __syncthreads();
-    while (left > 0) {
-        uint32_t hi[kAhead][H], lo[kAhead][H];
-        float sc[kAhead][H];
-        int down[kAhead][H];
-        uint16_t* to[kAhead];
-        const int n = left < kAhead ? left : kAhead;
+    const long long u0 = units * me / nwarps, u1 = units * (me + 1) / nwarps;
+    long long row = u0 / upr;
+    int at = (int)(u0 - row * upr);
+    for (long long u = u0; u < u1; ++u) {
+        const float inv = w.scale ? inverse_pow2(__ldg(row_pow2 + row)) : 1.f;
+        const int c = at * kUnit + 8 * lane;
+        uint32_t v[4];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (i < n) {  // the same in every lane
-                const int c = at * kUnit + 8 * lane;
-                to[i] = c < cols ? dst + c : nullptr;
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const int ch = c + N * h;
-                    hi[i][h] = lo[i][h] = 0u;
-                    sc[i][h] = 0.f;
-                    down[i][h] = 0;
-                    if (ch < cols) {
-                        const int j = tshift >= 0 ? ch >> tshift : (int)((unsigned)ch / (unsigned)T);
-                        const int end = (ch - j * T + N) * K;  // of the last window, in the block's stream
-                        const int e = T32 ? (int)(((long long)(ch + N) * K - 1) >> 5) : j * W + ((end - 1) >> 5);
-                        down[i][h] = bits_behind(end);
-                        if (TCQ_IN_BOUNDS((bits - w.bits) + e, w.rows * nb * W)) {
-                            hi[i][h] = __ldg(end > 32 ? bits + e - 1 : start + j);
-                            lo[i][h] = __ldg(bits + e);
-                            sc[i][h] = scale ? __ldg(scale + j) * inv : 1.f;
-                        }
-                    }
-                }
-                if (++at == upr) {
-                    at = 0;
-                    ++row;
-                    bits += nb * W;
-                    start += nb;
-                    dst += ldw;
-                    if (scale) {
-                        scale += nb;
-                        if (row < w.rows) inv = inverse_pow2(__ldg(row_pow2 + row));
-                    }
+        for (int h = 0; h < H; ++h) {
+            const int ch = c + N * h;
+            uint32_t hi = 0u, lo = 0u;
+            float sc = 0.f;
+            int down = 0;
+            if (ch < cols) {
+                const int j = (int)((unsigned)ch / (unsigned)T);
+                const long long b = row * nb + j;
+                const int end = (ch - j * T + N) * K;  // of the last window, in the block's stream
+                down = bits_behind(end);
+                if (TCQ_IN_BOUNDS(b, w.rows * nb)) {
+                    const uint32_t* p = w.bits + b * W + ((end - 1) >> 5);
+                    lo = __ldg(p);
+                    hi = __ldg(end > 32 ? p - 1 : w.start_state + b);
+                    sc = w.scale ? __ldg(w.scale + b) * inv : 1.f;
                 }
             }
+            decode_weights<K, N, CODE>(hi, lo, down, mask, sm, sc, v + N / 2 * h);
         }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (i >= n) break;
-            uint32_t v[4];
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-                decode_weights<K, N, CODE>(hi[i][h], lo[i][h], down[i][h], mask, sm, sc[i][h], v + N / 2 * h);
-            // ldw is cols rounded up to 8: a lane's eight columns are all stored (those
-            // behind the last are padding that nothing reads) or none is
-            if (to[i] && TCQ_IN_BOUNDS(to[i] - out + 7, w.rows * ldw))
-                *reinterpret_cast<uint4*>(to[i]) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (c < cols && TCQ_IN_BOUNDS(row * ldw + c + 7, w.rows * ldw))
+            *reinterpret_cast<uint4*>(out + row * ldw + c) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (++at == upr) {
+            at = 0;
+            ++row;
         }
-        left -= n;
     }
 }
 
-template <int K, int CODE, int N, bool T32>
+template <int K, int CODE>
 cudaError_t launch(const CodedMatrix& w, void* out, long long ldw, const float* row_pow2, int num_sms,
                    cudaStream_t stream)
 {
+    typedef void (*Kernel)(CodedMatrix, uint16_t*, long long, const float*);
+    const Kernel kernel = w.T % 32 == 0  ? Kernel(decode16_rows_kernel<K, CODE>)
+                          : w.T % 8 == 0 ? Kernel(decode16_kernel<K, CODE, 8>)
+                                         : Kernel(decode16_kernel<K, CODE, 4>);
     const size_t smem = table_bytes(CODE, w.L);
-    cudaError_t e = cudaFuncSetAttribute(decode16_kernel<K, CODE, N, T32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long units = (w.cols + kUnit - 1) / kUnit * w.rows;
     const long long need = (units + kThreads / 32 - 1) / (kThreads / 32);
     const int grid = (int)(need < num_sms ? need : num_sms);
-    return launch_pdl(decode16_kernel<K, CODE, N, T32>, dim3(grid), dim3(kThreads), smem, stream, w.scale != nullptr, w,
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, w.scale != nullptr, w,
                       static_cast<uint16_t*>(out), ldw, row_pow2);
 }
 
@@ -146,34 +177,21 @@ template <int CODE>
 cudaError_t launch_k(const CodedMatrix& w, void* out, long long ldw, const float* row_pow2, int num_sms,
                      cudaStream_t stream)
 {
-#define TCQ_DECODE16(KK)                                                                     \
-    case KK:                                                                                 \
-        return w.T % 32 == 0  ? launch<KK, CODE, 8, true>(w, out, ldw, row_pow2, num_sms, stream)  \
-               : w.T % 8 == 0 ? launch<KK, CODE, 8, false>(w, out, ldw, row_pow2, num_sms, stream) \
-                              : launch<KK, CODE, 4, false>(w, out, ldw, row_pow2, num_sms, stream);
     switch (w.K) {
-        TCQ_DECODE16(1)
-        TCQ_DECODE16(2)
-        TCQ_DECODE16(3)
-        TCQ_DECODE16(4)
-    default: return cudaErrorInvalidValue;
+    case 1: return launch<1, CODE>(w, out, ldw, row_pow2, num_sms, stream);
+    case 2: return launch<2, CODE>(w, out, ldw, row_pow2, num_sms, stream);
+    case 3: return launch<3, CODE>(w, out, ldw, row_pow2, num_sms, stream);
+    default: return launch<4, CODE>(w, out, ldw, row_pow2, num_sms, stream);
     }
-#undef TCQ_DECODE16
 }
 
 }  // namespace
-
-cudaError_t launch_row_pow2(const CodedMatrix& w, float* row_pow2, cudaStream_t stream)
-{
-    row_pow2_kernel<<<(unsigned)((w.rows + 7) / 8), 256, 0, stream>>>(w.scale, w.rows, w.cols / w.T, row_pow2);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, int num_sms,
                             cudaStream_t stream)
 {
     if (w.scale) {
-        const cudaError_t e = launch_row_pow2(w, row_pow2, stream);
+        const cudaError_t e = launch_prepare({}, {w.scale, w.rows, (int)(w.cols / w.T), row_pow2}, stream);
         if (e != cudaSuccess) return e;
     }
     switch (w.cb_f16) {

@@ -67,13 +67,34 @@ cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& 
 cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, int num_sms,
                             cudaStream_t stream);
 
-// x [n, cols] as binary16 rows over a power of two each (row_pow2[n]); col_pow2
-// (or nullptr) multiplies the columns first.  `early`: the launch before it in the
-// stream is one of this call's (launch_decode16, launch_row_pow2), which it may run
-// beside; col_pow2 may then be the row powers that launch_decode16 read.
-cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long long n, long long cols,
-                              const float* col_pow2, void* out, long long ldo, float* row_pow2, bool early,
-                              cudaStream_t stream);
+// x [n, cols] as binary16 rows over a power of two each (row_pow2[n]); col_pow2 (or
+// nullptr) multiplies the columns first.  `early`: the launch before it in the stream is
+// one of this call's (launch_decode16), which it may run beside; col_pow2 may then be the
+// row powers that launch_decode16 read.
+struct ScaleRows {
+    const void* x = nullptr;
+    int xdtype = TCQ_X_F16;
+    long long ldx = 0, n = 0, cols = 0;
+    const float* col_pow2 = nullptr;
+    void* out = nullptr;
+    long long ldo = 0;
+    float* row_pow2 = nullptr;
+    bool early = false;
+    bool vec = false;  // set by the launch: rows that 16-byte loads can read
+};
+
+// out[r] for the rows of a coded matrix, per_row scales each: the least power of two
+// above the largest finite |scale|.
+struct RowPowers {
+    const float* scale = nullptr;
+    long long rows = 0;
+    int per_row = 0;
+    float* out = nullptr;
+};
+
+// Either or both (n == 0 or rows == 0: not wanted), in one launch.
+cudaError_t launch_prepare(ScaleRows a, RowPowers p, cudaStream_t stream);
+
 // 16-bit rows copied to another stride.
 cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
                           int num_sms, cudaStream_t stream);
@@ -87,9 +108,6 @@ size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, lo
 cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx, long long n, int xdtype,
                               const float* row_pow2, float* partial, const Epilogue& e, int num_sms, unsigned int* err,
                               bool early, cudaStream_t stream);
-
-// The powers of two of W's rows (launch_decode16 includes it).
-cudaError_t launch_row_pow2(const CodedMatrix& w, float* row_pow2, cudaStream_t stream);
 
 cudaError_t launch_pack8(const void* x, int xdtype, long long ldx, long long n, long long cols, int format,
                          uint8_t* codes, uint8_t* scales, int num_sms, cudaStream_t stream);

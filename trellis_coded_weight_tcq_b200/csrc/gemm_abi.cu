@@ -156,21 +156,35 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     const int64_t ldw = round_up(cols, 8);
 
     const bool fused = fused_shape(T, rows, cols, n);
-    cudaError_t e = !fused  ? launch_decode16(w, ws, ldw, row_pow2, num_sms, st)
-                    : scale ? launch_row_pow2(w, row_pow2, st)
-                            : cudaSuccess;
-    if (e != cudaSuccess) return TCQ_ERR_CUDA;
     GemmProblem p = {x, ldx, ws, ldw, n, rows, cols, 0, xdtype};
     Epilogue ep = plain_epilogue(y, ldy);
     // binary16 rows that TMA can read are used where they are
     const bool scaled = xdtype != TCQ_X_F16 || !direct(x, ldx);
+    ScaleRows sx;
     if (scaled) {
-        e = launch_scale_rows(x, xdtype, ldx, n, cols, nullptr, ws + sp.x, ldw, x_pow2, !fused || scale, st);
-        if (e != cudaSuccess) return TCQ_ERR_CUDA;
+        sx.x = x;
+        sx.xdtype = xdtype;
+        sx.ldx = ldx;
+        sx.n = n;
+        sx.cols = cols;
+        sx.out = ws + sp.x;
+        sx.ldo = ldw;
+        sx.row_pow2 = x_pow2;
         p.a = ws + sp.x;
         p.lda = ldw;
         ep.row_scale = x_pow2;
     }
+    cudaError_t e = cudaSuccess;
+    if (fused) {
+        RowPowers rp;
+        if (scale) rp = {scale, rows, (int)(cols / T), row_pow2};
+        if (scaled || scale) e = launch_prepare(sx, rp, st);
+    } else {
+        e = launch_decode16(w, ws, ldw, row_pow2, num_sms, st);
+        sx.early = true;
+        if (e == cudaSuccess && scaled) e = launch_prepare(sx, {}, st);
+    }
+    if (e != cudaSuccess) return TCQ_ERR_CUDA;
     ep.col_scale = scale ? row_pow2 : nullptr;
     ep.bias = bias;
     ep.residual = residual;
@@ -225,8 +239,18 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
     // W's rows run along the reduction: their powers go with dZ's columns
     if (xdtype != TCQ_X_F16 || scale || !direct(dz, lddz)) {
         const int64_t ldz = round_up(rows, 8);
-        e = launch_scale_rows(dz, xdtype, lddz, n, rows, scale ? row_pow2 : nullptr, ws + sp.x, ldz, x_pow2, true,
-                              st);
+        ScaleRows sx;
+        sx.x = dz;
+        sx.xdtype = xdtype;
+        sx.ldx = lddz;
+        sx.n = n;
+        sx.cols = rows;
+        sx.col_pow2 = scale ? row_pow2 : nullptr;
+        sx.out = ws + sp.x;
+        sx.ldo = ldz;
+        sx.row_pow2 = x_pow2;
+        sx.early = true;
+        e = launch_prepare(sx, {}, st);
         if (e != cudaSuccess) return TCQ_ERR_CUDA;
         p.a = ws + sp.x;
         p.lda = ldz;

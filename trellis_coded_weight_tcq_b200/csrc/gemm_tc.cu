@@ -1,6 +1,5 @@
 // gemm_tc.cu -- the 16-bit matrix products of the batched layer on the
-// fifth-generation tensor cores, and the passes that bring their operands to
-// binary16 rows.
+// fifth-generation tensor cores.
 //
 // One kernel serves the three products; they differ in which operands run along
 // the reduction (the tensor core reads either order from 128-byte swizzled tiles)
@@ -28,8 +27,6 @@
 #include "gemm.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
-#include "decode16.cuh"
-#include "pdl.cuh"
 
 namespace tcq {
 
@@ -498,85 +495,6 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigne
     return cudaGetLastError();
 }
 
-// ---- operand passes
-// One CTA per row: the row's largest finite magnitude, then the row over the power of
-// two that brings it to [2^14, 2^15).  Memory bound (2 bytes read twice, the second
-// time from L2, and 2 written per element).  It starts while the matrix is decoded,
-// which is bound by shared-memory lookups: the two run side by side.
-constexpr int kRowThreads = 256;
-
-template <int XT>
-__global__ void __launch_bounds__(kRowThreads) scale_rows_kernel(const uint16_t* x, long long ldx, long long cols,
-                                                                 const float* col_pow2, uint16_t* out, long long ldo,
-                                                                 float* row_pow2, bool vec)
-{
-    __shared__ uint32_t part[kRowThreads / 32];
-    pdl_release();
-    const long long r = blockIdx.x;
-    const uint16_t* xr = x + r * ldx;
-    uint16_t* o = out + r * ldo;
-    uint32_t top = 0u;
-    auto eight = [&](long long c, float (&f)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(xr + c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const float2 t = x_unpack2<XT>(w[h]);
-            f[2 * h] = t.x;
-            f[2 * h + 1] = t.y;
-        }
-        if (col_pow2) {
-            const float4 p = *reinterpret_cast<const float4*>(col_pow2 + c);
-            const float4 q = *reinterpret_cast<const float4*>(col_pow2 + c + 4);
-            f[0] *= p.x; f[1] *= p.y; f[2] *= p.z; f[3] *= p.w;
-            f[4] *= q.x; f[5] *= q.y; f[6] *= q.z; f[7] *= q.w;
-        }
-    };
-    const long long vcols = vec ? cols / 8 * 8 : 0;
-    for (long long c = 8ll * threadIdx.x; c < vcols; c += 8 * kRowThreads) {
-        float f[8];
-        eight(c, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, finite_magnitude(f[i]));
-    }
-    for (long long c = vcols + threadIdx.x; c < cols; c += kRowThreads)
-        top = max(top, finite_magnitude(x_load<XT>(xr, c) * (col_pow2 ? col_pow2[c] : 1.f)));
-#pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRowThreads / 32; ++i) top = max(top, part[i]);
-    // |x| < 2^p; the factor stays in the normal range, so tiny rows end lower than 2^15
-    int p = 0;
-    if (top != 0u) p = power_above(top) - 15;
-    if (p < -126) p = -126;
-    const float inv = pow2_clamped(-p);
-    if (threadIdx.x == 0) row_pow2[r] = pow2_clamped(p);
-    for (long long c = 8ll * threadIdx.x; c < vcols; c += 8 * kRowThreads) {
-        float f[8];
-        eight(c, f);
-        uint32_t w[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) w[h] = x_pack2<TCQ_X_F16>(f[2 * h] * inv, f[2 * h + 1] * inv);
-        *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    for (long long c = vcols + threadIdx.x; c < cols; c += kRowThreads)
-        o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (col_pow2 ? col_pow2[c] : 1.f) * inv);
-    pdl_wait();  // ends after the decode that it ran beside
-}
-
-__global__ void __launch_bounds__(256) copy16_kernel(const uint16_t* x, long long ldx, long long n, long long cols,
-                                                     uint16_t* out, long long ldo)
-{
-    const long long total = n * cols;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-         i += (long long)gridDim.x * blockDim.x) {
-        const long long r = i / cols, c = i - r * cols;
-        out[r * ldo + c] = x[r * ldx + c];
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, int num_sms, unsigned int* err,
@@ -592,28 +510,6 @@ cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& 
                   : launch<kGemmDgrad, TCQ_X_F16>(p, e, num_sms, err, stream);
     default: return launch<kGemmWgrad, TCQ_X_F16>(p, e, num_sms, err, stream);
     }
-}
-
-cudaError_t launch_scale_rows(const void* x, int xdtype, long long ldx, long long n, long long cols,
-                              const float* col_pow2, void* out, long long ldo, float* row_pow2, bool early,
-                              cudaStream_t stream)
-{
-    const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && ldx % 8 == 0;
-    const uint16_t* xi = static_cast<const uint16_t*>(x);
-    uint16_t* o = static_cast<uint16_t*>(out);
-    return launch_pdl(xdtype == TCQ_X_BF16 ? scale_rows_kernel<TCQ_X_BF16> : scale_rows_kernel<TCQ_X_F16>,
-                      dim3((unsigned)n), dim3(kRowThreads), 0, stream, early, xi, ldx, cols, col_pow2, o, ldo, row_pow2,
-                      vec);
-}
-
-cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
-                          int num_sms, cudaStream_t stream)
-{
-    long long grid = (n * cols + 1023) / 1024;
-    if (grid > 16ll * num_sms) grid = 16ll * num_sms;
-    copy16_kernel<<<(int)grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x), ldx, n, cols,
-                                                 static_cast<uint16_t*>(out), ldo);
-    return cudaGetLastError();
 }
 
 }  // namespace tcq

@@ -1,0 +1,128 @@
+// operands.cu -- the passes that bring the activations of a product to binary16 rows,
+// and the powers of two of a coded matrix's rows.
+//
+// A bfloat16 row scaled by a power of two of its own is exact in binary16 down to
+// 2^-32 of its largest element (binary16 has three more bits, and 30 powers below the
+// largest before its subnormals begin to cut); binary16 keeps the weights exact where
+// bfloat16 would not.  The rows are read twice (the second time from L2) and written
+// once: bound by memory, about 4 bytes per element.
+#include "decode16.cuh"
+#include "gemm.cuh"
+#include "pdl.cuh"
+#include "q8.cuh"
+
+namespace tcq {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// The power of two above the largest finite |scale| of a row of W: one warp per row.
+__device__ __forceinline__ void row_power(const RowPowers& p, long long r)
+{
+    uint32_t top = 0u;
+    for (int j = threadIdx.x & 31; j < p.per_row; j += 32)
+        top = max(top, finite_magnitude(__ldg(p.scale + r * p.per_row + j)));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) p.out[r] = pow2_clamped(power_above(top));
+}
+
+// One CTA per row: the row's largest finite magnitude, then the row over the power of
+// two that brings it to [2^14, 2^15).
+template <int XT>
+__device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
+{
+    __shared__ uint32_t part[kThreads / 32];
+    const uint16_t* xr = static_cast<const uint16_t*>(a.x) + r * a.ldx;
+    uint16_t* o = static_cast<uint16_t*>(a.out) + r * a.ldo;
+    uint32_t top = 0u;
+    auto eight = [&](long long c, float (&f)[8]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(xr + c);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const float2 t = x_unpack2<XT>(w[h]);
+            f[2 * h] = t.x;
+            f[2 * h + 1] = t.y;
+        }
+        if (a.col_pow2) {
+            const float4 p = *reinterpret_cast<const float4*>(a.col_pow2 + c);
+            const float4 q = *reinterpret_cast<const float4*>(a.col_pow2 + c + 4);
+            f[0] *= p.x; f[1] *= p.y; f[2] *= p.z; f[3] *= p.w;
+            f[4] *= q.x; f[5] *= q.y; f[6] *= q.z; f[7] *= q.w;
+        }
+    };
+    const long long vcols = a.vec ? a.cols / 8 * 8 : 0;
+    for (long long c = 8ll * threadIdx.x; c < vcols; c += 8 * kThreads) {
+        float f[8];
+        eight(c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, finite_magnitude(f[i]));
+    }
+    for (long long c = vcols + threadIdx.x; c < a.cols; c += kThreads)
+        top = max(top, finite_magnitude(x_load<XT>(xr, c) * (a.col_pow2 ? a.col_pow2[c] : 1.f)));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) top = max(top, part[i]);
+    // |x| < 2^p; the factor stays in the normal range, so tiny rows end lower than 2^15
+    int p = 0;
+    if (top != 0u) p = power_above(top) - 15;
+    if (p < -126) p = -126;
+    const float inv = pow2_clamped(-p);
+    if (threadIdx.x == 0) a.row_pow2[r] = pow2_clamped(p);
+    for (long long c = 8ll * threadIdx.x; c < vcols; c += 8 * kThreads) {
+        float f[8];
+        eight(c, f);
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) w[h] = x_pack2<TCQ_X_F16>(f[2 * h] * inv, f[2 * h + 1] * inv);
+        *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    for (long long c = vcols + threadIdx.x; c < a.cols; c += kThreads)
+        o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (a.col_pow2 ? a.col_pow2[c] : 1.f) * inv);
+}
+
+// CTAs below a.n scale a row of activations each, the others take eight rows of W.
+template <int XT>
+__global__ void __launch_bounds__(kThreads) prepare_kernel(ScaleRows a, RowPowers p)
+{
+    pdl_release();
+    if (blockIdx.x < a.n) {
+        scale_row<XT>(a, blockIdx.x);
+    } else {
+        const long long r = (blockIdx.x - a.n) * (kThreads / 32) + (threadIdx.x >> 5);
+        if (r < p.rows) row_power(p, r);
+    }
+    pdl_wait();  // ends after the launch that it ran beside
+}
+
+// One CTA per row (or several rows in turn).
+__global__ void __launch_bounds__(kThreads) copy16_kernel(const uint16_t* x, long long ldx, long long n, long long cols,
+                                                          uint16_t* out, long long ldo)
+{
+    for (long long r = blockIdx.x; r < n; r += gridDim.x)
+        for (long long c = threadIdx.x; c < cols; c += kThreads) out[r * ldo + c] = x[r * ldx + c];
+}
+
+}  // namespace
+
+cudaError_t launch_prepare(ScaleRows a, RowPowers p, cudaStream_t stream)
+{
+    a.vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ldx % 8 == 0;
+    const long long grid = a.n + (p.rows + kThreads / 32 - 1) / (kThreads / 32);
+    return launch_pdl(a.xdtype == TCQ_X_BF16 ? prepare_kernel<TCQ_X_BF16> : prepare_kernel<TCQ_X_F16>,
+                      dim3((unsigned)grid), dim3(kThreads), 0, stream, a.early, a, p);
+}
+
+cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
+                          int num_sms, cudaStream_t stream)
+{
+    const long long grid = n < 32ll * num_sms ? n : 32ll * num_sms;
+    copy16_kernel<<<(int)grid, kThreads, 0, stream>>>(static_cast<const uint16_t*>(x), ldx, n, cols,
+                                                      static_cast<uint16_t*>(out), ldo);
+    return cudaGetLastError();
+}
+
+}  // namespace tcq
