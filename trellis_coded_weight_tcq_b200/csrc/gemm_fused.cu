@@ -9,12 +9,15 @@
 //
 // 16 warps decode, in two groups that take turns at units of 128 columns (two stages
 // of the ring): a warp covers 16 rows, lanes 0-15 the first stage's 64 columns of
-// them, lanes 16-31 the second's.  A lane turns its 2 k stream words (16 bytes for k =
-// 2; the warp reads whole 32-byte sectors, half the cache lines that a row per lane
-// would touch, and the second half's preceding word comes from the first by shuffle)
-// into eight 16-byte pieces of the swizzled K-major tile, held in registers until the
-// stage is free.  Warp 16 loads the activations' tiles by TMA, one thread of warp 17
-// issues the MMAs.
+// them, lanes 16-31 the second's.  A lane turns its 2 k stream words into eight 16-byte
+// pieces of the swizzled K-major tile, held in registers until the stage is free.
+// The look-ups leave the load/store pipe little room (46k of 88k cycles for 14336 x
+// 4096, 71k with everything else), so the stream words come by TMA where shared memory
+// and their alignment allow: boxes of 128 rows by a unit's words and the four before
+// them, through a ring of their own; a warp's reads of 16 separate rows from global
+// memory would take 16 passes each.  Otherwise a warp reads whole 32-byte sectors of its
+// rows.  Warp 16 loads the activations' tiles, warp 18 the stream words, one thread of
+// warp 17 issues the MMAs.
 //
 // Work is split over the SMs evenly, in units: a CTA takes a contiguous run of (tile,
 // unit) pairs, so a tile's reduction may be cut into pieces; each writes its fp32 sums
@@ -31,15 +34,17 @@ namespace tcq {
 namespace {
 
 constexpr int kDecodeWarps = 16;
-constexpr int kThreads = (kDecodeWarps + 2) * 32;
+constexpr int kThreads = (kDecodeWarps + 3) * 32;
 constexpr int kRows = 128;             // rows of W per tile
 constexpr int kDepth = 64;             // columns per stage
 constexpr int kABytes = kRows * kDepth * 2;
 constexpr int kMaxSlots = 8;
+constexpr int kMaxBoxes = 4;
 constexpr int kSmemBytes = 227 * 1024;
 
 struct Barriers {
     unsigned long long full[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2], drain;
+    unsigned long long words_full[kMaxBoxes], words_empty[kMaxBoxes];
     uint32_t tmem;
     int stop;
     int fills[kMaxSlots];  // warps that have filled a slot, counted from the start
@@ -57,6 +62,7 @@ struct Plan {
     int per;              // stages per slot: 2 (a unit), or 1 where only two stages fit
     int tmem_columns;
     int table;            // shared-memory bytes of the table, a multiple of 1024
+    int boxes;            // depth of the stream words' ring, or 0: read from global memory
 };
 
 // the CTA that has unit u, and the first unit of a CTA
@@ -86,16 +92,21 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[2 * 
     }
 }
 
+// Bytes of a row in a box of stream words: a unit's 4 k words and the four before them.
+__host__ __device__ constexpr int box_row_bytes(int k) { return 16 * (k + 1); }
+
 template <int K, int CODE>
 __global__ void __launch_bounds__(kThreads, 1)
-fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, const float* row_pow2, float* partial,
-             unsigned int* err)
+fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_words,
+             Plan p, const float* row_pow2, float* partial, unsigned int* err)
 {
+    constexpr int RB = box_row_bytes(K);
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char* ring = sm + p.table;
     const int bbytes = p.np * kDepth * 2;
     const int sbytes = p.per * (kABytes + bbytes);  // a slot: its A stages, then its B stages
-    Barriers& B = *reinterpret_cast<Barriers*>(ring + (size_t)p.slots * sbytes);
+    unsigned char* boxes = ring + (size_t)p.slots * sbytes;
+    Barriers& B = *reinterpret_cast<Barriers*>(boxes + p.boxes * kRows * RB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.slots; ++i) {
@@ -107,10 +118,15 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
             mbar_init(smem_addr(&B.tfull[i]), 1);
             mbar_init(smem_addr(&B.tempty[i]), kDecodeWarps);
         }
+        for (int i = 0; i < p.boxes; ++i) {
+            mbar_init(smem_addr(&B.words_full[i]), 1);
+            mbar_init(smem_addr(&B.words_empty[i]), kDecodeWarps / 2);
+        }
         mbar_init(smem_addr(&B.drain), 1);
         B.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         tma_prefetch_map(&map_x);
+        if (p.boxes) tma_prefetch_map(&map_words);
     }
     if (warp == kDecodeWarps + 1) tmem_alloc<1>(smem_addr(&B.tmem), p.tmem_columns);
     stage_table<CODE>(sm, w.cb, w.cb_f16, w.L);
@@ -152,31 +168,49 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
         enter_tile();
         advance(group);
         // The words of this lane's 64 columns, the word before them, their scale, the row's
-        // inverse power.  Nothing here depends on what was loaded, so that the loads stay
-        // in flight over the decoding of the unit before.
-        auto fetch = [&](uint32_t (&words)[2 * K], uint32_t& prev, float& sc, float& in) {
+        // inverse power, of the group's unit i (counted from u0).  Nothing here depends on
+        // what was loaded from global memory, so that the loads stay in flight over the
+        // decoding of the unit before.
+        bool ok = true;
+        auto fetch = [&](int i, uint32_t (&words)[2 * K], uint32_t& prev, float& sc, float& in) {
             const int c = ks * 128 + half * kDepth;
+            const bool in_row = bits && c < cols;
+            const int j = tshift >= 0 ? c >> tshift : c / T;
+            const bool first = c == j * T;
             sc = 0.f;
             prev = 0u;
             in = inv;
+            if (p.boxes) {
+                const int box = i % p.boxes;
+                ok = ok && mbar_wait(smem_addr(&B.words_full[box]), (i / p.boxes) & 1, stop, err);
+                const unsigned char* q = boxes + (box * kRows + r) * RB + 16 + 8 * K * half;
 #pragma unroll
-            for (int i = 0; i < 2 * K; ++i) words[i] = 0u;
-            if (bits && c < cols) {
-                const uint32_t* q = bits + c / 32 * K;
-                const int j = tshift >= 0 ? c >> tshift : c / T;
-                const bool first = c == j * T;
-                load_words<K>(q, words, wide);
-                if (first || !half) prev = __ldg(first ? w.start_state + row * nb + j : q - 1);
+                for (int h = 0; h < 2 * K; h += 2) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(q + 4 * h);
+                    words[h] = v.x;
+                    words[h + 1] = v.y;
+                }
+                prev = *reinterpret_cast<const uint32_t*>(q - 4);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&B.words_empty[box]));
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2 * K; ++h) words[h] = 0u;
+                if (in_row) {
+                    const uint32_t* q = bits + c / 32 * K;
+                    load_words<K>(q, words, wide);
+                    if (!first) prev = __ldg(q - 1);
+                }
+            }
+            if (in_row) {
+                if (first) prev = __ldg(w.start_state + row * nb + j);
                 sc = w.scale ? __ldg(w.scale + row * nb + j) : 1.f;
             }
-            return c;
         };
         uint32_t words[2 * K], prev;
         float sc, pw;
-        int c0 = 0;
         long long u = u0 + group;
-        if (u < u1) c0 = fetch(words, prev, sc, pw);
-        bool ok = true;
+        if (u < u1) fetch(group, words, prev, sc, pw);
         int done = 0;
         for (long long s0 = u0; s0 < u1 && ok; ++done) {  // segments: runs of one tile's units
             const long long seg_tile = s0 / p.steps;
@@ -195,19 +229,14 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                 const bool ready = p.per == 2 && mbar_test(empty, (round & 1) ^ 1);
                 uint32_t nwords[2 * K], nprev;
                 float nsc, npw;
-                int nc0 = 0;
                 if (u + 2 < u1) {
                     advance(2);
-                    nc0 = fetch(nwords, nprev, nsc, npw);
+                    fetch((int)(u - u0) + 2, nwords, nprev, nsc, npw);
                 }
-                // the second half's word before it is the first half's last, inside a block
-                const uint32_t other = __shfl_up_sync(0xffffffffu, words[2 * K - 1], 16);
-                const int j0 = tshift >= 0 ? c0 >> tshift : c0 / T;
-                const uint32_t before = half && c0 != j0 * T ? other : prev;
                 uint32_t v[32];
-                decode_64<K, CODE>(words, before, mask, sm, sc * inverse_pow2(pw), v);
-                if (!__all_sync(0xffffffffu, ready)) {
-                    if (p.per == 1) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
+                decode_64<K, CODE>(words, prev, mask, sm, sc * inverse_pow2(pw), v);
+                if (!__all_sync(0xffffffffu, ready && ok)) {
+                    if (ok && p.per == 1) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
                     ok = ok && mbar_wait(empty, (round & 1) ^ 1, stop, err);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -228,7 +257,6 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
                 prev = nprev;
                 sc = nsc;
                 pw = npw;
-                c0 = nc0;
             }
             if (!ok) break;
             // the segment's sums: lane = row, 16 tokens at a time shared among the warps
@@ -276,6 +304,33 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, Plan p, c
             if (!ok)  // what was loaded last is still waited for (unless its decoders stopped)
                 for (int j = i > p.slots ? i - p.slots : 0; j < i; ++j)
                     mbar_drain(smem_addr(&B.full[j % p.slots]), (j / p.slots) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kDecodeWarps + 2) {
+        if (lane == 0 && p.boxes) {
+            bool ok = true;
+            int i = 0;
+            const int n = (int)(u1 - u0);
+            long long tile = u0 / p.steps;
+            int ks = (int)(u0 - tile * p.steps);
+            for (; i < n; ++i) {
+                const int box = i % p.boxes;
+                const uint32_t full = smem_addr(&B.words_full[box]);
+                ok = mbar_wait(smem_addr(&B.words_empty[box]), ((i / p.boxes) & 1) ^ 1, stop, err);
+                if (!ok) break;
+                mbar_expect_tx(full, kRows * RB);
+                // 16 k bytes per unit: every copy starts on a 16-byte boundary; before a row's
+                // first word and behind its last the box is filled with zeros
+                tma_load_2d(smem_addr(boxes + box * kRows * RB), &map_words, full, 4 * K * ks - 4,
+                            (int)(tile % p.row_tiles) * kRows);
+                if (++ks == p.steps) {
+                    ks = 0;
+                    ++tile;
+                }
+            }
+            if (!ok)
+                for (int j = i > p.boxes ? i - p.boxes : 0; j < i; ++j)
+                    mbar_drain(smem_addr(&B.words_full[j % p.boxes]), (j / p.boxes) & 1);
         }
         __syncwarp();
     } else {
@@ -389,7 +444,8 @@ __global__ void __launch_bounds__(256) fused_finish_kernel(Plan p, Epilogue e, l
 
 int code_of(const CodedMatrix& w) { return w.cb_f16 == 1 ? kCode16F16 : w.cb_f16 == 0 ? kCode16F32 : kCode16Mad; }
 
-Plan make_plan(int code, int L, long long rows, long long cols, long long n, int num_sms)
+// `words_tma`: the stream's rows can be read by TMA
+Plan make_plan(int code, int L, int K, long long rows, long long cols, long long n, int num_sms, bool words_tma)
 {
     Plan p;
     p.n = n;
@@ -411,35 +467,41 @@ Plan make_plan(int code, int L, long long rows, long long cols, long long n, int
     // fit beside the table (the barriers of a slot share the pipe that the look-ups fill,
     // about 300 cycles each); slots of a stage otherwise
     const int room = kSmemBytes - p.table - (int)sizeof(Barriers), stage = kABytes + p.np * kDepth * 2;
+    const int box = kRows * box_row_bytes(K);
     p.per = room >= 4 * stage ? 2 : 1;
-    p.slots = p.per == 2 ? room / (2 * stage) : 2;
+    p.slots = p.per == 2 ? (room - (words_tma ? kMaxBoxes * box : 0)) / (2 * stage) : 2;
+    if (p.slots < 2) p.slots = 2;
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+    p.boxes = words_tma ? (room - p.slots * p.per * stage) / box : 0;
+    // an even number, so that a group's boxes are its own: it has then seen the phase before
+    p.boxes = p.boxes >= kMaxBoxes ? kMaxBoxes : p.boxes / 2 * 2;
     p.tmem_columns = 32;
     while (p.tmem_columns < 2 * p.np) p.tmem_columns *= 2;
     return p;
 }
 
 template <int K, int CODE>
-cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const Plan& p, const float* row_pow2, float* partial,
+cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p, const float* row_pow2, float* partial,
                    unsigned int* err, bool early, cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(fused_kernel<K, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemBytes);
     if (e != cudaSuccess) return e;
-    const size_t smem = p.table + (size_t)p.slots * p.per * (kABytes + p.np * kDepth * 2) + sizeof(Barriers);
-    return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, p, row_pow2,
+    const size_t smem = p.table + (size_t)p.slots * p.per * (kABytes + p.np * kDepth * 2) + p.boxes * kRows * box_row_bytes(K) +
+                        sizeof(Barriers);
+    return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, words, p, row_pow2,
                       partial, err);
 }
 
 template <int CODE>
-cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const Plan& p, const float* row_pow2, float* partial,
+cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p, const float* row_pow2, float* partial,
                      unsigned int* err, bool early, cudaStream_t stream)
 {
     switch (w.K) {
-    case 1: return launch<1, CODE>(w, map, p, row_pow2, partial, err, early, stream);
-    case 2: return launch<2, CODE>(w, map, p, row_pow2, partial, err, early, stream);
-    case 3: return launch<3, CODE>(w, map, p, row_pow2, partial, err, early, stream);
-    default: return launch<4, CODE>(w, map, p, row_pow2, partial, err, early, stream);
+    case 1: return launch<1, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
+    case 2: return launch<2, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
+    case 3: return launch<3, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
+    default: return launch<4, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
     }
 }
 
@@ -454,7 +516,7 @@ bool fused_shape(int T, long long rows, long long cols, long long n)
 size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms)
 {
     const int code = cb_f16 == 1 ? kCode16F16 : cb_f16 == 0 ? kCode16F32 : kCode16Mad;
-    const Plan p = make_plan(code, L, rows, cols, n, num_sms);
+    const Plan p = make_plan(code, L, 1, rows, cols, n, num_sms, false);  // the pieces do not depend on the ring
     return (size_t)p.row_tiles * p.token_tiles * p.pieces * p.np * kRows * sizeof(float);
 }
 
@@ -463,12 +525,18 @@ cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx
                               bool early, cudaStream_t stream)
 {
     const int code = code_of(w);
-    const Plan p = make_plan(code, w.L, w.rows, w.cols, n, num_sms);
-    CUtensorMap map;
+    const long long row_words = w.cols / 32 * w.K;
+    const bool words_tma = (reinterpret_cast<uintptr_t>(w.bits) & 15) == 0 && row_words % 4 == 0;
+    const Plan p = make_plan(code, w.L, w.K, w.rows, w.cols, n, num_sms, words_tma);
+    CUtensorMap map, words;
     if (!make_map_16bit(&map, x, n, w.cols, ldx, p.np)) return cudaErrorInvalidValue;
-    cudaError_t st = code == kCode16Mad   ? launch_k<kCode16Mad>(w, map, p, row_pow2, partial, err, early, stream)
-                     : code == kCode16F16 ? launch_k<kCode16F16>(w, map, p, row_pow2, partial, err, early, stream)
-                                          : launch_k<kCode16F32>(w, map, p, row_pow2, partial, err, early, stream);
+    if (p.boxes == 0)
+        words = map;  // not used
+    else if (!make_map_words(&words, w.bits, w.rows, row_words, 4 * (w.K + 1), kRows))
+        return cudaErrorInvalidValue;
+    cudaError_t st = code == kCode16Mad   ? launch_k<kCode16Mad>(w, map, words, p, row_pow2, partial, err, early, stream)
+                     : code == kCode16F16 ? launch_k<kCode16F16>(w, map, words, p, row_pow2, partial, err, early, stream)
+                                          : launch_k<kCode16F32>(w, map, words, p, row_pow2, partial, err, early, stream);
     if (st != cudaSuccess) return st;
     bool vec = (reinterpret_cast<uintptr_t>(e.out) & 7) == 0 && e.ldo % 4 == 0;
     if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 7) == 0 && e.ldr % 4 == 0;

@@ -32,10 +32,9 @@ namespace tcq {
 
 namespace {
 
-// A tensor map of a row-major matrix with the 128-byte swizzle, boxes of box_rows x
-// 128 bytes; elements of 2 or 4 bytes.
+// A tensor map of a row-major matrix, elements of 2 or 4 bytes.
 bool make_map(CUtensorMap* map, CUtensorMapDataType type, int element, const void* base, long long rows, long long cols,
-              long long ld, int box_rows)
+              long long ld, int box_cols, int box_rows, CUtensorMapSwizzle swizzle)
 {
     typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -53,17 +52,17 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, int element, const voi
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld * element};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / element), (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t step[2] = {1u, 1u};
     return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool make_map_out(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld, int element)
 {
     return make_map(map, element == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, element, base,
-                    rows, cols, ld, 32);
+                    rows, cols, ld, 128 / element, 32, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
@@ -71,7 +70,13 @@ bool make_map_out(CUtensorMap* map, const void* base, long long rows, long long 
 bool make_map_16bit(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld, int box_rows)
 {
     // the element type only matters for the fill, which is zero in both
-    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, rows, cols, ld, box_rows);
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, rows, cols, ld, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool make_map_words(CUtensorMap* map, const void* base, long long rows, long long cols, int box_cols, int box_rows)
+{
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, base, rows, cols, cols, box_cols, box_rows,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 namespace {

@@ -310,5 +310,8 @@ __device__ __forceinline__ void tmem_load8(uint32_t addr, float (&v)[8])
 // `ld` elements (a multiple of 8), read in boxes of box_rows x 64 columns with the
 // 128-byte swizzle; elements outside read as zero.  The base is 16-byte aligned.
 bool make_map_16bit(CUtensorMap* map, const void* base, long long rows, long long cols, long long ld, int box_rows);
+// The same for 32-bit words without gaps between rows (cols a multiple of 4) and without
+// swizzle, in boxes of box_rows x box_cols (a multiple of 4).
+bool make_map_words(CUtensorMap* map, const void* base, long long rows, long long cols, int box_cols, int box_rows);
 
 }  // namespace tcq
