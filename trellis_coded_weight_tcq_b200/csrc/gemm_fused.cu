@@ -38,16 +38,16 @@ constexpr int kThreads = (kDecodeWarps + 3) * 32;
 constexpr int kRows = 128;             // rows of W per tile
 constexpr int kDepth = 64;             // columns per stage
 constexpr int kABytes = kRows * kDepth * 2;
-constexpr int kMaxSlots = 8;
-constexpr int kMaxBoxes = 4;
+constexpr int kSlots = 2;              // of the operand ring
 constexpr int kSmemBytes = 227 * 1024;
 
 struct Barriers {
-    unsigned long long full[kMaxSlots], empty[kMaxSlots], tfull[2], tempty[2], drain;
-    unsigned long long words_full[kMaxBoxes], words_empty[kMaxBoxes];
+    unsigned long long full[kSlots], empty[kSlots], tfull[2], tempty[2], drain;
+    unsigned long long go[2];           // a group may decode its next unit
+    unsigned long long words_empty[2];  // a group has read its box of stream words
     uint32_t tmem;
     int stop;
-    int fills[kMaxSlots];  // warps that have filled a slot, counted from the start
+    int fills[kSlots];  // warps that have filled a slot, counted from the start
 };
 
 struct Plan {
@@ -58,11 +58,10 @@ struct Plan {
     long long units;      // tiles * steps
     int ctas;
     int pieces;           // slots per tile in the workspace
-    int slots;            // ring depth
     int per;              // stages per slot: 2 (a unit), or 1 where only two stages fit
     int tmem_columns;
     int table;            // shared-memory bytes of the table, a multiple of 1024
-    int boxes;            // depth of the stream words' ring, or 0: read from global memory
+    int boxes;            // 1: a box of stream words per group, 0: words from global memory
 };
 
 // the CTA that has unit u, and the first unit of a CTA
@@ -95,6 +94,25 @@ __device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[2 * 
 // Bytes of a row in a box of stream words: a unit's 4 k words and the four before them.
 __host__ __device__ constexpr int box_row_bytes(int k) { return 16 * (k + 1); }
 
+// The same from a box in shared memory (8 k bytes, aligned to 8, for even k to 16).
+template <int K>
+__device__ __forceinline__ void read_words(const unsigned char* p, uint32_t (&w)[2 * K])
+{
+    if constexpr (K % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < 2 * K; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * K; i += 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * i);
+            w[i] = v.x; w[i + 1] = v.y;
+        }
+    }
+}
+
 template <int K, int CODE>
 __global__ void __launch_bounds__(kThreads, 1)
 fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_words,
@@ -105,21 +123,18 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
     unsigned char* ring = sm + p.table;
     const int bbytes = p.np * kDepth * 2;
     const int sbytes = p.per * (kABytes + bbytes);  // a slot: its A stages, then its B stages
-    unsigned char* boxes = ring + (size_t)p.slots * sbytes;
-    Barriers& B = *reinterpret_cast<Barriers*>(boxes + p.boxes * kRows * RB);
+    unsigned char* boxes = ring + kSlots * sbytes;
+    Barriers& B = *reinterpret_cast<Barriers*>(boxes + 2 * p.boxes * kRows * RB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < p.slots; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&B.full[i]), kDecodeWarps / 2 + 1);  // a group's warps, and the TMA thread
             mbar_init(smem_addr(&B.empty[i]), 1);
             B.fills[i] = 0;
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&B.tfull[i]), 1);
             mbar_init(smem_addr(&B.tempty[i]), kDecodeWarps);
-        }
-        for (int i = 0; i < p.boxes; ++i) {
-            mbar_init(smem_addr(&B.words_full[i]), 1);
+            // the other group has decoded its unit before, the words are there, the slot is free
+            mbar_init(smem_addr(&B.go[i]), kDecodeWarps / 2 + p.boxes + (p.per == 2));
             mbar_init(smem_addr(&B.words_empty[i]), kDecodeWarps / 2);
         }
         mbar_init(smem_addr(&B.drain), 1);
@@ -147,17 +162,18 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
         const int T = w.T, cols = (int)w.cols, nb = cols / T;
         const int tshift = (T & (T - 1)) == 0 ? __ffs(T) - 1 : -1;
         const bool wide = (reinterpret_cast<uintptr_t>(w.bits) & 15) == 0;
-        const int row_words = cols / 32 * K;
-        // where the group's next unit is: its tile, its place in the reduction, its row
+        // where the next unit is: its tile, its place in the reduction, this lane's row
         long long tile = u0 / p.steps;
         int ks = (int)(u0 - tile * p.steps);
-        const uint32_t* bits = nullptr;  // this lane's row, or none
-        long long row = 0;
+        const uint32_t *bits = nullptr, *start = nullptr;  // of the row, or none
+        const float* scale = nullptr;
         float inv = 1.f;  // the row's power
         auto enter_tile = [&]() {
-            row = (tile % p.row_tiles) * kRows + r;
-            bits = row < w.rows ? w.bits + row * row_words : nullptr;
-            if (bits && w.scale) inv = __ldg(row_pow2 + row);
+            const long long row = (tile % p.row_tiles) * kRows + r;
+            bits = row < w.rows ? w.bits + row * (cols / 32 * K) : nullptr;
+            start = w.start_state + row * nb;
+            scale = w.scale ? w.scale + row * nb : nullptr;
+            if (bits && scale) inv = __ldg(row_pow2 + row);
         };
         auto advance = [&](int by) {
             for (ks += by; ks >= p.steps; ks -= p.steps) {
@@ -167,96 +183,92 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
         };
         enter_tile();
         advance(group);
-        // The words of this lane's 64 columns, the word before them, their scale, the row's
-        // inverse power, of the group's unit i (counted from u0).  Nothing here depends on
-        // what was loaded from global memory, so that the loads stay in flight over the
-        // decoding of the unit before.
-        bool ok = true;
-        auto fetch = [&](int i, uint32_t (&words)[2 * K], uint32_t& prev, float& sc, float& in) {
+        // What the next unit needs from global memory, on its way while this one is decoded:
+        // its block's start state where the lane's columns begin one, its scale, the row's
+        // power, and without the ring of boxes its words and the one before them.
+        uint32_t nwords[2 * K], nprev = 0u;
+        float nsc = 0.f, npw = 1.f;
+        bool nfirst = false;
+        auto fetch = [&]() {
             const int c = ks * 128 + half * kDepth;
-            const bool in_row = bits && c < cols;
             const int j = tshift >= 0 ? c >> tshift : c / T;
-            const bool first = c == j * T;
-            sc = 0.f;
-            prev = 0u;
-            in = inv;
-            if (p.boxes) {
-                const int box = i % p.boxes;
-                ok = ok && mbar_wait(smem_addr(&B.words_full[box]), (i / p.boxes) & 1, stop, err);
-                const unsigned char* q = boxes + (box * kRows + r) * RB + 16 + 8 * K * half;
+            nfirst = c == j * T;
+            nsc = 0.f;
+            nprev = 0u;
+            npw = inv;
+            if (!p.boxes) {
 #pragma unroll
-                for (int h = 0; h < 2 * K; h += 2) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(q + 4 * h);
-                    words[h] = v.x;
-                    words[h + 1] = v.y;
-                }
-                prev = *reinterpret_cast<const uint32_t*>(q - 4);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&B.words_empty[box]));
-            } else {
-#pragma unroll
-                for (int h = 0; h < 2 * K; ++h) words[h] = 0u;
-                if (in_row) {
-                    const uint32_t* q = bits + c / 32 * K;
-                    load_words<K>(q, words, wide);
-                    if (!first) prev = __ldg(q - 1);
-                }
+                for (int h = 0; h < 2 * K; ++h) nwords[h] = 0u;
             }
-            if (in_row) {
-                if (first) prev = __ldg(w.start_state + row * nb + j);
-                sc = w.scale ? __ldg(w.scale + row * nb + j) : 1.f;
+            if (bits && c < cols) {
+                if (!p.boxes) load_words<K>(bits + c / 32 * K, nwords, wide);
+                if (nfirst)
+                    nprev = __ldg(start + j);
+                else if (!p.boxes)
+                    nprev = __ldg(bits + c / 32 * K - 1);
+                nsc = scale ? __ldg(scale + j) : 1.f;
             }
         };
-        uint32_t words[2 * K], prev;
-        float sc, pw;
+        bool ok = true;
         long long u = u0 + group;
-        if (u < u1) fetch(group, words, prev, sc, pw);
+        if (u < u1) fetch();
+        // Slots of a unit belong to a group each, slots of a stage to a half of every unit.
+        const int slot = p.per == 2 ? group : half;
+        const uint32_t go = smem_addr(&B.go[group]);
+        if (group == 1 && lane == 0) mbar_arrive(smem_addr(&B.go[0]));  // there is no unit before the first
+        const unsigned char* box = boxes + (group * kRows + r) * RB + 16 + 8 * K * half;
+        unsigned char* const a = ring + slot * sbytes + (p.per == 2 ? half * kABytes : 0) + r * 128;
+        int own = 0;  // the group's units so far
         int done = 0;
         for (long long s0 = u0; s0 < u1 && ok; ++done) {  // segments: runs of one tile's units
             const long long seg_tile = s0 / p.steps;
             const long long s1 = (seg_tile + 1) * p.steps < u1 ? (seg_tile + 1) * p.steps : u1;
-            for (; u < s1; u += 2) {
-                const int it = 2 * (int)(u - u0);  // the unit's first stage
-                // Where the unit's stages go.  A barrier's parity tells two neighbouring phases
-                // apart.  With four or more stages the wait one turn ago puts this one's
-                // phase next; with two, the group must first see the other group's fill.
-                // The slot is usually free by now: asked here, the answer is there after the
-                // decoding, while an answer waited for takes hundreds of cycles in the queue
-                // of the look-ups.
-                const int step = (it + half) / p.per, sub = (it + half) % p.per;
-                const int slot = step % p.slots, round = step / p.slots;
-                const uint32_t empty = smem_addr(&B.empty[slot]);
-                const bool ready = p.per == 2 && mbar_test(empty, (round & 1) ^ 1);
-                uint32_t nwords[2 * K], nprev;
-                float nsc, npw;
+            for (; u < s1; u += 2, ++own) {
+                uint32_t words[2 * K], prev = nprev;
+                const float sc = nsc, pw = npw;
+                const bool first = nfirst;
+#pragma unroll
+                for (int h = 0; h < 2 * K; ++h) words[h] = nwords[h];
                 if (u + 2 < u1) {
                     advance(2);
-                    fetch((int)(u - u0) + 2, nwords, nprev, nsc, npw);
+                    fetch();
+                }
+                // The groups decode in turns: one fills the load/store pipe by itself, and the
+                // other stores, fetches and waits meanwhile (left alone they fall into step).
+                // A wait takes hundreds of cycles in the queue of the other's look-ups, so
+                // one barrier stands for all that a unit needs.
+                ok = ok && mbar_wait(go, own & 1, stop, err);
+                if (p.boxes) {
+                    read_words<K>(box, words);
+                    const uint32_t before = *reinterpret_cast<const uint32_t*>(box - 4);
+                    if (!first) prev = before;
                 }
                 uint32_t v[32];
                 decode_64<K, CODE>(words, prev, mask, sm, sc * inverse_pow2(pw), v);
-                if (!__all_sync(0xffffffffu, ready && ok)) {
-                    if (ok && p.per == 1) ok = wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err);
-                    ok = ok && mbar_wait(empty, (round & 1) ^ 1, stop, err);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&B.go[group ^ 1]));
+                    if (p.boxes) mbar_arrive(smem_addr(&B.words_empty[group]));
                 }
-                unsigned char* a = ring + (size_t)slot * sbytes + sub * kABytes + r * 128;
+                if (p.per == 1) {
+                    // A barrier's parity tells two neighbouring phases apart: the group must
+                    // first see the other group's fill of these slots.
+                    const int round = 2 * own + group;
+                    ok = ok && wait_count(&B.fills[slot], kDecodeWarps / 2 * round, stop, err) &&
+                         mbar_wait(smem_addr(&B.empty[slot]), (round & 1) ^ 1, stop, err);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     *reinterpret_cast<uint4*>(a + ((q ^ (r & 7)) << 4)) =
                         make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                fence_async_shared();
                 __syncwarp();
                 if (lane == 0 || (p.per == 1 && lane == 16)) {
                     mbar_arrive(smem_addr(&B.full[slot]));
                     if (p.per == 1) atomicAdd(&B.fills[slot], 1);
                 }
-#pragma unroll
-                for (int i = 0; i < 2 * K; ++i) words[i] = nwords[i];
-                prev = nprev;
-                sc = nsc;
-                pw = npw;
             }
             if (!ok) break;
             // the segment's sums: lane = row, 16 tokens at a time shared among the warps
@@ -287,13 +299,13 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
             long long tile = u0 / p.steps;
             int ks = 2 * (int)(u0 - tile * p.steps);  // in stages
             for (; i < fills; ++i) {
-                const int slot = i % p.slots;
+                const int slot = i & 1;
                 const uint32_t full = smem_addr(&B.full[slot]);
-                ok = mbar_wait(smem_addr(&B.empty[slot]), ((i / p.slots) & 1) ^ 1, stop, err);
+                ok = mbar_wait(smem_addr(&B.empty[slot]), ((i >> 1) & 1) ^ 1, stop, err);
                 if (!ok) break;
                 mbar_expect_tx(full, p.per * bbytes);
                 for (int h = 0; h < p.per; ++h)
-                    tma_load_2d(smem_addr(ring + (size_t)slot * sbytes + p.per * kABytes + h * bbytes), &map_x, full,
+                    tma_load_2d(smem_addr(ring + slot * sbytes + p.per * kABytes + h * bbytes), &map_x, full,
                                 (ks + h) * kDepth, (int)(tile / p.row_tiles) * p.np);
                 ks += p.per;
                 if (ks == 2 * p.steps) {
@@ -302,8 +314,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                 }
             }
             if (!ok)  // what was loaded last is still waited for (unless its decoders stopped)
-                for (int j = i > p.slots ? i - p.slots : 0; j < i; ++j)
-                    mbar_drain(smem_addr(&B.full[j % p.slots]), (j / p.slots) & 1);
+                for (int j = i > kSlots ? i - kSlots : 0; j < i; ++j) mbar_drain(smem_addr(&B.full[j & 1]), (j >> 1) & 1);
         }
         __syncwarp();
     } else if (warp == kDecodeWarps + 2) {
@@ -314,14 +325,14 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
             long long tile = u0 / p.steps;
             int ks = (int)(u0 - tile * p.steps);
             for (; i < n; ++i) {
-                const int box = i % p.boxes;
-                const uint32_t full = smem_addr(&B.words_full[box]);
-                ok = mbar_wait(smem_addr(&B.words_empty[box]), ((i / p.boxes) & 1) ^ 1, stop, err);
+                const int g = i & 1;
+                const uint32_t go = smem_addr(&B.go[g]);
+                ok = mbar_wait(smem_addr(&B.words_empty[g]), ((i >> 1) & 1) ^ 1, stop, err);
                 if (!ok) break;
-                mbar_expect_tx(full, kRows * RB);
+                mbar_expect_tx(go, kRows * RB);
                 // 16 k bytes per unit: every copy starts on a 16-byte boundary; before a row's
                 // first word and behind its last the box is filled with zeros
-                tma_load_2d(smem_addr(boxes + box * kRows * RB), &map_words, full, 4 * K * ks - 4,
+                tma_load_2d(smem_addr(boxes + g * kRows * RB), &map_words, go, 4 * K * ks - 4,
                             (int)(tile % p.row_tiles) * kRows);
                 if (++ks == p.steps) {
                     ks = 0;
@@ -329,8 +340,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                 }
             }
             if (!ok)
-                for (int j = i > p.boxes ? i - p.boxes : 0; j < i; ++j)
-                    mbar_drain(smem_addr(&B.words_full[j % p.boxes]), (j / p.boxes) & 1);
+                for (int j = i > 2 ? i - 2 : 0; j < i; ++j) mbar_drain(smem_addr(&B.go[j & 1]), (j >> 1) & 1);
         }
         __syncwarp();
     } else {
@@ -339,6 +349,8 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
             const unsigned long long desc0 = smem_desc_sw128(smem_addr(ring), 16);
             bool ok = true;
             int done = 0;
+            if (p.per == 2)  // both slots start free
+                for (int g = 0; g < 2; ++g) mbar_arrive(smem_addr(&B.go[g]));
             for (long long s0 = u0; s0 < u1 && ok; ++done) {
                 const long long tile = s0 / p.steps;
                 const long long s1 = (tile + 1) * p.steps < u1 ? (tile + 1) * p.steps : u1;
@@ -348,8 +360,8 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                 tc_fence_after();
                 const int first = 2 / p.per * (int)(s0 - u0), last = 2 / p.per * (int)(s1 - u0);
                 for (int i = first; i < last; ++i) {
-                    const int slot = i % p.slots;
-                    ok = mbar_wait(smem_addr(&B.full[slot]), (i / p.slots) & 1, stop, err);
+                    const int slot = i & 1;
+                    ok = mbar_wait(smem_addr(&B.full[slot]), (i >> 1) & 1, stop, err);
                     if (!ok) break;
                     tc_fence_after();
                     // descriptors count in 16 bytes
@@ -361,6 +373,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                                        i != first || h != 0 || j != 0);
                     }
                     mma_commit<1>(smem_addr(&B.empty[slot]));
+                    if (p.per == 2) mma_commit<1>(smem_addr(&B.go[slot]));
                 }
                 if (ok) mma_commit<1>(smem_addr(&B.tfull[acc]));
                 s0 = s1;
@@ -469,12 +482,7 @@ Plan make_plan(int code, int L, int K, long long rows, long long cols, long long
     const int room = kSmemBytes - p.table - (int)sizeof(Barriers), stage = kABytes + p.np * kDepth * 2;
     const int box = kRows * box_row_bytes(K);
     p.per = room >= 4 * stage ? 2 : 1;
-    p.slots = p.per == 2 ? (room - (words_tma ? kMaxBoxes * box : 0)) / (2 * stage) : 2;
-    if (p.slots < 2) p.slots = 2;
-    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-    p.boxes = words_tma ? (room - p.slots * p.per * stage) / box : 0;
-    // an even number, so that a group's boxes are its own: it has then seen the phase before
-    p.boxes = p.boxes >= kMaxBoxes ? kMaxBoxes : p.boxes / 2 * 2;
+    p.boxes = words_tma && room - kSlots * p.per * stage >= 2 * box;
     p.tmem_columns = 32;
     while (p.tmem_columns < 2 * p.np) p.tmem_columns *= 2;
     return p;
@@ -487,7 +495,7 @@ cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const CUtensorM
     const cudaError_t e = cudaFuncSetAttribute(fused_kernel<K, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemBytes);
     if (e != cudaSuccess) return e;
-    const size_t smem = p.table + (size_t)p.slots * p.per * (kABytes + p.np * kDepth * 2) + p.boxes * kRows * box_row_bytes(K) +
+    const size_t smem = p.table + (size_t)kSlots * p.per * (kABytes + p.np * kDepth * 2) + 2 * p.boxes * kRows * box_row_bytes(K) +
                         sizeof(Barriers);
     return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, words, p, row_pow2,
                       partial, err);
