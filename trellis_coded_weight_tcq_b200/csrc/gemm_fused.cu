@@ -220,6 +220,29 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
         unsigned char* const a = ring + slot * sbytes + (p.per == 2 ? half * kABytes : 0) + r * 128;
         int own = 0;  // the group's units so far
         int done = 0;
+        // A segment's sums are written after the group's first unit of the next one, while the
+        // other group decodes: lane = row, 16 tokens at a time shared among the warps.
+        long long pending = -1;
+        int pending_set = 0, pending_parity = 0;
+        auto flush = [&]() {
+            if (pending < 0 || !ok) return;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&B.tfull[pending_set]), pending_parity, stop, err));
+            if (!ok) return;
+            tc_fence_after();
+            const int piece = (int)blockIdx.x - cta_of(p, pending * p.steps);
+            float* out = partial + ((pending * p.pieces + piece) * p.np) * kRows + (warp & 3) * 32 + lane;
+            const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + pending_set * acc_columns;
+            for (int c = 16 * (warp >> 2); c < p.np; c += 64) {
+                float d[16];
+                tmem_load16(lanes + c, d);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) __stcg(out + (long long)(c + i) * kRows, d[i]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&B.tempty[pending_set]));
+            pending = -1;
+        };
         for (long long s0 = u0; s0 < u1 && ok; ++done) {  // segments: runs of one tile's units
             const long long seg_tile = s0 / p.steps;
             const long long s1 = (seg_tile + 1) * p.steps < u1 ? (seg_tile + 1) * p.steps : u1;
@@ -269,28 +292,16 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                     mbar_arrive(smem_addr(&B.full[slot]));
                     if (p.per == 1) atomicAdd(&B.fills[slot], 1);
                 }
+                if (pending >= 0) flush();
             }
             if (!ok) break;
-            // the segment's sums: lane = row, 16 tokens at a time shared among the warps
-            const int acc = done & 1;
-            ok = mbar_wait(smem_addr(&B.tfull[acc]), (done >> 1) & 1, stop, err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            const int piece = (int)blockIdx.x - cta_of(p, seg_tile * p.steps);
-            float* out = partial + ((seg_tile * p.pieces + piece) * p.np) * kRows + (warp & 3) * 32 + lane;
-            const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + acc * acc_columns;
-            for (int c = 16 * (warp >> 2); c < p.np; c += 64) {
-                float d[16];
-                tmem_load16(lanes + c, d);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) __stcg(out + (long long)(c + i) * kRows, d[i]);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&B.tempty[acc]));
+            flush();  // of the segment before, where the group had no unit in this one
+            pending = seg_tile;
+            pending_set = done & 1;
+            pending_parity = (done >> 1) & 1;
             s0 = s1;
         }
+        flush();
     } else if (warp == kDecodeWarps) {
         if (lane == 0) {
             bool ok = true;
