@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(256) fused_finish_kernel(Plan p, Epilogue e, l
     const int pieces = cta_of(p, (tile + 1) * p.steps - 1) - cta_of(p, tile * p.steps) + 1;
     const float* src = partial + (tile * p.pieces * p.np + local) * kRows + 4 * lane;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int i = 0; i < pieces; ++i) {
         const float4 d = __ldcg(reinterpret_cast<const float4*>(src + (long long)i * p.np * kRows));
         v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;

@@ -321,10 +321,16 @@ def tcq_encode_path(L: int, k: int, cb_dtype: int) -> str:
 # ---------------------------------------------------------------------------
 # torch conveniences (device memory and streams only)
 # ---------------------------------------------------------------------------
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def cb_dtype_of(codebook) -> int:
@@ -594,10 +600,9 @@ class Packed8:
 # sizes compare with tuples, addresses and streams go to ctypes as integers.
 def _x_dtype(t, what: str) -> int:
     """TCQ_X_* of a 2-D 16-bit CUDA tensor with unit-stride rows."""
-    torch = _torch()
     if t.dim() != 2 or not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel()):
         raise ValueError(f"{what} must be a 2-D CUDA tensor with unit-stride rows")
-    dtype = t.dtype
+    dtype, torch = t.dtype, _torch_module
     if dtype == torch.bfloat16:
         return TCQ_X_BF16
     if dtype == torch.float16:
@@ -632,12 +637,11 @@ def _check_device(t, device, what):
 
 
 def _check_packed(p, n, cols, device, what):
-    torch = _torch()
-    fmt = _choice(Q8_FORMATS, p.format, f"{what}.format")
+    fmt = _choice(Q8_FORMATS, p.format, "format")
     codes, scales = p.codes, p.scales
     groups = (cols + 31) // 32
     if (codes.shape != (n, cols) or codes.element_size() != 1 or not codes.is_contiguous() or
-            scales.shape != (n, groups) or scales.dtype != torch.uint8 or not scales.is_contiguous()):
+            scales.shape != (n, groups) or scales.dtype != _torch().uint8 or not scales.is_contiguous()):
         raise ValueError(f"{what} must hold contiguous 8-bit codes [{n}, {cols}] and uint8 scales [{n}, {groups}]")
     _check_device(codes, device, what)
     _check_device(scales, device, what)
@@ -645,12 +649,10 @@ def _check_packed(p, n, cols, device, what):
 
 
 def _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, device, what):
-    torch = _torch()
-    W = tcq_words_per_block(k, T)
-    if W < 0:
-        raise TCQError(TCQ_ERR_UNSUPPORTED, "tcq_words_per_block")
+    if not (1 <= k <= TCQ_MAX_K and 1 <= T <= TCQ_MAX_T):
+        raise TCQError(TCQ_ERR_UNSUPPORTED, what)
     nb = rows * (cols // T)
-    if bits.numel() < nb * W or start_state.numel() < nb:
+    if bits.numel() < nb * ((T * k + 31) // 32) or start_state.numel() < nb:
         raise ValueError(f"{what}: tensors too small for a {rows} x {cols} matrix of T={T} blocks")
     if (bits.element_size() != 4 or start_state.element_size() != 4 or not bits.is_contiguous() or
             not start_state.is_contiguous()):
@@ -658,7 +660,7 @@ def _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, devic
     _check_device(bits, device, "bits")
     _check_device(start_state, device, "start_state")
     if scale is not None:
-        if scale.numel() < nb or scale.dtype != torch.float32 or not scale.is_contiguous():
+        if scale.numel() < nb or scale.dtype != _torch().float32 or not scale.is_contiguous():
             raise ValueError(f"{what}: scale must hold a contiguous float32 value per block")
         _check_device(scale, device, "scale")
     if codebook is not MAD:
