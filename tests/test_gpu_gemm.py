@@ -82,7 +82,11 @@ SHAPES = [  # L, k, T, rows, blocks per row, code, scaled, n, dtype
     (14, 1, 64, 2500, 9, "f32", True, 200, "f16"),
     (16, 4, 256, 20000, 1, "f16", False, 20, "bf16"),   # more row tiles than SMs, few stages each
     (8, 3, 64, 130, 1, "mad", True, 256, "f16"),        # one stage per tile
-    (16, 2, 256, 520, 8, "f16", True, 1025, "bf16"),    # the first count that decodes ahead
+    (16, 2, 256, 520, 8, "f16", True, 1025, "bf16"),
+    (16, 2, 256, 520, 8, "mad", True, 384, "f16"),      # two token tiles, decoded as it goes
+    (16, 2, 256, 520, 8, "mad", True, 385, "bf16"),     # the first count that decodes ahead
+    (12, 2, 100, 300, 20, "f32", True, 9, "f16"),       # decoded ahead, few tiles: a cut reduction
+    (16, 3, 20, 270, 130, "mad", True, 300, "bf16"),
 ]
 
 
@@ -136,6 +140,28 @@ def test_gemm_epilogue(act, n, rows, dtype, fmt, cuda_device):
     buf = res.clone()
     y2 = tcq.gemm(*args, x, bias=bias, act=act, residual=buf, out=buf)
     assert y2.data_ptr() == buf.data_ptr() and torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("dtype,fmt", [("bf16", "e4m3"), ("f16", "int8")])
+def test_gemm_epilogue_of_a_cut_reduction(dtype, fmt, cuda_device):
+    """The epilogue on sums of pieces: bias, activation, residual and the 8-bit
+    pre-activation, ragged rows, an output that only 2-byte stores can reach."""
+    import torch
+    from tests import gemm_reference as ref
+
+    rng = np.random.default_rng(60)
+    for rows in (301, 512):
+        args, w = ref.random_matrix(rng, 12, 2, 100, rows, 2000, "f16", True, cuda_device)
+        x = _x(rng, 33, 2000, _dtype(dtype), cuda_device)
+        bias = torch.from_numpy(rng.standard_normal(rows).astype(np.float32)).to(cuda_device)
+        res = _x(rng, 33, rows, _dtype(dtype), cuda_device, pad=1)
+        ck = tcq.Packed8(torch.empty((33, rows), dtype=torch.int8, device=cuda_device),
+                         torch.empty((33, -(-rows // 32)), dtype=torch.uint8, device=cuda_device), fmt)
+        buf = torch.full((33, rows + 3), 7.0, dtype=x.dtype, device=cuda_device)
+        y = tcq.gemm(*args, x, bias=bias, act="gelu", residual=res, checkpoint=ck, out=buf[:, 1:rows + 1])
+        check_gemm(args, w, x, y, "gelu", bias, res, ck)
+        assert (buf[:, :1] == 7).all() and (buf[:, rows + 1:] == 7).all()
+        assert torch.equal(tcq.gemm(*args, x, bias=bias, act="gelu", residual=res), y)
 
 
 def test_gemm_strides_and_alignment(cuda_device):

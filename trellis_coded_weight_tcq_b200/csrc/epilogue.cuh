@@ -1,0 +1,71 @@
+// epilogue.cuh -- a product's epilogue on sums that come from memory (the pieces of a
+// cut reduction), four columns per lane.
+#pragma once
+
+#include "gemm.cuh"
+#include "q8.cuh"
+
+namespace tcq {
+
+// Outputs (t, r .. r + 3), those below `rows`, from their sums: the powers of two, bias,
+// 8-bit checkpoint, activation and residual, rounded once.  All lanes of a warp have the
+// same t and consecutive quads, eight lanes a group of 32.  `vec`: out and residual rows
+// that 8-byte accesses can reach.
+template <int XT>
+__device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long long r, long long rows, float (&v)[4],
+                                            bool vec)
+{
+    const int lane = threadIdx.x & 31;
+    const int count = rows - r < 4 ? (rows - r > 0 ? (int)(rows - r) : 0) : 4;
+    const float rs = e.row_scale ? __ldg(e.row_scale + t) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] *= rs;
+        if (i < count) v[i] = fmaf(v[i], e.col_scale ? __ldg(e.col_scale + r + i) : 1.f, e.bias ? __ldg(e.bias + r + i) : 0.f);
+    }
+    if (e.z_codes) {  // a group of 32 is eight lanes
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool int8 = e.z_format == TCQ_Q8_INT8;
+        const uint32_t byte = int8 ? q8_scale_byte<TCQ_Q8_INT8>(top) : q8_scale_byte<TCQ_Q8_E4M3>(top);
+        const float inv = q8_inv(byte);
+        if (count > 0 && (lane & 7) == 0) e.z_scales[t * ((rows + 31) / 32) + r / 32] = (uint8_t)byte;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count)
+                e.z_codes[t * rows + r + i] = byte == 255u ? 0 : (uint8_t)(int8 ? q8_encode<TCQ_Q8_INT8>(v[i], inv)
+                                                                              : q8_encode<TCQ_Q8_E4M3>(v[i], inv));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], e.act);
+    uint16_t* out = static_cast<uint16_t*>(e.out) + t * e.ldo + r;
+    const uint16_t* res = e.residual ? static_cast<const uint16_t*>(e.residual) + t * e.ldr + r : nullptr;
+    if (vec && count == 4) {
+        if (res) {
+            const uint2 q = *reinterpret_cast<const uint2*>(res);
+            const float2 a = x_unpack2<XT>(q.x), b = x_unpack2<XT>(q.y);
+            v[0] += a.x; v[1] += a.y; v[2] += b.x; v[3] += b.y;
+        }
+        *reinterpret_cast<uint2*>(out) = make_uint2(x_pack2<XT>(v[0], v[1]), x_pack2<XT>(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) out[i] = x_bits<XT>(res ? v[i] + x_load<XT>(res, i) : v[i]);
+    }
+}
+
+// The fp32 outputs of the weight gradient.
+__device__ __forceinline__ void finish_quad_f32(const Epilogue& e, long long t, long long r, long long rows,
+                                                const float (&v)[4])
+{
+    float* out = static_cast<float*>(e.out) + t * e.ldo + r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r + i < rows) out[i] = e.accumulate ? out[i] + v[i] : v[i];
+}
+
+}  // namespace tcq

@@ -59,8 +59,10 @@ struct GemmProblem {
     int xdtype;  // output type of forward and dgrad
 };
 
-cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, int num_sms, unsigned int* err,
-                           cudaStream_t stream);
+// Workspace of a product with few tiles, whose reduction is cut into pieces (0: none).
+size_t gemm_partial_bytes(long long m, long long n, long long k, int num_sms);
+cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, float* partial, int num_sms,
+                           unsigned int* err, cudaStream_t stream);
 
 // W as binary16 [rows, ldw], each weight over its row's power of two (row_pow2[r],
 // written when the matrix has scales).
@@ -99,10 +101,9 @@ cudaError_t launch_prepare(ScaleRows a, RowPowers p, cudaStream_t stream);
 cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
                           int num_sms, cudaStream_t stream);
 
-// The forward product with the decoding inside it, for up to kFusedMaxTokens tokens:
+// The forward product with the decoding inside it, for small batches (fused_shape):
 // x binary16 [n, cols] (ldx a multiple of 8, 16-byte aligned).  `early`: the launch
 // before it in the stream is one of this call's, which it may start beside.
-constexpr long long kFusedMaxTokens = 1024;
 bool fused_shape(int T, long long rows, long long cols, long long n);
 size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms);
 cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx, long long n, int xdtype,

@@ -70,17 +70,18 @@ CodedMatrix matrix(const uint32_t* bits, const uint32_t* start, const float* sca
 // Workspace of a product: the binary16 matrix, its row powers, the binary16
 // activations (rows of `inner` elements) and theirs.
 struct GemmSpace {
-    size_t row_pow2, x, x_pow2, total;
+    size_t row_pow2, x, x_pow2, partial, total;
 };
 
-// `weights`: bytes of the binary16 matrix, or of the partial sums in its place
-GemmSpace gemm_space(size_t weights, int64_t rows, int64_t n, int64_t inner)
+// `weights`: bytes of the binary16 matrix; `partial`: of the sums of a reduction's pieces
+GemmSpace gemm_space(size_t weights, int64_t rows, int64_t n, int64_t inner, size_t partial)
 {
     GemmSpace s;
     s.row_pow2 = align256(weights);
     s.x = s.row_pow2 + align256((size_t)rows * 4);
     s.x_pow2 = s.x + align256((size_t)n * round_up(inner, 8) * 2);
-    s.total = s.x_pow2 + align256((size_t)n * 4);
+    s.partial = s.x_pow2 + align256((size_t)n * 4);
+    s.total = s.partial + align256(partial);
     return s;
 }
 
@@ -88,9 +89,28 @@ size_t matrix16_bytes(int64_t rows, int64_t cols) { return (size_t)rows * round_
 
 GemmSpace forward_space(tcq_dtype dt, int L, int T, int64_t rows, int64_t cols, int64_t n, int num_sms)
 {
-    const bool fused = fused_shape(T, rows, cols, n);
-    return gemm_space(fused ? fused_partial_bytes(code_mode(dt), L, rows, cols, n, num_sms) : matrix16_bytes(rows, cols),
-                      rows, n, cols);
+    if (fused_shape(T, rows, cols, n))
+        return gemm_space(0, rows, n, cols, fused_partial_bytes(code_mode(dt), L, rows, cols, n, num_sms));
+    return gemm_space(matrix16_bytes(rows, cols), rows, n, cols, gemm_partial_bytes(n, rows, cols, num_sms));
+}
+
+GemmSpace dgrad_space(int64_t rows, int64_t cols, int64_t n, int num_sms)
+{
+    return gemm_space(matrix16_bytes(rows, cols), rows, n, rows, gemm_partial_bytes(n, cols, rows, num_sms));
+}
+
+// The checkpoint's values, a copy of dZ (where TMA cannot read it), the pieces' sums.
+struct WgradSpace {
+    size_t dz, partial, total;
+};
+
+WgradSpace wgrad_space(int64_t rows, int64_t cols, int64_t n, int num_sms)
+{
+    WgradSpace s;
+    s.dz = align256((size_t)n * round_up(cols, 8) * 2);
+    s.partial = s.dz + align256((size_t)n * round_up(rows, 8) * 2);
+    s.total = s.partial + align256(gemm_partial_bytes(rows, cols, n, num_sms));
+    return s;
 }
 
 Epilogue plain_epilogue(void* out, int64_t ldo)
@@ -153,6 +173,7 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     float* row_pow2 = reinterpret_cast<float*>(ws + sp.row_pow2);
     float* x_pow2 = reinterpret_cast<float*>(ws + sp.x_pow2);
+    float* partial = reinterpret_cast<float*>(ws + sp.partial);
     const int64_t ldw = round_up(cols, 8);
 
     const bool fused = fused_shape(T, rows, cols, n);
@@ -194,16 +215,17 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     ep.z_scales = z_scales;
     ep.z_format = z_format;
     if (fused)
-        return status(launch_gemm_fused(w, p.a, p.lda, n, xdtype, row_pow2, reinterpret_cast<float*>(ws), ep, num_sms, err,
+        return status(launch_gemm_fused(w, p.a, p.lda, n, xdtype, row_pow2, partial, ep, num_sms, err,
                                         scaled || scale, st));
-    return status(launch_gemm_tc(kGemmForward, p, ep, num_sms, err, st));
+    return status(launch_gemm_tc(kGemmForward, p, ep, partial, num_sms, err, st));
 }
 
 size_t tcq_gemm_dgrad_workspace_bytes(int L, int k, int T, int64_t rows, int64_t cols, int64_t n, tcq_dtype cb_dtype)
 {
     if (check_matrix(cb_dtype, L, k, T, rows, cols) != TCQ_OK || !valid_dim(n) || n == 0 || rows == 0 || cols == 0)
         return 0;
-    return gemm_space(matrix16_bytes(rows, cols), rows, n, rows).total;
+    const int num_sms = sms();
+    return dgrad_space(rows, cols, n, num_sms > 0 ? num_sms : 148).total;
 }
 
 tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, const float* scale, const void* codebook,
@@ -221,14 +243,15 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
     if (!matrix_pointers(bits, start_state, scale, codebook, cb_dtype) || !valid_rows(dz, lddz, rows) || !workspace ||
         !aligned(workspace, 256))
         return TCQ_ERR_INVALID_ARG;
-    const GemmSpace sp = gemm_space(matrix16_bytes(rows, cols), rows, n, rows);
-    if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
     const int num_sms = sms();
+    const GemmSpace sp = dgrad_space(rows, cols, n, num_sms > 0 ? num_sms : 148);
+    if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
     if (num_sms <= 0) return TCQ_ERR_CUDA;
     unsigned int* err = device_error_word(st);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     float* row_pow2 = reinterpret_cast<float*>(ws + sp.row_pow2);
     float* x_pow2 = reinterpret_cast<float*>(ws + sp.x_pow2);
+    float* partial = reinterpret_cast<float*>(ws + sp.partial);
     const CodedMatrix w = matrix(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols);
     const int64_t ldw = round_up(cols, 8);
 
@@ -256,13 +279,14 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
         p.lda = ldz;
         ep.row_scale = x_pow2;
     }
-    return status(launch_gemm_tc(kGemmDgrad, p, ep, num_sms, err, st));
+    return status(launch_gemm_tc(kGemmDgrad, p, ep, partial, num_sms, err, st));
 }
 
 size_t tcq_wgrad8_workspace_bytes(int64_t rows, int64_t cols, int64_t n)
 {
     if (!valid_dim(rows) || !valid_dim(cols) || !valid_dim(n) || n == 0 || rows == 0 || cols == 0) return 0;
-    return align256((size_t)n * round_up(cols, 8) * 2) + align256((size_t)n * round_up(rows, 8) * 2);
+    const int num_sms = sms();
+    return wgrad_space(rows, cols, n, num_sms > 0 ? num_sms : 148).total;
 }
 
 tcq_status tcq_wgrad8(const void* dz, tcq_xdtype xdtype, int64_t lddz, const uint8_t* x_codes, const uint8_t* x_scales,
@@ -280,8 +304,9 @@ tcq_status tcq_wgrad8(const void* dz, tcq_xdtype xdtype, int64_t lddz, const uin
     }
     if (!valid_rows(dz, lddz, rows) || !x_codes || !x_scales || !workspace || !aligned(workspace, 256))
         return TCQ_ERR_INVALID_ARG;
-    if (workspace_bytes < tcq_wgrad8_workspace_bytes(rows, cols, n)) return TCQ_ERR_WORKSPACE;
     const int num_sms = sms();
+    const WgradSpace sp = wgrad_space(rows, cols, n, num_sms > 0 ? num_sms : 148);
+    if (workspace_bytes < sp.total) return TCQ_ERR_WORKSPACE;
     if (num_sms <= 0) return TCQ_ERR_CUDA;
     unsigned int* err = device_error_word(st);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -290,7 +315,7 @@ tcq_status tcq_wgrad8(const void* dz, tcq_xdtype xdtype, int64_t lddz, const uin
     if (e != cudaSuccess) return TCQ_ERR_CUDA;
     GemmProblem p = {dz, lddz, ws, ldq, rows, cols, n, xdtype == TCQ_X_BF16 ? 1 : 0, xdtype};
     if (!direct(dz, lddz)) {
-        unsigned char* copy = ws + align256((size_t)n * ldq * 2);
+        unsigned char* copy = ws + sp.dz;
         const int64_t ldz = round_up(rows, 8);
         e = launch_copy16(dz, lddz, n, rows, copy, ldz, num_sms, st);
         if (e != cudaSuccess) return TCQ_ERR_CUDA;
@@ -299,7 +324,7 @@ tcq_status tcq_wgrad8(const void* dz, tcq_xdtype xdtype, int64_t lddz, const uin
     }
     Epilogue ep = plain_epilogue(dw, lddw);
     ep.accumulate = accumulate != 0;
-    return status(launch_gemm_tc(kGemmWgrad, p, ep, num_sms, err, st));
+    return status(launch_gemm_tc(kGemmWgrad, p, ep, reinterpret_cast<float*>(ws + sp.partial), num_sms, err, st));
 }
 
 tcq_status tcq_pack8(const void* x, tcq_xdtype xdtype, int64_t ldx, int64_t n, int64_t cols, tcq_q8 format,

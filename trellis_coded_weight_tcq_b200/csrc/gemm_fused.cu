@@ -24,6 +24,7 @@
 // to the workspace, and a second kernel adds a tile's pieces in order and applies the
 // epilogue.  The split depends on the shape and the SM count only.
 #include "decode16.cuh"
+#include "epilogue.cuh"
 #include "gemm.cuh"
 #include "pdl.cuh"
 #include "q8.cuh"
@@ -425,46 +426,7 @@ __global__ void __launch_bounds__(256) fused_finish_kernel(Plan p, Epilogue e, l
         const float4 d = __ldcg(reinterpret_cast<const float4*>(src + (long long)i * p.np * kRows));
         v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
     }
-    const int count = rows - r < 4 ? (rows - r > 0 ? (int)(rows - r) : 0) : 4;
-    const float rs = e.row_scale ? __ldg(e.row_scale + t) : 1.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] *= rs;
-        if (i < count) v[i] = fmaf(v[i], e.col_scale ? __ldg(e.col_scale + r + i) : 1.f, e.bias ? __ldg(e.bias + r + i) : 0.f);
-    }
-    if (e.z_codes) {  // a group of 32 is eight lanes
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < count) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 4; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool int8 = e.z_format == TCQ_Q8_INT8;
-        const uint32_t byte = int8 ? q8_scale_byte<TCQ_Q8_INT8>(top) : q8_scale_byte<TCQ_Q8_E4M3>(top);
-        const float inv = q8_inv(byte);
-        if (count > 0 && (lane & 7) == 0) e.z_scales[t * ((rows + 31) / 32) + r / 32] = (uint8_t)byte;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < count)
-                e.z_codes[t * rows + r + i] = byte == 255u ? 0 : (uint8_t)(int8 ? q8_encode<TCQ_Q8_INT8>(v[i], inv)
-                                                                              : q8_encode<TCQ_Q8_E4M3>(v[i], inv));
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], e.act);
-    uint16_t* out = static_cast<uint16_t*>(e.out) + t * e.ldo + r;
-    const uint16_t* res = e.residual ? static_cast<const uint16_t*>(e.residual) + t * e.ldr + r : nullptr;
-    if (vec && count == 4) {
-        if (res) {
-            const uint2 q = *reinterpret_cast<const uint2*>(res);
-            const float2 a = x_unpack2<XT>(q.x), b = x_unpack2<XT>(q.y);
-            v[0] += a.x; v[1] += a.y; v[2] += b.x; v[3] += b.y;
-        }
-        *reinterpret_cast<uint2*>(out) = make_uint2(x_pack2<XT>(v[0], v[1]), x_pack2<XT>(v[2], v[3]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < count) out[i] = x_bits<XT>(res ? v[i] + x_load<XT>(res, i) : v[i]);
-    }
+    finish_quad<XT>(e, t, r, rows, v, vec);
 }
 
 int code_of(const CodedMatrix& w) { return w.cb_f16 == 1 ? kCode16F16 : w.cb_f16 == 0 ? kCode16F32 : kCode16Mad; }
@@ -527,10 +489,15 @@ cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtenso
 
 }  // namespace
 
-// T a multiple of 64 keeps a stage inside one block and its words together.
+// T a multiple of 64 keeps a stage inside one block and its words together.  Every 256
+// tokens decode the matrix once more, so the product that decodes ahead soon wins; up to
+// 384 tokens it does not where its 256 x 256 tiles fill less than half the SMs.  Measured,
+// here / decoded ahead, in us: 14336 x 4096 (binary16 table) 32 tokens 52 / 72, 256 tokens
+// 77 / 74, 512 tokens 140 / 92; 4096 x 14336 256 tokens 72 / 123, 257 tokens 107 / 123;
+// 4096 x 4096 256 tokens 32 / 44, 512 tokens 50 / 47.
 bool fused_shape(int T, long long rows, long long cols, long long n)
 {
-    return T % kDepth == 0 && n <= kFusedMaxTokens && (rows / kRows + 1) * ((n + 255) / 256) * (cols / 128 + 1) < (1ll << 30);
+    return T % kDepth == 0 && (n <= 256 || (n <= 384 && rows <= 4096)) && (rows / kRows + 1) * (cols / 128 + 1) < (1ll << 30);
 }
 
 size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms)

@@ -20,10 +20,16 @@
 // all tokens, takes its sums out of tensor memory every 1024 tokens and adds them in
 // registers (error against float64 at 4096 tokens: 1.6e-6 without, 8e-7 with).
 //
+// Fewer tiles than half the pairs: the reduction is cut into as many pieces as there are
+// pairs for, each writes its fp32 sums to the workspace, and a second kernel adds a
+// tile's pieces in order and applies the epilogue (32 tokens through the input gradient
+// of a 14336 x 4096 matrix have 16 tiles of 224 stages: four pieces).
+//
 // Roles: warp 0 TMA, warp 1 MMA (first CTA of the pair only), warp 2 tensor memory,
 // warps 4 and up epilogue.  Barriers: full (both CTAs' loads of a stage landed; in the
 // first CTA), empty (the MMAs that read a stage are done; in both, by a commit to
 // both), tfull / tempty (an accumulator set is complete / has been read).
+#include "epilogue.cuh"
 #include "gemm.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
@@ -109,7 +115,20 @@ struct Shape {
     long long m, n, k;
     int m_tiles, n_tiles, k_steps;
     int fmt;
+    int pieces;  // of a tile's reduction; more than one: sums go to the workspace
 };
+
+// A pair's next piece of work: its tile's first row and column, its stages.
+struct Item {
+    int m0, n0, k0, k1;
+};
+
+__device__ __forceinline__ Item work_item(const Shape& p, int t)
+{
+    const int tile = p.pieces == 1 ? t : t / p.pieces, piece = t - tile * p.pieces;
+    return {tile % p.m_tiles * kTile, tile / p.m_tiles * kTile, p.k_steps * piece / p.pieces,
+            p.k_steps * (piece + 1) / p.pieces};
+}
 
 // 32 values of one row through the epilogue: row r, columns c .. c + 31, `count` of them
 // below n.
@@ -235,14 +254,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND), 
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_out, Shape p, Epilogue e, bool vec, bool tma_out, unsigned int* err)
 {
+    // with pieces, map_out is the workspace's: [tile, piece, 256 rows] x 256 columns, fp32
     constexpr int AMN = KIND == kGemmWgrad, BMN = KIND != kGemmForward, EW = epilogue_warps(KIND);
-    const int segment = KIND == kGemmWgrad ? kSegment : p.k_steps;  // stages between two accumulator sets
+    constexpr int segment = KIND == kGemmWgrad ? kSegment : INT32_MAX / 2;  // stages between two accumulator sets
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem& S = *reinterpret_cast<Smem*>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int tiles = p.m_tiles * p.n_tiles;
+    const int items = p.m_tiles * p.n_tiles * p.pieces;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_addr(&S.full[i]), 1);
@@ -270,10 +290,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                const int m0 = (t % p.m_tiles) * kTile + (int)rank * 128;
-                const int n0 = (t / p.m_tiles) * kTile + (int)rank * 128;
-                for (int ks = 0; ks < p.k_steps; ++ks, ++it) {
+            for (int t = pair; t < items && ok; t += pairs) {
+                const Item w = work_item(p, t);
+                const int m0 = w.m0 + (int)rank * 128, n0 = w.n0 + (int)rank * 128;
+                for (int ks = w.k0; ks < w.k1; ++ks, ++it) {
                     const int s = it % kStages;
                     ok = mbar_wait(smem_addr(&S.empty[s]), ((it / kStages) & 1) ^ 1, stop, err);
                     if (!ok) break;
@@ -306,13 +326,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const uint32_t idesc = mma_idesc(256, 256, p.fmt, AMN, BMN);
             int it = 0, done = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                for (int k0 = 0; k0 < p.k_steps && ok; k0 += segment, ++done) {
+            for (int t = pair; t < items && ok; t += pairs) {
+                const Item w = work_item(p, t);
+                for (int k0 = w.k0; k0 < w.k1 && ok; k0 += segment, ++done) {
                     const int acc = done & 1;
                     ok = mbar_wait(smem_addr(&S.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
                     if (!ok) break;
                     tc_fence_after();
-                    const int k1 = k0 + segment < p.k_steps ? k0 + segment : p.k_steps;
+                    const int k1 = w.k1 - k0 > segment ? k0 + segment : w.k1;
                     for (int ks = k0; ks < k1; ++ks, ++it) {
                         const int s = it % kStages;
                         ok = mbar_wait(smem_addr(&S.full[s]), (it / kStages) & 1, stop, err);
@@ -342,14 +363,18 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         int done = 0;
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
+        for (int t = pair; t < items && ok; t += pairs) {
+            const Item w = work_item(p, t);
+            // rows and columns in the output, or in the workspace
+            const bool cut = p.pieces > 1;
+            const int out_row = cut ? t * kTile : w.m0, out_col = cut ? 0 : w.n0;
             if constexpr (KIND == kGemmWgrad) {
                 const int half = (warp - 4) >> 2;
                 unsigned char* box = S.box[warp - 4];
                 float sum[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) sum[i] = 0.f;
-                for (int k0 = 0; k0 < p.k_steps && ok; k0 += segment, ++done) {
+                for (int k0 = w.k0; k0 < w.k1 && ok; k0 += segment, ++done) {
                     const int acc = done & 1;
                     ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
                     if (!ok) break;
@@ -366,13 +391,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_addr(&S.tempty[acc]), 0));
                 }
                 if (!ok) break;
-                const int r0 = (t % p.m_tiles) * kTile + (int)rank * 128 + quarter * 32;
-                const int c0 = (t / p.m_tiles) * kTile + 128 * half;
+                const int local = (int)rank * 128 + quarter * 32, r0 = w.m0 + local;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int c = c0 + 32 * j;
+                    const int c = w.n0 + 128 * half + 32 * j;
                     if (c >= p.n || r0 >= p.m) break;  // the same in every lane
-                    if (tma_out) {
+                    if (tma_out || cut) {
                         if (lane == 0) bulk_wait_read<0>();
                         __syncwarp();
 #pragma unroll
@@ -383,10 +407,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         fence_async_shared();
                         __syncwarp();
                         if (lane == 0) {
-                            if (e.accumulate)
+                            if (e.accumulate && !cut)
                                 tma_add_2d(&map_out, smem_addr(box), c, r0);
                             else
-                                tma_store_2d(&map_out, smem_addr(box), c, r0);
+                                tma_store_2d(&map_out, smem_addr(box), out_col + c - w.n0, out_row + local);
                             bulk_commit();
                         }
                     } else if (r0 + lane < p.m) {
@@ -397,8 +421,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                 }
             } else {
-                const long long r0 = (long long)(t % p.m_tiles) * kTile + rank * 128 + quarter * 32, r = r0 + lane;
-                const long long n0 = (long long)(t / p.m_tiles) * kTile;
+                const int local = (int)rank * 128 + quarter * 32;
+                const long long r0 = w.m0 + local, r = r0 + lane, n0 = w.n0;
                 const int acc = done & 1;
                 if constexpr (KIND == kGemmForward) {
                     // this tile's columns, while its product still runs
@@ -416,8 +440,29 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 if (!ok) break;
                 tc_fence_after();
                 const float row_scale = e.row_scale && r < p.m ? __ldg(e.row_scale + r) : 1.f;
+                if (cut) {  // the sums as they are, 32 columns at a time
 #pragma unroll 1
-                for (int c = 0; c < kTile; c += 64) {
+                    for (int c = 0; c < kTile; c += 32) {
+                        if (n0 + c >= p.n || r0 >= p.m) break;
+                        unsigned char* box = S.box[2 * quarter + ((c >> 5) & 1)];
+                        if (lane == 0) bulk_wait_read<1>();
+                        __syncwarp();
+                        float v[32];
+                        tmem_load32(lanes + acc * 256 + c, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&map_out, smem_addr(box), c, out_row + local);
+                            bulk_commit();
+                        }
+                    }
+                }
+#pragma unroll 1
+                for (int c = cut ? kTile : 0; c < kTile; c += 64) {
                     if (n0 + c >= p.n || r0 >= p.m) break;  // the same in every lane
                     unsigned char* box = S.box[2 * quarter + ((c >> 6) & 1)];
                     if (tma_out) {
@@ -465,8 +510,40 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
 }
 
+// Adds a tile's pieces in order and applies the epilogue: a warp takes 128 columns of a row.
 template <int KIND, int XT>
-cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigned int* err, cudaStream_t stream)
+__global__ void __launch_bounds__(256) finish_kernel(Shape p, Epilogue e, const float* partial, bool vec)
+{
+    const int lane = threadIdx.x & 31, tile = blockIdx.x;
+    const int local = blockIdx.y * 8 + (threadIdx.x >> 5), c = blockIdx.z * 128 + 4 * lane;
+    const long long r = (long long)(tile % p.m_tiles) * kTile + local;
+    const long long n0 = (long long)(tile / p.m_tiles) * kTile;
+    if (r >= p.m || n0 + blockIdx.z * 128 >= p.n) return;
+    const float* src = partial + ((long long)tile * p.pieces * kTile + local) * kTile + c;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < p.pieces; ++i) {
+        const float4 d = __ldcg(reinterpret_cast<const float4*>(src + (long long)i * kTile * kTile));
+        v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
+    }
+    if constexpr (KIND == kGemmWgrad)
+        finish_quad_f32(e, r, n0 + c, p.n, v);
+    else
+        finish_quad<XT>(e, r, n0 + c, p.n, v, vec);
+}
+
+// Pieces of a tile's reduction: as many as there are pairs for, at least four stages each.
+int reduction_pieces(long long tiles, int k_steps, int pairs)
+{
+    if (tiles > pairs / 2) return 1;
+    int p = pairs / (int)tiles;
+    if (p > k_steps / 4) p = k_steps / 4;
+    return p < 1 ? 1 : p;
+}
+
+template <int KIND, int XT>
+cudaError_t launch(const GemmProblem& g, const Epilogue& e, float* partial, int num_sms, unsigned int* err,
+                   cudaStream_t stream)
 {
     CUtensorMap ma, mb, mo;
     const bool ok = (KIND == kGemmWgrad ? make_map_16bit(&ma, g.a, g.k, g.m, g.lda, 64)
@@ -484,36 +561,55 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, int num_sms, unsigne
     s.fmt = g.fmt;
     const int es = KIND == kGemmWgrad ? 4 : 2;
     bool vec = (reinterpret_cast<uintptr_t>(e.out) & 15) == 0 && e.ldo * es % 16 == 0;
+    const long long tiles = (long long)s.m_tiles * s.n_tiles;
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    s.pieces = reduction_pieces(tiles, s.k_steps, num_sms / 2);
     const bool tma_out = vec;
-    if (!tma_out)
+    if (s.pieces > 1) {
+        if (!make_map_out(&mo, partial, tiles * s.pieces * kTile, kTile, kTile, 4)) return cudaErrorInvalidValue;
+    } else if (!tma_out) {
         mo = ma;  // not used
-    else if (!make_map_out(&mo, e.out, g.m, g.n, e.ldo, es))
+    } else if (!make_map_out(&mo, e.out, g.m, g.n, e.ldo, es)) {
         return cudaErrorInvalidValue;
+    }
     if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 15) == 0 && e.ldr % 8 == 0;
     cudaError_t st = cudaFuncSetAttribute(gemm_kernel<KIND, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)sizeof(Smem));
     if (st != cudaSuccess) return st;
-    const long long tiles = (long long)s.m_tiles * s.n_tiles;
-    if (tiles > INT32_MAX - num_sms) return cudaErrorInvalidValue;
-    const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    const long long items = tiles * s.pieces;
+    const int pairs = (int)(items < num_sms / 2 ? items : num_sms / 2);
     gemm_kernel<KIND, XT><<<2 * pairs, gemm_threads(KIND), sizeof(Smem), stream>>>(ma, mb, mo, s, e, vec, tma_out, err);
+    st = cudaGetLastError();
+    if (st != cudaSuccess || s.pieces == 1) return st;
+    // quads: 8-byte accesses
+    bool quads = (reinterpret_cast<uintptr_t>(e.out) & 7) == 0 && e.ldo % 4 == 0;
+    if (e.residual) quads = quads && (reinterpret_cast<uintptr_t>(e.residual) & 7) == 0 && e.ldr % 4 == 0;
+    finish_kernel<KIND, XT><<<dim3((unsigned)tiles, kTile / 8, kTile / 128), 256, 0, stream>>>(s, e, partial, quads);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, int num_sms, unsigned int* err,
-                           cudaStream_t stream)
+size_t gemm_partial_bytes(long long m, long long n, long long k, int num_sms)
+{
+    const long long tiles = (m + kTile - 1) / kTile * ((n + kTile - 1) / kTile);
+    if (tiles > num_sms / 2) return 0;
+    const int pieces = reduction_pieces(tiles, (int)((k + kDepth - 1) / kDepth), num_sms / 2);
+    return pieces > 1 ? (size_t)tiles * pieces * kTile * kTile * sizeof(float) : 0;
+}
+
+cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, float* partial, int num_sms,
+                           unsigned int* err, cudaStream_t stream)
 {
     const bool bf = p.xdtype == TCQ_X_BF16;
     switch (kind) {
     case kGemmForward:
-        return bf ? launch<kGemmForward, TCQ_X_BF16>(p, e, num_sms, err, stream)
-                  : launch<kGemmForward, TCQ_X_F16>(p, e, num_sms, err, stream);
+        return bf ? launch<kGemmForward, TCQ_X_BF16>(p, e, partial, num_sms, err, stream)
+                  : launch<kGemmForward, TCQ_X_F16>(p, e, partial, num_sms, err, stream);
     case kGemmDgrad:
-        return bf ? launch<kGemmDgrad, TCQ_X_BF16>(p, e, num_sms, err, stream)
-                  : launch<kGemmDgrad, TCQ_X_F16>(p, e, num_sms, err, stream);
-    default: return launch<kGemmWgrad, TCQ_X_F16>(p, e, num_sms, err, stream);
+        return bf ? launch<kGemmDgrad, TCQ_X_BF16>(p, e, partial, num_sms, err, stream)
+                  : launch<kGemmDgrad, TCQ_X_F16>(p, e, partial, num_sms, err, stream);
+    default: return launch<kGemmWgrad, TCQ_X_F16>(p, e, partial, num_sms, err, stream);
     }
 }
 

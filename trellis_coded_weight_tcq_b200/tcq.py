@@ -602,7 +602,7 @@ def _x_dtype(t, what: str) -> int:
     """TCQ_X_* of a 2-D 16-bit CUDA tensor with unit-stride rows."""
     if t.dim() != 2 or not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel()):
         raise ValueError(f"{what} must be a 2-D CUDA tensor with unit-stride rows")
-    dtype, torch = t.dtype, _torch_module
+    dtype, torch = t.dtype, _torch()
     if dtype == torch.bfloat16:
         return TCQ_X_BF16
     if dtype == torch.float16:
