@@ -78,13 +78,13 @@ SHAPES = [  # L, k, T, rows, blocks per row, code, scaled, n, dtype
     (16, 2, 256, 2048, 16, "f16", True, 512, "bf16"),   # several tiles in every direction
     (12, 3, 64, 4099, 3, "f16", True, 2, "f16"),
     (16, 2, 256, 3000, 6, "f16", True, 100, "f16"),     # runs of stages that cut tiles, a ring of three
-    (16, 2, 128, 1500, 24, "mad", True, 1000, "bf16"),  # four token tiles, the last one short
+    (16, 2, 128, 1500, 24, "mad", True, 1000, "bf16"),
     (14, 1, 64, 2500, 9, "f32", True, 200, "f16"),
     (16, 4, 256, 20000, 1, "f16", False, 20, "bf16"),   # more row tiles than SMs, few stages each
     (8, 3, 64, 130, 1, "mad", True, 256, "f16"),        # one stage per tile
     (16, 2, 256, 520, 8, "f16", True, 1025, "bf16"),
-    (16, 2, 256, 520, 8, "mad", True, 384, "f16"),      # two token tiles, decoded as it goes
-    (16, 2, 256, 520, 8, "mad", True, 385, "bf16"),     # the first count that decodes ahead
+    (16, 2, 256, 520, 8, "mad", True, 256, "f16"),      # the largest count decoded as it goes
+    (16, 2, 256, 520, 8, "mad", True, 257, "bf16"),     # the first that decodes ahead
     (12, 2, 100, 300, 20, "f32", True, 9, "f16"),       # decoded ahead, few tiles: a cut reduction
     (16, 3, 20, 270, 130, "mad", True, 300, "bf16"),
 ]

@@ -52,9 +52,9 @@ struct Barriers {
 };
 
 struct Plan {
-    long long n;          // tokens
-    int np;               // tokens per tile, a multiple of 16
-    int row_tiles, token_tiles;
+    long long n;          // tokens, at most 256
+    int np;               // n rounded up to a multiple of 16
+    int row_tiles;
     int steps;            // units of 128 columns of a whole reduction
     long long units;      // tiles * steps
     int ctas;
@@ -170,7 +170,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
         const float* scale = nullptr;
         float inv = 1.f;  // the row's power
         auto enter_tile = [&]() {
-            const long long row = (tile % p.row_tiles) * kRows + r;
+            const long long row = tile * kRows + r;
             bits = row < w.rows ? w.bits + row * (cols / 32 * K) : nullptr;
             start = w.start_state + row * nb;
             scale = w.scale ? w.scale + row * nb : nullptr;
@@ -318,7 +318,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                 mbar_expect_tx(full, p.per * bbytes);
                 for (int h = 0; h < p.per; ++h)
                     tma_load_2d(smem_addr(ring + slot * sbytes + p.per * kABytes + h * bbytes), &map_x, full,
-                                (ks + h) * kDepth, (int)(tile / p.row_tiles) * p.np);
+                                (ks + h) * kDepth, 0);
                 ks += p.per;
                 if (ks == 2 * p.steps) {
                     ks = 0;
@@ -345,7 +345,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                 // 16 k bytes per unit: every copy starts on a 16-byte boundary; before a row's
                 // first word and behind its last the box is filled with zeros
                 tma_load_2d(smem_addr(boxes + g * kRows * RB), &map_words, go, 4 * K * ks - 4,
-                            (int)(tile % p.row_tiles) * kRows);
+                            (int)tile * kRows);
                 if (++ks == p.steps) {
                     ks = 0;
                     ++tile;
@@ -414,12 +414,11 @@ __global__ void __launch_bounds__(256) fused_finish_kernel(Plan p, Epilogue e, l
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const long long tile = blockIdx.x;
-    const long long t = (tile / p.row_tiles) * p.np + (long long)blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int local = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (local >= p.np || t >= p.n) return;
-    const long long r = (tile % p.row_tiles) * kRows + 4 * lane;
+    const int t = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (t >= p.n) return;
+    const long long r = tile * kRows + 4 * lane;
     const int pieces = cta_of(p, (tile + 1) * p.steps - 1) - cta_of(p, tile * p.steps) + 1;
-    const float* src = partial + (tile * p.pieces * p.np + local) * kRows + 4 * lane;
+    const float* src = partial + (tile * p.pieces * p.np + t) * kRows + 4 * lane;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = 0; i < pieces; ++i) {
@@ -436,12 +435,10 @@ Plan make_plan(int code, int L, int K, long long rows, long long cols, long long
 {
     Plan p;
     p.n = n;
-    const long long tt = (n + 255) / 256;
-    p.token_tiles = (int)tt;
-    p.np = (int)(((n + tt - 1) / tt + 15) / 16 * 16);
+    p.np = (int)((n + 15) / 16 * 16);
     p.row_tiles = (int)((rows + kRows - 1) / kRows);
     p.steps = (int)((cols + 127) / 128);
-    p.units = (long long)p.row_tiles * p.token_tiles * p.steps;
+    p.units = (long long)p.row_tiles * p.steps;
     // at least two units per CTA, one for each group of decoding warps
     long long ctas = (p.units + 1) / 2;
     if (ctas > num_sms) ctas = num_sms;
@@ -463,21 +460,21 @@ Plan make_plan(int code, int L, int K, long long rows, long long cols, long long
 }
 
 template <int K, int CODE>
-cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p, const float* row_pow2, float* partial,
-                   unsigned int* err, bool early, cudaStream_t stream)
+cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p,
+                   const float* row_pow2, float* partial, unsigned int* err, bool early, cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(fused_kernel<K, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemBytes);
     if (e != cudaSuccess) return e;
-    const size_t smem = p.table + (size_t)kSlots * p.per * (kABytes + p.np * kDepth * 2) + 2 * p.boxes * kRows * box_row_bytes(K) +
-                        sizeof(Barriers);
+    const size_t smem = p.table + (size_t)kSlots * p.per * (kABytes + p.np * kDepth * 2) +
+                        2 * p.boxes * kRows * box_row_bytes(K) + sizeof(Barriers);
     return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, words, p, row_pow2,
                       partial, err);
 }
 
 template <int CODE>
-cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p, const float* row_pow2, float* partial,
-                     unsigned int* err, bool early, cudaStream_t stream)
+cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p,
+                     const float* row_pow2, float* partial, unsigned int* err, bool early, cudaStream_t stream)
 {
     switch (w.K) {
     case 1: return launch<1, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
@@ -489,22 +486,21 @@ cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtenso
 
 }  // namespace
 
-// T a multiple of 64 keeps a stage inside one block and its words together.  Every 256
-// tokens decode the matrix once more, so the product that decodes ahead soon wins; up to
-// 384 tokens it does not where its 256 x 256 tiles fill less than half the SMs.  Measured,
-// here / decoded ahead, in us: 14336 x 4096 (binary16 table) 32 tokens 52 / 72, 256 tokens
-// 77 / 74, 512 tokens 140 / 92; 4096 x 14336 256 tokens 72 / 123, 257 tokens 107 / 123;
-// 4096 x 4096 256 tokens 32 / 44, 512 tokens 50 / 47.
+// T a multiple of 64 keeps a stage inside one block and its words together.  More than
+// 256 tokens would decode the matrix again, and the product that decodes ahead wins.
+// Measured, here / decoded ahead, in us: 14336 x 4096 (binary16 table) 32 tokens 52 / 72,
+// 256 tokens 77 / 74, 257 tokens 112 / 90; 4096 x 14336 257 tokens 107 / 86; 4096 x 4096
+// 32 tokens 24 / 29, 257 tokens 41 / 37.
 bool fused_shape(int T, long long rows, long long cols, long long n)
 {
-    return T % kDepth == 0 && (n <= 256 || (n <= 384 && rows <= 4096)) && (rows / kRows + 1) * (cols / 128 + 1) < (1ll << 30);
+    return T % kDepth == 0 && n <= 256 && (rows / kRows + 1) * (cols / 128 + 1) < (1ll << 30);
 }
 
 size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms)
 {
     const int code = cb_f16 == 1 ? kCode16F16 : cb_f16 == 0 ? kCode16F32 : kCode16Mad;
     const Plan p = make_plan(code, L, 1, rows, cols, n, num_sms, false);  // the pieces do not depend on the ring
-    return (size_t)p.row_tiles * p.token_tiles * p.pieces * p.np * kRows * sizeof(float);
+    return (size_t)p.row_tiles * p.pieces * p.np * kRows * sizeof(float);
 }
 
 cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx, long long n, int xdtype,
@@ -527,7 +523,7 @@ cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx
     if (st != cudaSuccess) return st;
     bool vec = (reinterpret_cast<uintptr_t>(e.out) & 7) == 0 && e.ldo % 4 == 0;
     if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 7) == 0 && e.ldr % 4 == 0;
-    const dim3 grid((unsigned)(p.row_tiles * p.token_tiles), (unsigned)((p.np + 7) / 8));
+    const dim3 grid((unsigned)p.row_tiles, (unsigned)((p.np + 7) / 8));
     return launch_pdl(xdtype == TCQ_X_BF16 ? fused_finish_kernel<TCQ_X_BF16> : fused_finish_kernel<TCQ_X_F16>, grid,
                       dim3(256), 0, stream, true, p, e, w.rows, static_cast<const float*>(partial), vec);
 }
