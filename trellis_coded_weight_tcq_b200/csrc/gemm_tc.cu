@@ -92,7 +92,7 @@ constexpr int kTile = 256;            // rows and columns of a pair's tile
 constexpr int kDepth = 64;            // reduction depth of a stage
 constexpr int kHalfBytes = 128 * kDepth * 2;  // one CTA's half of one operand's stage
 constexpr int kBoxBytes = 32 * 128;   // a warp's box of the output: 32 rows of 128 bytes
-constexpr int kSegment = 16;          // stages (1024 deep) that the weight gradient sums in tensor memory
+constexpr int kSegment = 20;          // stages (1280 deep) at most that the weight gradient sums in tensor memory
 
 // Four epilogue warps, two boxes each; the weight gradient has eight with one box, a
 // half of the tile's columns each, because they hold their sums in registers.
@@ -256,7 +256,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 {
     // with pieces, map_out is the workspace's: [tile, piece, 256 rows] x 256 columns, fp32
     constexpr int AMN = KIND == kGemmWgrad, BMN = KIND != kGemmForward, EW = epilogue_warps(KIND);
-    constexpr int segment = KIND == kGemmWgrad ? kSegment : INT32_MAX / 2;  // stages between two accumulator sets
+    // stages between two accumulator sets: equal parts of at most kSegment, or all
+    const int parts = KIND == kGemmWgrad ? (p.k_steps + kSegment * p.pieces - 1) / (kSegment * p.pieces) : 1;
+    const int segment = (p.k_steps + p.pieces * parts - 1) / (p.pieces * parts) + (p.pieces > 1);
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem& S = *reinterpret_cast<Smem*>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

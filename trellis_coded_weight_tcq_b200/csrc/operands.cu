@@ -98,12 +98,19 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(ScaleRows a, RowPower
     pdl_wait();  // ends after the launch that it ran beside
 }
 
-// One CTA per row (or several rows in turn).
+// One CTA per row (or several rows in turn); eight elements per thread and step, read
+// one by one (the rows start anywhere), written together.
 __global__ void __launch_bounds__(kThreads) copy16_kernel(const uint16_t* x, long long ldx, long long n, long long cols,
                                                           uint16_t* out, long long ldo)
 {
     for (long long r = blockIdx.x; r < n; r += gridDim.x)
-        for (long long c = threadIdx.x; c < cols; c += kThreads) out[r * ldo + c] = x[r * ldx + c];
+        for (long long c = 8ll * threadIdx.x; c < cols; c += 8 * kThreads) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? x[r * ldx + c + i] : 0u;
+            *reinterpret_cast<uint4*>(out + r * ldo + c) =
+                make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        }
 }
 
 }  // namespace
