@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) unpack8_kernel(const uint8_t* codes,
 constexpr int kRowThreads = 8;
 
 template <int XT, int FMT, int ACT, int CPT>
-__global__ void __launch_bounds__(kThreads, 3) act_grad8_kernel(ActGradArgs a)
+__global__ void __launch_bounds__(kThreads, 4) act_grad8_kernel(ActGradArgs a)
 {
     __shared__ float part[kRowThreads][32 * CPT + 1];
     const int ct = threadIdx.x & 31, rt = threadIdx.x >> 5;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad8_kernel(ActGradArgs a)
 #pragma unroll
     for (int i = 0; i < P; ++i) sum[i] = f2(0.f, 0.f);
     if (c < a.rows) {
-        // a row's loads, two rows ahead of their use
+        // a row's loads, one row ahead of their use
         struct Row {
             uint4 d;
             uint2 z;
@@ -213,9 +213,9 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad8_kernel(ActGradArgs a)
             return v;
         };
         uint16_t* dz = static_cast<uint16_t*>(a.dz) + first * a.lddz + c;
-        Row now = fetch(), next = fetch();
+        Row now = fetch();
         for (; rows > 0; --rows) {
-            const Row after = fetch();
+            const Row next = fetch();
             float z[8];
             float s = 0.f;
             if constexpr (ACT != TCQ_ACT_NONE) {
@@ -242,7 +242,6 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad8_kernel(ActGradArgs a)
                 *dz = (uint16_t)o[0];
             dz += kRowThreads * a.lddz;
             now = next;
-            next = after;
         }
     }
     if (!a.partial) return;  // the same in every thread
