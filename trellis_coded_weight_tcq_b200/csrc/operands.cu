@@ -95,7 +95,9 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(ScaleRows a, RowPower
         const long long r = (blockIdx.x - a.n) * (kThreads / 32) + (threadIdx.x >> 5);
         if (r < p.rows) row_power(p, r);
     }
-    pdl_wait();  // ends after the launch that it ran beside
+    // The grid ends after the launch that it ran beside: one CTA waits for that (if all
+    // did, they would hold the places of the rows behind them).
+    if (blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // One CTA per row (or several rows in turn); eight elements per thread and step, read
