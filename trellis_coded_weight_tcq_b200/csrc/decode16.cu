@@ -187,11 +187,11 @@ cudaError_t launch_k(const CodedMatrix& w, void* out, long long ldw, const float
 
 }  // namespace
 
-cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, int num_sms,
-                            cudaStream_t stream)
+cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, uint8_t* row_exponents,
+                            int num_sms, cudaStream_t stream)
 {
     if (w.scale) {
-        const cudaError_t e = launch_prepare({}, {w.scale, w.rows, (int)(w.cols / w.T), row_pow2}, stream);
+        const cudaError_t e = launch_prepare({}, {w.scale, w.rows, (int)(w.cols / w.T), row_pow2, row_exponents}, stream);
         if (e != cudaSuccess) return e;
     }
     switch (w.cb_f16) {

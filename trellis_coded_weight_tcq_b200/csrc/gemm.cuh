@@ -64,20 +64,21 @@ size_t gemm_partial_bytes(long long m, long long n, long long k, int num_sms);
 cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, float* partial, int num_sms,
                            unsigned int* err, cudaStream_t stream);
 
-// W as binary16 [rows, ldw], each weight over its row's power of two (row_pow2[r],
-// written when the matrix has scales).
-cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, int num_sms,
-                            cudaStream_t stream);
+// W as binary16 [rows, ldw], each weight over its row's power of two (row_pow2[r] and its
+// exponent field row_exponents[r], or nullptr; written when the matrix has scales).
+cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, uint8_t* row_exponents,
+                            int num_sms, cudaStream_t stream);
 
-// x [n, cols] as binary16 rows over a power of two each (row_pow2[n]); col_pow2 (or
-// nullptr) multiplies the columns first.  `early`: the launch before it in the stream is
-// one of this call's (launch_decode16), which it may run beside; col_pow2 may then be the
-// row powers that launch_decode16 read.
+// x [n, cols] as binary16 rows over a power of two each (row_pow2[n]).  col_exponents (or
+// nullptr, 8-byte aligned): fp32 exponent fields of powers of two that multiply the
+// columns first.  `early`: the launch before it in the stream is one of this call's
+// (launch_decode16), which it may run beside; the exponents may then be those of the row
+// powers that launch_decode16 read.
 struct ScaleRows {
     const void* x = nullptr;
     int xdtype = TCQ_X_F16;
     long long ldx = 0, n = 0, cols = 0;
-    const float* col_pow2 = nullptr;
+    const uint8_t* col_exponents = nullptr;
     void* out = nullptr;
     long long ldo = 0;
     float* row_pow2 = nullptr;
@@ -86,12 +87,13 @@ struct ScaleRows {
 };
 
 // out[r] for the rows of a coded matrix, per_row scales each: the least power of two
-// above the largest finite |scale|.
+// above the largest finite |scale|, and its exponent field (or nullptr).
 struct RowPowers {
     const float* scale = nullptr;
     long long rows = 0;
     int per_row = 0;
     float* out = nullptr;
+    uint8_t* exponents = nullptr;
 };
 
 // Either or both (n == 0 or rows == 0: not wanted), in one launch.

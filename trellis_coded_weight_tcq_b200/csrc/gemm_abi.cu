@@ -70,7 +70,7 @@ CodedMatrix matrix(const uint32_t* bits, const uint32_t* start, const float* sca
 // Workspace of a product: the binary16 matrix, its row powers, the binary16
 // activations (rows of `inner` elements) and theirs.
 struct GemmSpace {
-    size_t row_pow2, x, x_pow2, partial, total;
+    size_t row_pow2, row_exponents, x, x_pow2, partial, total;
 };
 
 // `weights`: bytes of the binary16 matrix; `partial`: of the sums of a reduction's pieces
@@ -78,7 +78,8 @@ GemmSpace gemm_space(size_t weights, int64_t rows, int64_t n, int64_t inner, siz
 {
     GemmSpace s;
     s.row_pow2 = align256(weights);
-    s.x = s.row_pow2 + align256((size_t)rows * 4);
+    s.row_exponents = s.row_pow2 + align256((size_t)rows * 4);
+    s.x = s.row_exponents + align256((size_t)rows);
     s.x_pow2 = s.x + align256((size_t)n * round_up(inner, 8) * 2);
     s.partial = s.x_pow2 + align256((size_t)n * 4);
     s.total = s.partial + align256(partial);
@@ -198,10 +199,10 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     cudaError_t e = cudaSuccess;
     if (fused) {
         RowPowers rp;
-        if (scale) rp = {scale, rows, (int)(cols / T), row_pow2};
+        if (scale) rp = {scale, rows, (int)(cols / T), row_pow2, nullptr};
         if (scaled || scale) e = launch_prepare(sx, rp, st);
     } else {
-        e = launch_decode16(w, ws, ldw, row_pow2, num_sms, st);
+        e = launch_decode16(w, ws, ldw, row_pow2, nullptr, num_sms, st);
         sx.early = true;
         if (e == cudaSuccess && scaled) e = launch_prepare(sx, {}, st);
     }
@@ -255,7 +256,8 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
     const CodedMatrix w = matrix(bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols);
     const int64_t ldw = round_up(cols, 8);
 
-    cudaError_t e = launch_decode16(w, ws, ldw, row_pow2, num_sms, st);
+    uint8_t* row_exponents = ws + sp.row_exponents;
+    cudaError_t e = launch_decode16(w, ws, ldw, row_pow2, row_exponents, num_sms, st);
     if (e != cudaSuccess) return TCQ_ERR_CUDA;
     GemmProblem p = {dz, lddz, ws, ldw, n, cols, rows, 0, xdtype};
     Epilogue ep = plain_epilogue(dx, lddx);
@@ -268,7 +270,7 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
         sx.ldx = lddz;
         sx.n = n;
         sx.cols = rows;
-        sx.col_pow2 = scale ? row_pow2 : nullptr;
+        sx.col_exponents = scale ? row_exponents : nullptr;
         sx.out = ws + sp.x;
         sx.ldo = ldz;
         sx.row_pow2 = x_pow2;

@@ -24,8 +24,15 @@ __device__ __forceinline__ void row_power(const RowPowers& p, long long r)
     for (int j = threadIdx.x & 31; j < p.per_row; j += 32)
         top = max(top, finite_magnitude(__ldg(p.scale + r * p.per_row + j)));
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) p.out[r] = pow2_clamped(power_above(top));
+    if ((threadIdx.x & 31) == 0) {
+        const float v = pow2_clamped(power_above(top));
+        p.out[r] = v;
+        if (p.exponents) p.exponents[r] = (uint8_t)(__float_as_uint(v) >> 23);
+    }
 }
+
+// The power of two with this exponent field.
+__device__ __forceinline__ float power_of(uint32_t exponent) { return __uint_as_float(exponent << 23); }
 
 // One CTA per row: the row's largest finite magnitude, then the row over the power of
 // two that brings it to [2^14, 2^15).
@@ -45,11 +52,13 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
             f[2 * h] = t.x;
             f[2 * h + 1] = t.y;
         }
-        if (a.col_pow2) {
-            const float4 p = *reinterpret_cast<const float4*>(a.col_pow2 + c);
-            const float4 q = *reinterpret_cast<const float4*>(a.col_pow2 + c + 4);
-            f[0] *= p.x; f[1] *= p.y; f[2] *= p.z; f[3] *= p.w;
-            f[4] *= q.x; f[5] *= q.y; f[6] *= q.z; f[7] *= q.w;
+        if (a.col_exponents) {  // bytes: as fp32 powers they would be twice the row's own traffic
+            const uint2 e = *reinterpret_cast<const uint2*>(a.col_exponents + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i] *= power_of((e.x >> (8 * i)) & 0xffu);
+                f[4 + i] *= power_of((e.y >> (8 * i)) & 0xffu);
+            }
         }
     };
     const long long vcols = a.vec ? a.cols / 8 * 8 : 0;
@@ -60,7 +69,7 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
         for (int i = 0; i < 8; ++i) top = max(top, finite_magnitude(f[i]));
     }
     for (long long c = vcols + threadIdx.x; c < a.cols; c += kThreads)
-        top = max(top, finite_magnitude(x_load<XT>(xr, c) * (a.col_pow2 ? a.col_pow2[c] : 1.f)));
+        top = max(top, finite_magnitude(x_load<XT>(xr, c) * (a.col_exponents ? power_of(a.col_exponents[c]) : 1.f)));
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
     __syncthreads();
@@ -81,7 +90,7 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
         *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     for (long long c = vcols + threadIdx.x; c < a.cols; c += kThreads)
-        o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (a.col_pow2 ? a.col_pow2[c] : 1.f) * inv);
+        o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (a.col_exponents ? power_of(a.col_exponents[c]) : 1.f) * inv);
 }
 
 // CTAs below a.n scale a row of activations each, the others take eight rows of W.
