@@ -377,12 +377,13 @@ tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 forma
  *     Z[i, r] = sum_c X[i, c] W[r, c] + bias[r],   Y[i, r] = act(Z[i, r]) + residual[i, r]
  * computed in fp32 and rounded once to xdtype.
  *
- * The products run on the tensor cores with both operands in binary16: a weight is
- * its codeword times its block's scale rounded once to binary16 (exact without
- * scales for a binary16 table and the computed code), relative to a power of two
- * per row of W; a bfloat16 row of X is scaled to binary16 by a power of two of its
- * own, exactly for elements above 2^-32 of the row's largest and within 2^-39 of
- * that largest for the others.  Sums are fp32.  A single token (n == 1, no checkpoint
+ * The products run on the tensor cores with both operands in 16 bits and fp32 sums.
+ * More than 256 tokens of bfloat16 multiply in bfloat16, a weight being its codeword
+ * times its block's scale rounded once.  All others multiply in binary16: a weight is
+ * rounded once to binary16 (exact without scales for a binary16 table and the computed
+ * code), relative to a power of two per row of W; a bfloat16 row of X is scaled to
+ * binary16 by a power of two of its own, exactly for elements above 2^-32 of the row's
+ * largest and within 2^-39 of that largest for the others.  A single token (n == 1, no checkpoint
  * of Z) takes tcq_gemv's kernels, with both operands in fp32.
  *
  *   bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols  as tcq_gemv

@@ -38,19 +38,27 @@ def random_matrix(rng, L, k, T, rows, cols, code, scaled, device, small_scales=F
     return args, torch.from_numpy(values).to(device)
 
 
-def product_bound(a, b, rounded):
+def weight_half_step(n, dtype, exact):
+    """Half a step of the weights' rounding: to bfloat16 (2^-8) for more than 256 tokens of
+    that type, else to binary16 (2^-11), 0 where binary16 holds them."""
+    if dtype == torch.bfloat16 and n > 256:
+        return 2.0**-8
+    return 0.0 if exact else 2.0**-11
+
+
+def product_bound(a, b, half):
     """Bound of |computed - exact| for a @ b.T summed by the tensor cores.
 
     A 16-deep MMA adds its products and the running sum in fp32 with a few roundings
-    or truncations: 2^-22 of the sum of magnitudes per MMA is allowed.  ``rounded``:
-    one operand was rounded to binary16, each term off by at most half a step, 2^-11,
-    independently: 8 standard deviations' worth by Hoeffding's bound (a chance of
-    3e-14 per element), and subnormals by 2^-25 of an operand's unit (the operands are
-    scaled to below 1 and 2^15).  A scaled row of ``a`` is within 2^-39 of its largest."""
+    or truncations: 2^-22 of the sum of magnitudes per MMA is allowed.  ``half``: the
+    weights were rounded, each term off by at most this half step, independently: 8
+    standard deviations' worth by Hoeffding's bound (a chance of 3e-14 per element), and
+    binary16 subnormals by 2^-25 of an operand's unit (the operands are scaled to below 1
+    and 2^15).  A scaled row of ``a`` is within 2^-39 of its largest."""
     mags = a.abs() @ b.abs().T
     bound = (a.shape[1] / 16 + 2) * 2.0**-22 * mags
-    if rounded:
-        bound = bound + 8 * 2.0**-11 * ((a * a) @ (b * b).T).sqrt()
+    if half:
+        bound = bound + 8 * half * ((a * a) @ (b * b).T).sqrt()
         bound = bound + 2.0**-24 * a.abs().sum(1, keepdim=True) * b.abs().amax(1)[None, :]
     return bound + 2.0**-39 * a.abs().amax(1, keepdim=True) * b.abs().sum(1)[None, :]
 

@@ -35,13 +35,15 @@ def _check(got, want, bound, what):
     assert worst <= 1, f"{what}: {worst:.3g} times its bound"
 
 
-def check_gemm(args, w, x, y, act="none", bias=None, residual=None, checkpoint=None):
+def check_gemm(args, w, x, y, act="none", bias=None, residual=None, checkpoint=None, tokens=None):
+    # tokens: of the call, where x and y are a part of it
     import torch
     from tests import gemm_reference as ref
 
     xd = x.double()
     z = xd @ w.T
-    bz = ref.product_bound(xd, w, args[2] is not None or (args[3] is not tcq.MAD and args[3].dtype == torch.float32))
+    exact = args[2] is None and (args[3] is tcq.MAD or args[3].dtype == torch.float16)
+    bz = ref.product_bound(xd, w, ref.weight_half_step(tokens or x.shape[0], x.dtype, exact))
     if bias is not None:
         z = z + bias.double()
     bz = bz + 2.0**-23 * z.abs() + 1e-300
@@ -111,7 +113,8 @@ def test_gemm_dgrad(L, k, T, rows, nb, code, scaled, n, dtype, cuda_device):
     dx = tcq.gemm_dgrad(*args, dz)
     d = dz.double()
     want = d @ w
-    bound = ref.product_bound(d, w.T.contiguous(), scaled or code == "f32") + 1e-300
+    half = ref.weight_half_step(n, dz.dtype, not scaled and code != "f32")
+    bound = ref.product_bound(d, w.T.contiguous(), half) + 1e-300
     if scaled:  # a weight's subnormal error is relative to its row's power
         bound = bound + 2.0**-24 * (d.abs() @ w.abs().amax(1, keepdim=True))
     bound = bound + ref.half_step(dz.dtype) * (want.abs() + bound) + (2.0**-25 if dz.dtype == torch.float16 else 0)

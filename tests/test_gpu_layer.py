@@ -86,9 +86,10 @@ def test_block_forward_and_backward(n, dtype, cuda_device):
     dhd = g.double() @ down.w
     step = ref.packed_values(up.z8).abs().amax(1, keepdim=True) / 126
     u = 2.0**-8 if dtype == "bf16" else 2.0**-11
-    dz_off = dhd.abs() * (0.5 * step + 1.1 * 2 * u) + 1.1 * 8 * 2.0**-11 * dhd.norm(dim=1, keepdim=True) / 16
+    half = ref.weight_half_step(n, dt, False)
+    dz_off = dhd.abs() * (0.5 * step + 1.1 * 2 * u) + 1.1 * 8 * half * dhd.norm(dim=1, keepdim=True) / 16
     dx_off = dz_off @ up.w.abs()
-    dx_off = dx_off + 2 * u * dx.double().abs() + 2.0**-11 * (dhd.abs() @ up.w.abs())
+    dx_off = dx_off + 2 * u * dx.double().abs() + half * (dhd.abs() @ up.w.abs())
     # the errors of different elements are independent of vx: 6 standard deviations
     off_x = 6 * float((dx_off * vx).norm())
     off_b = 6 * float((dz_off * vb).norm())

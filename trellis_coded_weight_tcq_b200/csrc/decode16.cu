@@ -1,12 +1,13 @@
-// decode16.cu -- a trellis-coded matrix written out as binary16, the operand of
-// the tensor-core products for batches too large to decode inside the product.
+// decode16.cu -- a trellis-coded matrix written out in 16 bits, the operand of the
+// tensor-core products for batches too large to decode inside the product.
 //
 // A weight is scale * c[s], rounded once to binary16.  So that small scales do not
 // fall into binary16's subnormals, every row is divided by a power of two, the
 // least above its largest finite |scale|: the scales that multiply the codewords
 // are then below 1 and a product never overflows where the codeword does not.  The
 // products multiply the power back in (exactly).  Without scales a binary16 or
-// computed codeword is stored as it is.
+// computed codeword is stored as it is.  For large bfloat16 batches the weights are
+// rounded once to bfloat16 instead, as they are: its range needs no powers.
 //
 // A warp takes 256 columns of a row at a time, eight per lane: their windows lie in
 // two stream words, one 16-byte store per lane; each warp has a contiguous run.  Table
@@ -28,7 +29,7 @@ constexpr int kAhead = 4;   // steps whose words are loaded together
 // Blocks of whole 32s: a row's stream words follow one another without gaps, so a lane's
 // words lie 8 k apart from unit to unit and its window offset never changes.  The next
 // four units' words load while the current four are decoded.
-template <int K, int CODE>
+template <int K, int CODE, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix w, uint16_t* out, long long ldw,
                                                                     const float* row_pow2)
 {
@@ -86,13 +87,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix 
             ++row;
         }
         if (left > 0) fetch(nxt, row, at);
-        const float inv = w.scale ? inverse_pow2(__ldg(row_pow2 + r)) : 1.f;
+        const float inv = !BF16 && w.scale ? inverse_pow2(__ldg(row_pow2 + r)) : 1.f;
         uint16_t* dst = out + r * ldw + a * kUnit + 8 * lane;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (i >= n) break;
             uint32_t v[4];
-            decode_weights<K, 8, CODE>(cur.hi[i], cur.lo[i], down, mask, sm, cur.sc[i] * inv, v);
+            decode_weights<K, 8, CODE, BF16>(cur.hi[i], cur.lo[i], down, mask, sm, cur.sc[i] * inv, v);
             // ldw is cols rounded up to 8: a lane's eight columns are all stored or none is
             if ((a + i) * kUnit + 8 * lane < cols && TCQ_IN_BOUNDS(dst - out + i * kUnit + 7, w.rows * ldw))
                 *reinterpret_cast<uint4*>(dst + i * kUnit) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix 
 }
 
 // Any block of whole quads; N = 8: whole eights, 4: two reads per lane.
-template <int K, int CODE, int N>
+template <int K, int CODE, int N, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, uint16_t* out, long long ldw,
                                                                const float* row_pow2)
 {
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
     long long row = u0 / upr;
     int at = (int)(u0 - row * upr);
     for (long long u = u0; u < u1; ++u) {
-        const float inv = w.scale ? inverse_pow2(__ldg(row_pow2 + row)) : 1.f;
+        const float inv = !BF16 && w.scale ? inverse_pow2(__ldg(row_pow2 + row)) : 1.f;
         const int c = at * kUnit + 8 * lane;
         uint32_t v[4];
 #pragma unroll
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
                     sc = w.scale ? __ldg(w.scale + b) * inv : 1.f;
                 }
             }
-            decode_weights<K, N, CODE>(hi, lo, down, mask, sm, sc, v + N / 2 * h);
+            decode_weights<K, N, CODE, BF16>(hi, lo, down, mask, sm, sc, v + N / 2 * h);
         }
         if (c < cols && TCQ_IN_BOUNDS(row * ldw + c + 7, w.rows * ldw))
             *reinterpret_cast<uint4*>(out + row * ldw + c) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -155,33 +156,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
     }
 }
 
-template <int K, int CODE>
+template <int K, int CODE, bool BF16>
 cudaError_t launch(const CodedMatrix& w, void* out, long long ldw, const float* row_pow2, int num_sms,
                    cudaStream_t stream)
 {
     typedef void (*Kernel)(CodedMatrix, uint16_t*, long long, const float*);
-    const Kernel kernel = w.T % 32 == 0  ? Kernel(decode16_rows_kernel<K, CODE>)
-                          : w.T % 8 == 0 ? Kernel(decode16_kernel<K, CODE, 8>)
-                                         : Kernel(decode16_kernel<K, CODE, 4>);
+    const Kernel kernel = w.T % 32 == 0  ? Kernel(decode16_rows_kernel<K, CODE, BF16>)
+                          : w.T % 8 == 0 ? Kernel(decode16_kernel<K, CODE, 8, BF16>)
+                                         : Kernel(decode16_kernel<K, CODE, 4, BF16>);
     const size_t smem = table_bytes(CODE, w.L);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const long long units = (w.cols + kUnit - 1) / kUnit * w.rows;
     const long long need = (units + kThreads / 32 - 1) / (kThreads / 32);
     const int grid = (int)(need < num_sms ? need : num_sms);
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, w.scale != nullptr, w,
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, !BF16 && w.scale, w,
                       static_cast<uint16_t*>(out), ldw, row_pow2);
 }
 
-template <int CODE>
+template <int CODE, bool BF16>
 cudaError_t launch_k(const CodedMatrix& w, void* out, long long ldw, const float* row_pow2, int num_sms,
                      cudaStream_t stream)
 {
     switch (w.K) {
-    case 1: return launch<1, CODE>(w, out, ldw, row_pow2, num_sms, stream);
-    case 2: return launch<2, CODE>(w, out, ldw, row_pow2, num_sms, stream);
-    case 3: return launch<3, CODE>(w, out, ldw, row_pow2, num_sms, stream);
-    default: return launch<4, CODE>(w, out, ldw, row_pow2, num_sms, stream);
+    case 1: return launch<1, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
+    case 2: return launch<2, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
+    case 3: return launch<3, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
+    default: return launch<4, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
     }
 }
 
@@ -195,9 +196,18 @@ cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, floa
         if (e != cudaSuccess) return e;
     }
     switch (w.cb_f16) {
-    case kMadCodebook: return launch_k<kCode16Mad>(w, out, ldw, row_pow2, num_sms, stream);
-    case 1: return launch_k<kCode16F16>(w, out, ldw, row_pow2, num_sms, stream);
-    default: return launch_k<kCode16F32>(w, out, ldw, row_pow2, num_sms, stream);
+    case kMadCodebook: return launch_k<kCode16Mad, false>(w, out, ldw, row_pow2, num_sms, stream);
+    case 1: return launch_k<kCode16F16, false>(w, out, ldw, row_pow2, num_sms, stream);
+    default: return launch_k<kCode16F32, false>(w, out, ldw, row_pow2, num_sms, stream);
+    }
+}
+
+cudaError_t launch_decode_bf16(const CodedMatrix& w, void* out, long long ldw, int num_sms, cudaStream_t stream)
+{
+    switch (w.cb_f16) {
+    case kMadCodebook: return launch_k<kCode16Mad, true>(w, out, ldw, nullptr, num_sms, stream);
+    case 1: return launch_k<kCode16F16, true>(w, out, ldw, nullptr, num_sms, stream);
+    default: return launch_k<kCode16F32, true>(w, out, ldw, nullptr, num_sms, stream);
     }
 }
 

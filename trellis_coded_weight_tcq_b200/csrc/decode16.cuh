@@ -2,6 +2,8 @@
 // kernel that writes the matrix out and the product that decodes as it goes.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "codes.cuh"
 
 namespace tcq {
@@ -67,9 +69,21 @@ __device__ __forceinline__ float codeword_at(const unsigned char* tab, uint32_t 
         return *reinterpret_cast<const float*>(tab + offset);
 }
 
-// N weights, scale * c[s] rounded once to binary16, in pairs (the first in the low half);
-// `down`: stream bits of lo behind the last window.
-template <int K, int N, int CODE>
+// Two weights rounded once to binary16, or to bfloat16 (the first in the low half).
+template <bool BF16>
+__device__ __forceinline__ uint32_t weight_pair(float a, float b)
+{
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// N weights, scale * c[s], in pairs; `down`: stream bits of lo behind the last window.
+template <int K, int N, int CODE, bool BF16>
 __device__ __forceinline__ void decode_weights(uint32_t hi, uint32_t lo, int down, uint32_t mask,
                                                const unsigned char* tab, float scale, uint32_t* out)
 {
@@ -78,8 +92,7 @@ __device__ __forceinline__ void decode_weights(uint32_t hi, uint32_t lo, int dow
     for (int i = 0; i < N; i += 2) {
         const float c0 = codeword_at<CODE>(tab, window_offset<K, N, CODE>(b, a, i, mask));
         const float c1 = codeword_at<CODE>(tab, window_offset<K, N, CODE>(b, a, i + 1, mask));
-        const __half2 h = __floats2half2_rn(c0 * scale, c1 * scale);
-        out[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        out[i / 2] = weight_pair<BF16>(c0 * scale, c1 * scale);
     }
 }
 
@@ -107,8 +120,7 @@ __device__ __forceinline__ void decode_64(const uint32_t (&words)[2 * K], uint32
         if (step < 3) look_up(step + 1, c[(step + 1) & 1]);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-            const __half2 h = __floats2half2_rn(c[step & 1][i] * scale, c[step & 1][i + 1] * scale);
-            out[8 * step + i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            out[8 * step + i / 2] = weight_pair<false>(c[step & 1][i] * scale, c[step & 1][i + 1] * scale);
         }
     }
 }

@@ -69,6 +69,9 @@ cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& 
 cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, uint8_t* row_exponents,
                             int num_sms, cudaStream_t stream);
 
+// W as bfloat16, each weight scale * codeword rounded once.
+cudaError_t launch_decode_bf16(const CodedMatrix& w, void* out, long long ldw, int num_sms, cudaStream_t stream);
+
 // x [n, cols] as binary16 rows over a power of two each (row_pow2[n]).  col_exponents (or
 // nullptr, 8-byte aligned): fp32 exponent fields of powers of two that multiply the
 // columns first.  `early`: the launch before it in the stream is one of this call's
