@@ -13,7 +13,7 @@
 // Outputs that TMA can address (16-byte aligned base and rows) leave through shared
 // memory: a warp writes 32 rows of 128 bytes to a swizzled box and stores it as whole
 // lines (a lane's own 16-byte stores would each touch half a sector of 32 different
-// rows); other outputs are stored by the lanes.
+// rows); other outputs leave the box row by row.
 //
 // The tensor core's running fp32 sum loses about 1e-7 of a sum per square root of its
 // steps.  That does not show in 16-bit outputs; the weight gradient, fp32 and summed over
@@ -219,22 +219,19 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
     }
 }
 
-// 32 16-bit outputs of a row by its lane.
-template <int XT>
-__device__ __forceinline__ void store32(const Epilogue& e, long long r, long long c, const float (&v)[32], int count,
-                                        bool vec)
+// A box's rows to outputs that TMA cannot address, row by row: neighbouring lanes store
+// neighbouring elements (2 or 4 bytes each).
+template <typename T>
+__device__ __forceinline__ void store_rows(const unsigned char* box, T* out, long long ldo, int rows, int cols, int lane)
 {
-    uint16_t* o = static_cast<uint16_t*>(e.out) + r * e.ldo + c;
-    if (vec && count == 32) {
+    constexpr int per = 128 / sizeof(T);  // columns of a box
+    for (int i = 0; i < rows; ++i) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(o + i) =
-                make_uint4(x_pack2<XT>(v[i], v[i + 1]), x_pack2<XT>(v[i + 2], v[i + 3]),
-                           x_pack2<XT>(v[i + 4], v[i + 5]), x_pack2<XT>(v[i + 6], v[i + 7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < count) o[i] = x_bits<XT>(v[i]);
+        for (int h = 0; h < per; h += 32) {
+            const int c = lane + h, byte = c * (int)sizeof(T);
+            const T v = *reinterpret_cast<const T*>(box + i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15)));
+            if (c < cols) out[i * ldo + c] = v;
+        }
     }
 }
 
@@ -398,7 +395,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 for (int j = 0; j < 4; ++j) {
                     const int c = w.n0 + 128 * half + 32 * j;
                     if (c >= p.n || r0 >= p.m) break;  // the same in every lane
-                    if (tma_out || cut) {
+                    const bool plain = !tma_out && !cut;
+                    if (plain && e.accumulate && r0 + lane < p.m) {
+                        const float* o = static_cast<const float*>(e.out) + (long long)(r0 + lane) * e.ldo + c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < p.n) sum[32 * j + i] += o[i];
+                    }
+                    {
                         if (lane == 0) bulk_wait_read<0>();
                         __syncwarp();
 #pragma unroll
@@ -406,20 +410,19 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             *reinterpret_cast<float4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) =
                                 make_float4(sum[32 * j + 4 * i], sum[32 * j + 4 * i + 1], sum[32 * j + 4 * i + 2],
                                             sum[32 * j + 4 * i + 3]);
-                        fence_async_shared();
+                        if (!plain) fence_async_shared();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (plain) {
+                            store_rows(box, static_cast<float*>(e.out) + (long long)r0 * e.ldo + c, e.ldo,
+                                       p.m - r0 < 32 ? (int)(p.m - r0) : 32, p.n - c < 32 ? (int)(p.n - c) : 32, lane);
+                            __syncwarp();
+                        } else if (lane == 0) {
                             if (e.accumulate && !cut)
                                 tma_add_2d(&map_out, smem_addr(box), c, r0);
                             else
                                 tma_store_2d(&map_out, smem_addr(box), out_col + c - w.n0, out_row + local);
                             bulk_commit();
                         }
-                    } else if (r0 + lane < p.m) {
-                        float* o = static_cast<float*>(e.out) + (long long)(r0 + lane) * e.ldo + c;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < p.n) o[i] = e.accumulate ? o[i] + sum[32 * j + i] : sum[32 * j + i];
                     }
                 }
             } else {
@@ -467,10 +470,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 for (int c = cut ? kTile : 0; c < kTile; c += 64) {
                     if (n0 + c >= p.n || r0 >= p.m) break;  // the same in every lane
                     unsigned char* box = S.box[2 * quarter + ((c >> 6) & 1)];
-                    if (tma_out) {
-                        if (lane == 0) bulk_wait_read<1>();  // the box's last store, two ago, has been read
-                        __syncwarp();
-                    }
+                    if (lane == 0) bulk_wait_read<1>();  // the box's last store, two ago, has been read
+                    __syncwarp();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const long long ch = n0 + c + 32 * h;
@@ -478,11 +479,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c + 32 * h, v);
                         const int count = p.n - ch < 32 ? (int)(p.n - ch) : 32;
-                        if (r < p.m) {
-                            apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale, S.cols + c + 32 * h);
-                            if (!tma_out) store32<XT>(e, r, ch, v, count, vec);
-                        }
-                        if (tma_out) box32<XT>(box + lane * 128, lane, h, v);
+                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale, S.cols + c + 32 * h);
+                        box32<XT>(box + lane * 128, lane, h, v);
                         __syncwarp();
                     }
                     if (tma_out) {
@@ -492,6 +490,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             tma_store_2d(&map_out, smem_addr(box), (int)(n0 + c), (int)r0);
                             bulk_commit();
                         }
+                    } else {
+                        store_rows(box, static_cast<uint16_t*>(e.out) + r0 * e.ldo + n0 + c, e.ldo,
+                                   p.m - r0 < 32 ? (int)(p.m - r0) : 32, p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64, lane);
+                        __syncwarp();
                     }
                 }
                 tc_fence_before();
