@@ -134,7 +134,8 @@ __device__ __forceinline__ Item work_item(const Shape& p, int t)
 // below n.
 template <int KIND, int XT>
 __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                        int count, bool vec, float row_scale, const float2* cols)
+                                        int count, bool vec, float row_scale, const float2* cols,
+                                        const unsigned char* box_row, int half)
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= row_scale;
@@ -198,9 +199,10 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
         }
         if (e.residual) {
             const uint16_t* res = static_cast<const uint16_t*>(e.residual) + r * e.ldr + c;
-            if (vec && count == 32) {
+            if (vec) {
 #pragma unroll
                 for (int i = 0; i < 32; i += 8) {
+                    if (i >= count) break;  // rows of whole 16-byte vectors: all or none of the eight
                     const uint4 t = *reinterpret_cast<const uint4*>(res + i);
                     const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
@@ -210,10 +212,18 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
                         v[i + 2 * h + 1] += f.y;
                     }
                 }
-            } else {
+            } else {  // from the warp's box (load_rows)
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < count) v[i] += x_load<XT>(res, i);
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 t = *reinterpret_cast<const uint4*>(box_row + (((4 * half + i) ^ (threadIdx.x & 7)) << 4));
+                    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float2 f = x_unpack2<XT>(w[h]);
+                        v[8 * i + 2 * h] += f.x;
+                        v[8 * i + 2 * h + 1] += f.y;
+                    }
+                }
             }
         }
     }
@@ -231,6 +241,20 @@ __device__ __forceinline__ void store_rows(const unsigned char* box, T* out, lon
             const int c = lane + h, byte = c * (int)sizeof(T);
             const T v = *reinterpret_cast<const T*>(box + i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15)));
             if (c < cols) out[i * ldo + c] = v;
+        }
+    }
+}
+
+// The reverse, for 16-bit rows that no vector load can reach.
+__device__ __forceinline__ void load_rows(unsigned char* box, const uint16_t* in, long long ld, int rows, int cols, int lane)
+{
+#pragma unroll 4
+    for (int i = 0; i < rows; ++i) {
+#pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+            const int c = lane + h, byte = 2 * c;
+            *reinterpret_cast<uint16_t*>(box + i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15))) =
+                c < cols ? in[i * ld + c] : (uint16_t)0;
         }
     }
 }
@@ -472,6 +496,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     unsigned char* box = S.box[2 * quarter + ((c >> 6) & 1)];
                     if (lane == 0) bulk_wait_read<1>();  // the box's last store, two ago, has been read
                     __syncwarp();
+                    const int rows = p.m - r0 < 32 ? (int)(p.m - r0) : 32, cols = p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64;
+                    if (KIND == kGemmForward && e.residual && !vec) {
+                        // each half's values make room for that half's outputs
+                        load_rows(box, static_cast<const uint16_t*>(e.residual) + r0 * e.ldr + n0 + c, e.ldr, rows, cols, lane);
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const long long ch = n0 + c + 32 * h;
@@ -479,7 +509,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c + 32 * h, v);
                         const int count = p.n - ch < 32 ? (int)(p.n - ch) : 32;
-                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale, S.cols + c + 32 * h);
+                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale, S.cols + c + 32 * h,
+                                                       box + lane * 128, h);
                         box32<XT>(box + lane * 128, lane, h, v);
                         __syncwarp();
                     }
@@ -491,8 +522,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             bulk_commit();
                         }
                     } else {
-                        store_rows(box, static_cast<uint16_t*>(e.out) + r0 * e.ldo + n0 + c, e.ldo,
-                                   p.m - r0 < 32 ? (int)(p.m - r0) : 32, p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64, lane);
+                        store_rows(box, static_cast<uint16_t*>(e.out) + r0 * e.ldo + n0 + c, e.ldo, rows, cols, lane);
                         __syncwarp();
                     }
                 }
@@ -576,7 +606,9 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, float* partial, int 
     } else if (!make_map_out(&mo, e.out, g.m, g.n, e.ldo, es)) {
         return cudaErrorInvalidValue;
     }
-    if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 15) == 0 && e.ldr % 8 == 0;
+    // the residual by 16-byte loads: rows of whole vectors
+    if (e.residual)
+        vec = (reinterpret_cast<uintptr_t>(e.residual) & 15) == 0 && e.ldr % 8 == 0 && g.n % 8 == 0;
     cudaError_t st = cudaFuncSetAttribute(gemm_kernel<KIND, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)sizeof(Smem));
     if (st != cudaSuccess) return st;
