@@ -146,6 +146,43 @@ def test_other_stream(cuda_device):
     assert torch.equal(a, want) and torch.equal(b, want)
 
 
+def test_given_stream_owns_what_a_call_allocates(cuda_device):
+    """A stream that is given is not ordered after the current one: its results and its
+    scratch are not memory that the current stream still writes, nor may the current
+    stream get that scratch while the call has yet to run."""
+    import torch
+
+    up, _, x, g = _block(np.random.default_rng(10), cuda_device, 500, torch.bfloat16)
+    rows, cols = 1024, 512
+    nbytes = tcq.tcq_gemm_workspace_bytes(16, 2, 256, rows, cols, 500, tcq.TCQ_F16)
+    want, packed = tcq.gemm(*up.matrix, x), tcq.pack8(x)
+    grad = tcq.wgrad8(want, packed)
+    calls = [(lambda s: tcq.gemm(*up.matrix, x, stream=s), want),
+             (lambda s: tcq.gemm_dgrad(*up.matrix, want, stream=s), tcq.gemm_dgrad(*up.matrix, want)),
+             (lambda s: tcq.pack8(x, stream=s).codes, packed.codes),
+             (lambda s: tcq.unpack8(packed, stream=s), tcq.unpack8(packed)),
+             (lambda s: tcq.act_grad8(x, packed, "silu", stream=s)[0], tcq.act_grad8(x, packed, "silu")[0]),
+             (lambda s: tcq.wgrad8(want, packed, stream=s), grad)]
+    s = torch.cuda.Stream()
+    for call, expected in calls:
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        held = torch.empty_like(expected)  # the current stream writes it when the call is long over
+        torch.cuda._sleep(50_000_000)
+        held.fill_(1)
+        del held
+        got = call(s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, expected)
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    got = calls[0][0](s)
+    other = torch.empty(nbytes, dtype=torch.uint8, device=cuda_device).fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and bool((other == 255).all())
+
+
 @pytest.mark.parametrize("n", [1, 40, 700])
 def test_capture_and_replay(n, cuda_device):
     """The block's forward and backward captured once and replayed on new inputs gives

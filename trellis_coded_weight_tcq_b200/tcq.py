@@ -669,9 +669,20 @@ def _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, devic
         _check_device(codebook, device, "codebook")
 
 
-def _scratch(workspace, nbytes, like, what):
+def _empty(like, shape, dtype, stream):
+    """Memory of the stream that will write it: a given one may run before what the
+    current stream still does to memory freed there, and after this call has returned."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    if stream.device != like.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {like.device}")
+    with _torch().cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _scratch(workspace, nbytes, like, what, stream):
     if workspace is None:
-        return like.new_empty(nbytes or 1, dtype=_torch().uint8)
+        return _empty(like, nbytes or 1, _torch().uint8, stream)
     if workspace.device != like.device or workspace.dtype != _torch().uint8 or not workspace.is_contiguous():
         raise ValueError(f"{what}: workspace must be a contiguous uint8 tensor on x's device")
     return workspace
@@ -687,6 +698,8 @@ def _launch(what, device, stream, fn, *args):
     torch = _torch()
     index = device.index
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         handle = stream.cuda_stream
     else:
         handle = torch._C._cuda_getCurrentRawStream(index)
@@ -715,8 +728,8 @@ def pack8(x, format: str = "int8", out: Packed8 | None = None, stream=None) -> P
     n, cols = x.shape
     if out is None:
         fmt = _choice(Q8_FORMATS, format, "format")
-        out = Packed8(x.new_empty((n, cols), dtype=torch.int8),
-                      x.new_empty((n, (cols + 31) // 32), dtype=torch.uint8), format)
+        out = Packed8(_empty(x, (n, cols), torch.int8, stream),
+                      _empty(x, (n, (cols + 31) // 32), torch.uint8, stream), format)
     else:
         fmt = _check_packed(out, n, cols, x.device, "out")
     _launch("tcq_pack8", x.device, stream, lib.tcq_pack8, x.data_ptr(), xt, _ld(x), n, cols, fmt,
@@ -734,7 +747,7 @@ def unpack8(packed: Packed8, dtype=None, out=None, stream=None):
     dev = codes.device
     fmt = _check_packed(packed, n, cols, dev, "packed")
     if out is None:
-        out = codes.new_empty((n, cols), dtype=dtype or torch.bfloat16)
+        out = _empty(codes, (n, cols), dtype or torch.bfloat16, stream)
     else:
         _check_out(out, (n, cols), dtype or out.dtype, dev, "out")
     xt = _x_dtype(out, "out")
@@ -767,7 +780,7 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
         _check_out(residual, (n, rows), dtype, dev, "residual")
         ldr = _ld(residual)
     if out is None:
-        out = x.new_empty((n, rows))
+        out = _empty(x, (n, rows), dtype, stream)
     else:
         _check_out(out, (n, rows), dtype, dev, "out")
     zc = zs = None
@@ -778,7 +791,7 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
     cb = cb_dtype_of(codebook)
     wp, wb = None, 0
     if n != 1 or zc is not None:
-        ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_workspace_bytes, L, k, T, rows, cols, n, cb), x, "gemm")
+        ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_workspace_bytes, L, k, T, rows, cols, n, cb), x, "gemm", stream)
         wp, wb = ws.data_ptr(), ws.numel()
     _launch("tcq_gemm", dev, stream, lib.tcq_gemm, bits.data_ptr(), start_state.data_ptr(), _addr(scale),
             _addr(codebook), cb, L, k, T, rows, cols, x.data_ptr(), xt, _ld(x), n, _addr(bias), a, _addr(residual),
@@ -797,12 +810,12 @@ def gemm_dgrad(bits, start_state, scale, codebook, L: int, k: int, T: int, rows:
         raise ValueError(f"gemm_dgrad: dz has {dz.shape[1]} columns, the matrix {rows} rows")
     _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, dev, "gemm_dgrad")
     if out is None:
-        out = dz.new_empty((n, cols))
+        out = _empty(dz, (n, cols), dz.dtype, stream)
     else:
         _check_out(out, (n, cols), dz.dtype, dev, "out")
     cb = cb_dtype_of(codebook)
     ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_dgrad_workspace_bytes, L, k, T, rows, cols, n, cb), dz,
-                  "gemm_dgrad")
+                  "gemm_dgrad", stream)
     _launch("tcq_gemm_dgrad", dev, stream, lib.tcq_gemm_dgrad, bits.data_ptr(), start_state.data_ptr(), _addr(scale),
             _addr(codebook), cb, L, k, T, rows, cols, dz.data_ptr(), xt, _ld(dz), n, out.data_ptr(), _ld(out),
             ws.data_ptr(), ws.numel())
@@ -826,13 +839,13 @@ def act_grad8(dy, checkpoint, act: str, dbias: bool = True, out=None, workspace=
     elif a != TCQ_ACT_NONE:
         raise ValueError(f"act_grad8: {act!r} needs the checkpoint of the pre-activation")
     if out is None:
-        out = dy.new_empty((n, rows))
+        out = _empty(dy, (n, rows), dy.dtype, stream)
     else:
         _check_out(out, (n, rows), dy.dtype, dev, "out")
     db, dp, wp, wb = None, None, None, 0
     if dbias:
-        db = dy.new_empty(rows, dtype=torch.float32)
-        ws = _scratch(workspace, lib.tcq_act_grad8_workspace_bytes(n, rows), dy, "act_grad8")
+        db = _empty(dy, rows, torch.float32, stream)
+        ws = _scratch(workspace, lib.tcq_act_grad8_workspace_bytes(n, rows), dy, "act_grad8", stream)
         dp, wp, wb = db.data_ptr(), ws.data_ptr(), ws.numel()
     _launch("tcq_act_grad8", dev, stream, lib.tcq_act_grad8, dy.data_ptr(), xt, _ld(dy), zc, zs, zf, a, n, rows,
             out.data_ptr(), _ld(out), dp, wp, wb)
@@ -846,15 +859,17 @@ def wgrad8(dz, packed: Packed8, out=None, accumulate: bool = False, workspace=No
     xt = _x_dtype(dz, "dz")
     dev = dz.device
     n, rows = dz.shape
+    if packed.codes.dim() != 2:
+        raise ValueError("packed must hold CUDA tensors [n, cols]")
     cols = packed.codes.shape[1]
     fmt = _check_packed(packed, n, cols, dev, "packed")
     if out is None:
         if accumulate:
             raise ValueError("wgrad8: accumulate needs out")
-        out = dz.new_empty((rows, cols), dtype=torch.float32)
+        out = _empty(dz, (rows, cols), torch.float32, stream)
     else:
         _check_out(out, (rows, cols), torch.float32, dev, "out")
-    ws = _scratch(workspace, lib.tcq_wgrad8_workspace_bytes(rows, cols, n), dz, "wgrad8")
+    ws = _scratch(workspace, lib.tcq_wgrad8_workspace_bytes(rows, cols, n), dz, "wgrad8", stream)
     _launch("tcq_wgrad8", dev, stream, lib.tcq_wgrad8, dz.data_ptr(), xt, _ld(dz), packed.codes.data_ptr(),
             packed.scales.data_ptr(), fmt, n, rows, cols, out.data_ptr(), _ld(out), int(accumulate), ws.data_ptr(),
             ws.numel())
