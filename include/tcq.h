@@ -388,7 +388,8 @@ tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 forma
  *
  *   bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols  as tcq_gemv
  *               (T % 4 == 0, cols % T == 0, a binary16 table when L >= 15; the
- *               entries of a table are at most 65504 in magnitude).
+ *               entries of a table are at most 65504 in magnitude, and in the binary16
+ *               products those below 2^-14 keep only multiples of 2^-24).
  *   x           [n, cols] of xdtype, row stride ldx.
  *   bias        fp32 [rows] or NULL.
  *   residual    [n, rows] of xdtype, row stride ldr, or NULL.

@@ -17,8 +17,15 @@
 //
 // The tensor core's running fp32 sum loses about 1e-7 of a sum per square root of its
 // steps.  That does not show in 16-bit outputs; the weight gradient, fp32 and summed over
-// all tokens, takes its sums out of tensor memory every 1024 tokens and adds them in
-// registers (error against float64 at 4096 tokens: 1.6e-6 without, 8e-7 with).
+// all tokens, takes its sums out of tensor memory every 1280 tokens at most and adds them
+// in registers (root mean square error against float64 at 4096 tokens, relative to the
+// gradient's: 1.6e-6 without, 2.8e-7 with).
+//
+// Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP): forward 373 us,
+// input gradient 339 us, weight gradient 363 us of kernel time; the plain product of the
+// vendor library takes 346 to 352 us there.  All of them run at the board's power limit
+// (SM clock 1.4 to 1.55 GHz of 1.965 GHz), so the bound is the energy of the MMAs: a
+// 256 x 512 tile with two thirds of the operand traffic is no faster.
 //
 // Fewer tiles than half the pairs: the reduction is cut into as many pieces as there are
 // pairs for, each writes its fp32 sums to the workspace, and a second kernel adds a
