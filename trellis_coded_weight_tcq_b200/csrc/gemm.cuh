@@ -102,7 +102,8 @@ struct RowPowers {
 // Either or both (n == 0 or rows == 0: not wanted), in one launch.
 cudaError_t launch_prepare(ScaleRows a, RowPowers p, cudaStream_t stream);
 
-// 16-bit rows copied to another stride.
+// 16-bit rows copied to another stride, beside the launch before it in the stream (one of
+// this call's that neither reads nor writes these rows).
 cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long cols, void* out, long long ldo,
                           int num_sms, cudaStream_t stream);
 

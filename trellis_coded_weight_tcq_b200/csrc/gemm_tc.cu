@@ -38,6 +38,7 @@
 // both), tfull / tempty (an accumulator set is complete / has been read).
 #include "epilogue.cuh"
 #include "gemm.cuh"
+#include "pdl.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
 
@@ -313,6 +314,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    pdl_wait();  // the operands, and the workspace that the call before may have used
+    pdl_release();
     const uint32_t tmem = S.tmem;
     volatile int* stop = &S.stop;
 
@@ -559,6 +562,7 @@ __global__ void __launch_bounds__(256) finish_kernel(Shape p, Epilogue e, const 
     const int local = blockIdx.y * 8 + (threadIdx.x >> 5), c = blockIdx.z * 128 + 4 * lane;
     const long long r = (long long)(tile % p.m_tiles) * kTile + local;
     const long long n0 = (long long)(tile / p.m_tiles) * kTile;
+    pdl_wait();
     if (r >= p.m || n0 + blockIdx.z * 128 >= p.n) return;
     const float* src = partial + ((long long)tile * p.pieces * kTile + local) * kTile + c;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -621,14 +625,15 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, float* partial, int 
     if (st != cudaSuccess) return st;
     const long long items = tiles * s.pieces;
     const int pairs = (int)(items < num_sms / 2 ? items : num_sms / 2);
-    gemm_kernel<KIND, XT><<<2 * pairs, gemm_threads(KIND), sizeof(Smem), stream>>>(ma, mb, mo, s, e, vec, tma_out, err);
-    st = cudaGetLastError();
+    // every product comes after a launch of its own call (the decode, the unpacking)
+    st = launch_pdl(gemm_kernel<KIND, XT>, dim3(2 * pairs), dim3(gemm_threads(KIND)), sizeof(Smem), stream, true, ma, mb, mo,
+                    s, e, vec, tma_out, err);
     if (st != cudaSuccess || s.pieces == 1) return st;
     // quads: 8-byte accesses
     bool quads = (reinterpret_cast<uintptr_t>(e.out) & 7) == 0 && e.ldo % 4 == 0;
     if (e.residual) quads = quads && (reinterpret_cast<uintptr_t>(e.residual) & 7) == 0 && e.ldr % 4 == 0;
-    finish_kernel<KIND, XT><<<dim3((unsigned)tiles, kTile / 8, kTile / 128), 256, 0, stream>>>(s, e, partial, quads);
-    return cudaGetLastError();
+    return launch_pdl(finish_kernel<KIND, XT>, dim3((unsigned)tiles, kTile / 8, kTile / 128), dim3(256), 0, stream, true, s,
+                      e, static_cast<const float*>(partial), quads);
 }
 
 }  // namespace

@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(ScaleRows a, RowPower
 __global__ void __launch_bounds__(kThreads) copy16_kernel(const uint16_t* x, long long ldx, long long n, long long cols,
                                                           uint16_t* out, long long ldo)
 {
+    pdl_release();
     for (long long r = blockIdx.x; r < n; r += gridDim.x)
         for (long long c = 8ll * threadIdx.x; c < cols; c += 8 * kThreads) {
             uint32_t v[8];
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) copy16_kernel(const uint16_t* x, lon
             *reinterpret_cast<uint4*>(out + r * ldo + c) =
                 make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
         }
+    if (blockIdx.x == gridDim.x - 1) pdl_wait();  // as above
 }
 
 }  // namespace
@@ -138,9 +140,8 @@ cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long c
                           int num_sms, cudaStream_t stream)
 {
     const long long grid = n < 32ll * num_sms ? n : 32ll * num_sms;
-    copy16_kernel<<<(int)grid, kThreads, 0, stream>>>(static_cast<const uint16_t*>(x), ldx, n, cols,
-                                                      static_cast<uint16_t*>(out), ldo);
-    return cudaGetLastError();
+    return launch_pdl(copy16_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, true,
+                      static_cast<const uint16_t*>(x), ldx, n, cols, static_cast<uint16_t*>(out), ldo);
 }
 
 }  // namespace tcq

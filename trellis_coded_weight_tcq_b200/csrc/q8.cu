@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads) unpack8_vec_kernel(const uint8_t* co
 {
     const long long groups = (cols + 31) / 32, pieces = cols / 8;
     const long long step = blockDim.x;
+    pdl_release();  // the weight gradient's next launch
     for (long long r = blockIdx.x; r < n; r += gridDim.x) {
         const uint2* cr = reinterpret_cast<const uint2*>(codes + r * cols);
         const uint8_t* sr = scales + r * groups;
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kThreads) unpack8_kernel(const uint8_t* codes,
                                                            long long cols, uint16_t* x, long long ldx)
 {
     const long long groups = (cols + 31) / 32;
+    pdl_release();
     for (long long r = blockIdx.x; r < n; r += gridDim.x) {
         for (long long c = (long long)blockIdx.y * blockDim.x + threadIdx.x; c < cols;
              c += (long long)gridDim.y * blockDim.x)
