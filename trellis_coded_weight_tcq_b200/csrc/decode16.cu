@@ -12,7 +12,8 @@
 // A warp takes 256 columns of a row at a time, eight per lane: their windows lie in
 // two stream words, one 16-byte store per lane; each warp has a contiguous run.  Table
 // lookups at random shared-memory addresses bound it (as in the decoder, about 3.6 bank
-// passes per 32), then the 2 bytes per weight written.
+// passes per 32), then the 2 bytes per weight written: 39 us for 14336 x 4096, L = 16,
+// k = 2 (the look-ups alone 24 us, the 132 MB read and written 21 us).
 #include "codes.cuh"
 #include "decode16.cuh"
 #include "gemm.cuh"
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix 
             ++row;
         }
         if (left > 0) fetch(nxt, row, at);
-        const float inv = !BF16 && w.scale ? inverse_pow2(__ldg(row_pow2 + r)) : 1.f;
+        const float inv = !BF16 && w.scale ? inverse_pow2(__ldcg(row_pow2 + r)) : 1.f;
         uint16_t* dst = out + r * ldw + a * kUnit + 8 * lane;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
     long long row = u0 / upr;
     int at = (int)(u0 - row * upr);
     for (long long u = u0; u < u1; ++u) {
-        const float inv = !BF16 && w.scale ? inverse_pow2(__ldg(row_pow2 + row)) : 1.f;
+        const float inv = !BF16 && w.scale ? inverse_pow2(__ldcg(row_pow2 + row)) : 1.f;
         const int c = at * kUnit + 8 * lane;
         uint32_t v[4];
 #pragma unroll

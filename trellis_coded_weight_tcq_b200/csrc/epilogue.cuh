@@ -17,11 +17,11 @@ __device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long
 {
     const int lane = threadIdx.x & 31;
     const int count = rows - r < 4 ? (rows - r > 0 ? (int)(rows - r) : 0) : 4;
-    const float rs = e.row_scale ? __ldg(e.row_scale + t) : 1.f;
+    const float rs = e.row_scale ? __ldcg(e.row_scale + t) : 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         v[i] *= rs;
-        if (i < count) v[i] = fmaf(v[i], e.col_scale ? __ldg(e.col_scale + r + i) : 1.f, e.bias ? __ldg(e.bias + r + i) : 0.f);
+        if (i < count) v[i] = fmaf(v[i], e.col_scale ? __ldcg(e.col_scale + r + i) : 1.f, e.bias ? __ldg(e.bias + r + i) : 0.f);
     }
     if (e.z_codes) {  // a group of 32 is eight lanes
         uint32_t top = 0u;

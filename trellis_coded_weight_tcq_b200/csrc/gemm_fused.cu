@@ -178,7 +178,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
             bits = row < w.rows ? w.bits + row * (cols / 32 * K) : nullptr;
             start = w.start_state + row * nb;
             scale = w.scale ? w.scale + row * nb : nullptr;
-            if (bits && scale) inv = __ldg(row_pow2 + row);
+            if (bits && scale) inv = __ldcg(row_pow2 + row);
         };
         auto advance = [&](int by) {
             for (ks += by; ks >= p.steps; ks -= p.steps) {

@@ -468,7 +468,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     named_barrier(1, 128);  // the last tile's have been read
                     for (int i = threadIdx.x - 128; i < kTile; i += 128) {
                         const long long c = n0 + i;
-                        S.cols[i] = make_float2(e.col_scale && c < p.n ? __ldg(e.col_scale + c) : 1.f,
+                        S.cols[i] = make_float2(e.col_scale && c < p.n ? __ldcg(e.col_scale + c) : 1.f,
                                                 e.bias && c < p.n ? __ldg(e.bias + c) : 0.f);
                     }
                 }
@@ -478,7 +478,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 if constexpr (KIND == kGemmForward) ok = named_all(1, 128, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float row_scale = e.row_scale && r < p.m ? __ldg(e.row_scale + r) : 1.f;
+                const float row_scale = e.row_scale && r < p.m ? __ldcg(e.row_scale + r) : 1.f;
                 if (cut) {  // the sums as they are, 32 columns at a time
 #pragma unroll 1
                     for (int c = 0; c < kTile; c += 32) {

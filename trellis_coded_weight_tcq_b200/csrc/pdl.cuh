@@ -13,6 +13,8 @@ __device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.lau
 // Waits until the kernel before this one in the stream has ended and its results are
 // visible (at once when this kernel was launched in the plain way).  A kernel that
 // starts early waits before it ends, so that ends keep the stream's order.
+// What the kernel before wrote is read past L1 (__ldcg, TMA): __ldg is for data that does
+// not change while a kernel runs, and this one was running.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Launches `kernel`; with `early` it may start before the kernel ahead of it ends.

@@ -11,6 +11,7 @@ computing anything itself.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -598,22 +599,22 @@ class Packed8:
 
 # These calls can be shorter than their checks, so the checks are few and plain: torch
 # sizes compare with tuples, addresses and streams go to ctypes as integers.
-def _x_dtype(t, what: str) -> int:
-    """TCQ_X_* of a 2-D 16-bit CUDA tensor with unit-stride rows."""
-    if t.dim() != 2 or not t.is_cuda or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel()):
+def _rows(t, what: str):
+    """(TCQ_X_*, n, columns, row stride) of a 2-D 16-bit CUDA tensor with unit-stride rows
+    (the stride of one row, or of none, does not matter)."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor with unit-stride rows")
+    (n, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1 and n:
         raise ValueError(f"{what} must be a 2-D CUDA tensor with unit-stride rows")
     dtype, torch = t.dtype, _torch()
     if dtype == torch.bfloat16:
-        return TCQ_X_BF16
-    if dtype == torch.float16:
-        return TCQ_X_F16
-    raise TypeError(f"{what} must be float16 or bfloat16, got {dtype}")
-
-
-def _ld(t) -> int:
-    """Row stride in elements (that of one row, or of none, does not matter)."""
-    n, cols = t.shape
-    return t.stride(0) if n > 1 and cols else max(cols, 1)
+        xt = TCQ_X_BF16
+    elif dtype == torch.float16:
+        xt = TCQ_X_F16
+    else:
+        raise TypeError(f"{what} must be float16 or bfloat16, got {dtype}")
+    return xt, n, cols, ld if n > 1 and cols else max(cols, 1)
 
 
 def _choice(table, name, what):
@@ -623,12 +624,17 @@ def _choice(table, name, what):
         raise ValueError(f"{what} must be one of {', '.join(table)}; got {name!r}") from None
 
 
-def _check_out(out, shape, dtype, device, what):
-    if out.shape != shape or out.dtype != dtype or (out.stride(1) != 1 and shape[1] > 1 and out.numel()):
-        raise ValueError(f"{what} must be a {dtype} tensor {list(shape)} with unit-stride rows")
-    if shape[0] > 1 and out.numel() and out.stride(0) < shape[1]:
+def _check_out(out, shape, dtype, device, what) -> int:
+    """The row stride of an array that the caller gave."""
+    if out.shape != shape or out.dtype != dtype:
+        raise ValueError(f"{what} must be a {dtype} tensor {list(shape)}")
+    (n, cols), (ld, step) = shape, out.stride()
+    if n and step != 1 and cols > 1:
+        raise ValueError(f"{what} must have unit-stride rows")
+    if n > 1 and cols and ld < cols:
         raise ValueError(f"{what}: rows overlap")
     _check_device(out, device, what)
+    return ld if n > 1 and cols else max(cols, 1)
 
 
 def _check_device(t, device, what):
@@ -712,27 +718,25 @@ def _launch(what, device, stream, fn, *args):
         raise TCQError(status, what)
 
 
-def _sized(device, fn, *args):
-    """A workspace query, which counts the multiprocessors of the tensors' device."""
-    torch = _torch()
-    if device.index == torch._C._cuda_getDevice():
-        return fn(*args)
-    with torch.cuda.device(device.index):
-        return fn(*args)
+@functools.lru_cache(maxsize=1024)
+def _sized(device, query, *args) -> int:
+    """A workspace query, a function of the shape and the device (whose multiprocessors it
+    counts)."""
+    with _torch().cuda.device(device):
+        return getattr(load_library(), query)(*args)
 
 
 def pack8(x, format: str = "int8", out: Packed8 | None = None, stream=None) -> Packed8:
     """8-bit checkpoint of ``x`` (float16 or bfloat16 CUDA [n, cols], unit-stride rows)."""
     torch, lib = _torch(), load_library()
-    xt = _x_dtype(x, "x")
-    n, cols = x.shape
+    xt, n, cols, ld = _rows(x, "x")
     if out is None:
         fmt = _choice(Q8_FORMATS, format, "format")
         out = Packed8(_empty(x, (n, cols), torch.int8, stream),
                       _empty(x, (n, (cols + 31) // 32), torch.uint8, stream), format)
     else:
         fmt = _check_packed(out, n, cols, x.device, "out")
-    _launch("tcq_pack8", x.device, stream, lib.tcq_pack8, x.data_ptr(), xt, _ld(x), n, cols, fmt,
+    _launch("tcq_pack8", x.device, stream, lib.tcq_pack8, x.data_ptr(), xt, ld, n, cols, fmt,
             out.codes.data_ptr(), out.scales.data_ptr())
     return out
 
@@ -750,9 +754,9 @@ def unpack8(packed: Packed8, dtype=None, out=None, stream=None):
         out = _empty(codes, (n, cols), dtype or torch.bfloat16, stream)
     else:
         _check_out(out, (n, cols), dtype or out.dtype, dev, "out")
-    xt = _x_dtype(out, "out")
+    xt, _, _, ld = _rows(out, "out")
     _launch("tcq_unpack8", dev, stream, lib.tcq_unpack8, codes.data_ptr(), packed.scales.data_ptr(), fmt, n, cols,
-            out.data_ptr(), xt, _ld(out))
+            out.data_ptr(), xt, ld)
     return out
 
 
@@ -765,10 +769,10 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
     [n, rows] that receives the pre-activation in 8 bits.  ``workspace`` (uint8, at
     least tcq_gemm_workspace_bytes) and ``out`` are allocated when not given."""
     torch, lib = _torch(), load_library()
-    xt = _x_dtype(x, "x")
-    dev, dtype, n = x.device, x.dtype, x.shape[0]
-    if x.shape[1] != cols:
-        raise ValueError(f"gemm: x has {x.shape[1]} columns, the matrix {cols}")
+    xt, n, width, ldx = _rows(x, "x")
+    dev, dtype = x.device, x.dtype
+    if width != cols:
+        raise ValueError(f"gemm: x has {width} columns, the matrix {cols}")
     a = _choice(ACTIVATIONS, act, "act")
     _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, dev, "gemm")
     if bias is not None:
@@ -777,12 +781,11 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
         _check_device(bias, dev, "bias")
     ldr = 0
     if residual is not None:
-        _check_out(residual, (n, rows), dtype, dev, "residual")
-        ldr = _ld(residual)
+        ldr = _check_out(residual, (n, rows), dtype, dev, "residual")
     if out is None:
-        out = _empty(x, (n, rows), dtype, stream)
+        out, ldy = _empty(x, (n, rows), dtype, stream), max(rows, 1)
     else:
-        _check_out(out, (n, rows), dtype, dev, "out")
+        ldy = _check_out(out, (n, rows), dtype, dev, "out")
     zc = zs = None
     zf = TCQ_Q8_INT8
     if checkpoint is not None:
@@ -791,11 +794,12 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
     cb = cb_dtype_of(codebook)
     wp, wb = None, 0
     if n != 1 or zc is not None:
-        ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_workspace_bytes, L, k, T, rows, cols, n, cb), x, "gemm", stream)
+        ws = _scratch(workspace, _sized(dev, "tcq_gemm_workspace_bytes", L, k, T, rows, cols, n, cb), x, "gemm",
+                      stream)
         wp, wb = ws.data_ptr(), ws.numel()
     _launch("tcq_gemm", dev, stream, lib.tcq_gemm, bits.data_ptr(), start_state.data_ptr(), _addr(scale),
-            _addr(codebook), cb, L, k, T, rows, cols, x.data_ptr(), xt, _ld(x), n, _addr(bias), a, _addr(residual),
-            ldr, out.data_ptr(), _ld(out), zc, zs, zf, wp, wb)
+            _addr(codebook), cb, L, k, T, rows, cols, x.data_ptr(), xt, ldx, n, _addr(bias), a, _addr(residual),
+            ldr, out.data_ptr(), ldy, zc, zs, zf, wp, wb)
     return out
 
 
@@ -804,20 +808,20 @@ def gemm_dgrad(bits, start_state, scale, codebook, L: int, k: int, T: int, rows:
     """dz W for a trellis-coded W [rows, cols] and ``dz`` float16 or bfloat16 [n, rows];
     [n, cols] of dz's type."""
     lib = load_library()
-    xt = _x_dtype(dz, "dz")
-    dev, n = dz.device, dz.shape[0]
-    if dz.shape[1] != rows:
-        raise ValueError(f"gemm_dgrad: dz has {dz.shape[1]} columns, the matrix {rows} rows")
+    xt, n, width, lddz = _rows(dz, "dz")
+    dev = dz.device
+    if width != rows:
+        raise ValueError(f"gemm_dgrad: dz has {width} columns, the matrix {rows} rows")
     _check_matrix(bits, start_state, scale, codebook, L, k, T, rows, cols, dev, "gemm_dgrad")
     if out is None:
-        out = _empty(dz, (n, cols), dz.dtype, stream)
+        out, lddx = _empty(dz, (n, cols), dz.dtype, stream), max(cols, 1)
     else:
-        _check_out(out, (n, cols), dz.dtype, dev, "out")
+        lddx = _check_out(out, (n, cols), dz.dtype, dev, "out")
     cb = cb_dtype_of(codebook)
-    ws = _scratch(workspace, _sized(dev, lib.tcq_gemm_dgrad_workspace_bytes, L, k, T, rows, cols, n, cb), dz,
+    ws = _scratch(workspace, _sized(dev, "tcq_gemm_dgrad_workspace_bytes", L, k, T, rows, cols, n, cb), dz,
                   "gemm_dgrad", stream)
     _launch("tcq_gemm_dgrad", dev, stream, lib.tcq_gemm_dgrad, bits.data_ptr(), start_state.data_ptr(), _addr(scale),
-            _addr(codebook), cb, L, k, T, rows, cols, dz.data_ptr(), xt, _ld(dz), n, out.data_ptr(), _ld(out),
+            _addr(codebook), cb, L, k, T, rows, cols, dz.data_ptr(), xt, lddz, n, out.data_ptr(), lddx,
             ws.data_ptr(), ws.numel())
     return out
 
@@ -827,9 +831,8 @@ def act_grad8(dy, checkpoint, act: str, dbias: bool = True, out=None, workspace=
     unless ``dbias``), from the 8-bit checkpoint of the pre-activation (None for act
     "none").  ``out`` may be ``dy``."""
     torch, lib = _torch(), load_library()
-    xt = _x_dtype(dy, "dy")
+    xt, n, rows, lddy = _rows(dy, "dy")
     dev = dy.device
-    n, rows = dy.shape
     a = _choice(ACTIVATIONS, act, "act")
     zc = zs = None
     zf = TCQ_Q8_INT8
@@ -839,16 +842,16 @@ def act_grad8(dy, checkpoint, act: str, dbias: bool = True, out=None, workspace=
     elif a != TCQ_ACT_NONE:
         raise ValueError(f"act_grad8: {act!r} needs the checkpoint of the pre-activation")
     if out is None:
-        out = _empty(dy, (n, rows), dy.dtype, stream)
+        out, lddz = _empty(dy, (n, rows), dy.dtype, stream), max(rows, 1)
     else:
-        _check_out(out, (n, rows), dy.dtype, dev, "out")
+        lddz = _check_out(out, (n, rows), dy.dtype, dev, "out")
     db, dp, wp, wb = None, None, None, 0
     if dbias:
         db = _empty(dy, rows, torch.float32, stream)
-        ws = _scratch(workspace, lib.tcq_act_grad8_workspace_bytes(n, rows), dy, "act_grad8", stream)
+        ws = _scratch(workspace, _sized(dev, "tcq_act_grad8_workspace_bytes", n, rows), dy, "act_grad8", stream)
         dp, wp, wb = db.data_ptr(), ws.data_ptr(), ws.numel()
-    _launch("tcq_act_grad8", dev, stream, lib.tcq_act_grad8, dy.data_ptr(), xt, _ld(dy), zc, zs, zf, a, n, rows,
-            out.data_ptr(), _ld(out), dp, wp, wb)
+    _launch("tcq_act_grad8", dev, stream, lib.tcq_act_grad8, dy.data_ptr(), xt, lddy, zc, zs, zf, a, n, rows,
+            out.data_ptr(), lddz, dp, wp, wb)
     return out, db
 
 
@@ -856,9 +859,8 @@ def wgrad8(dz, packed: Packed8, out=None, accumulate: bool = False, workspace=No
     """dz^T x, float32 [rows, cols], for ``dz`` float16 or bfloat16 [n, rows] and the
     8-bit checkpoint of x [n, cols]; added to ``out`` when ``accumulate``."""
     torch, lib = _torch(), load_library()
-    xt = _x_dtype(dz, "dz")
+    xt, n, rows, lddz = _rows(dz, "dz")
     dev = dz.device
-    n, rows = dz.shape
     if packed.codes.dim() != 2:
         raise ValueError("packed must hold CUDA tensors [n, cols]")
     cols = packed.codes.shape[1]
@@ -866,12 +868,12 @@ def wgrad8(dz, packed: Packed8, out=None, accumulate: bool = False, workspace=No
     if out is None:
         if accumulate:
             raise ValueError("wgrad8: accumulate needs out")
-        out = _empty(dz, (rows, cols), torch.float32, stream)
+        out, lddw = _empty(dz, (rows, cols), torch.float32, stream), max(cols, 1)
     else:
-        _check_out(out, (rows, cols), torch.float32, dev, "out")
-    ws = _scratch(workspace, lib.tcq_wgrad8_workspace_bytes(rows, cols, n), dz, "wgrad8", stream)
-    _launch("tcq_wgrad8", dev, stream, lib.tcq_wgrad8, dz.data_ptr(), xt, _ld(dz), packed.codes.data_ptr(),
-            packed.scales.data_ptr(), fmt, n, rows, cols, out.data_ptr(), _ld(out), int(accumulate), ws.data_ptr(),
+        lddw = _check_out(out, (rows, cols), torch.float32, dev, "out")
+    ws = _scratch(workspace, _sized(dev, "tcq_wgrad8_workspace_bytes", rows, cols, n), dz, "wgrad8", stream)
+    _launch("tcq_wgrad8", dev, stream, lib.tcq_wgrad8, dz.data_ptr(), xt, lddz, packed.codes.data_ptr(),
+            packed.scales.data_ptr(), fmt, n, rows, cols, out.data_ptr(), lddw, int(accumulate), ws.data_ptr(),
             ws.numel())
     return out
 
