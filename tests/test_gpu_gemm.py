@@ -281,6 +281,50 @@ def test_wgrad8(n, rows, cols, dtype, fmt, pad, cuda_device):
     assert torch.equal(buf[:, :cols], dw)
 
 
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1801), ("f16", 1800)])
+def test_cut_last_round(dtype, rows, cuda_device):
+    """More tiles than the device takes at a time and a few left over: whole tiles and cut
+    ones in one product (74 pairs of multiprocessors take 88 and 90 tiles in two rounds)."""
+    import torch
+    from tests import gemm_reference as ref
+
+    rng = np.random.default_rng(rows)
+    n = 2600
+    args, w = ref.random_matrix(rng, 16, 2, 256, rows, 2560, "f16", True, cuda_device)
+    x = _x(rng, n, 2560, _dtype(dtype), cuda_device)
+    bias = torch.from_numpy(rng.standard_normal(rows)).float().to(cuda_device)
+    residual = _x(rng, n, rows, _dtype(dtype), cuda_device)
+    ck = tcq.Packed8(torch.empty((n, rows), dtype=torch.int8, device=cuda_device),
+                     torch.empty((n, -(-rows // 32)), dtype=torch.uint8, device=cuda_device))
+    y = tcq.gemm(*args, x, bias=bias, act="silu", residual=residual, checkpoint=ck)
+    check_gemm(args, w, x, y, "silu", bias, residual, ck)
+    dz = _x(rng, n, rows + 310, _dtype(dtype), cuda_device, std=1e-3)
+    packed = tcq.pack8(x[:, :2500].contiguous())
+    xv = ref.packed_values(packed)
+    want = dz.double().T @ xv
+    bound = (n / 16 + 2) * 2.0**-22 * (dz.double().abs().T @ xv.abs()) + 2.0**-24 * want.abs() + 1e-300
+    dw = tcq.wgrad8(dz, packed)
+    _check(dw, want, bound, "wgrad8")
+    tcq.wgrad8(dz, packed, out=dw, accumulate=True)
+    _check(dw, 2 * want, 2 * bound + 2.0**-23 * 2 * want.abs(), "wgrad8 accumulate")
+
+
+@pytest.mark.parametrize("rows,nb,n", [(2603, 8, 2600), (14336, 9, 2100)])
+def test_dgrad_cut_last_round(rows, nb, n, cuda_device):
+    """The same for the input gradient; the longer one goes through its tiles in bands, the
+    last of them one tile wide."""
+    from tests import gemm_reference as ref
+
+    rng = np.random.default_rng(rows + n)
+    args, w = ref.random_matrix(rng, 16, 2, 256, rows, nb * 256, "mad", False, cuda_device)
+    dz = _x(rng, n, rows, _dtype("f16"), cuda_device, std=1e-3)
+    dx = tcq.gemm_dgrad(*args, dz)
+    d = dz.double()
+    want = d @ w
+    bound = ref.product_bound(d, w.T.contiguous(), ref.weight_half_step(n, dz.dtype, True)) + 1e-300
+    _check(dx, want, bound + ref.half_step(dz.dtype) * (want.abs() + bound) + 2.0**-25, "dgrad")
+
+
 def test_wgrad8_without_tokens(cuda_device):
     import torch
 

@@ -27,10 +27,11 @@
 // (SM clock 1.4 to 1.55 GHz of 1.965 GHz), so the bound is the energy of the MMAs: a
 // 256 x 512 tile with two thirds of the operand traffic is no faster.
 //
-// Fewer tiles than half the pairs: the reduction is cut into as many pieces as there are
-// pairs for, each writes its fp32 sums to the workspace, and a second kernel adds a
-// tile's pieces in order and applies the epilogue (32 tokens through the input gradient
-// of a 14336 x 4096 matrix have 16 tiles of 224 stages: four pieces).
+// The last round of tiles, where it has work for half the pairs or fewer: a reduction is cut
+// into as many pieces as there are pairs for, each writes its fp32 sums to the workspace,
+// and a second kernel adds a tile's pieces in order and applies the epilogue (32 tokens
+// through the input gradient of a 14336 x 4096 matrix have 16 tiles of 224 stages: four
+// pieces; 4096 tokens have 256, three rounds of 74 and 34 more: two pieces each).
 //
 // Roles: warp 0 TMA, warp 1 MMA (first CTA of the pair only), warp 2 tensor memory,
 // warps 4 and up epilogue.  Barriers: full (both CTAs' loads of a stage landed; in the
@@ -100,6 +101,7 @@ constexpr int kTile = 256;            // rows and columns of a pair's tile
 constexpr int kDepth = 64;            // reduction depth of a stage
 constexpr int kHalfBytes = 128 * kDepth * 2;  // one CTA's half of one operand's stage
 constexpr int kBoxBytes = 32 * 128;   // a warp's box of the output: 32 rows of 128 bytes
+constexpr int kWorthCutting = 24;     // stages that cutting the last round's tiles has to save
 constexpr int kSegment = 20;          // stages (1280 deep) at most that the weight gradient sums in tensor memory
 
 // Four epilogue warps, two boxes each; the weight gradient has eight with one box, a
@@ -123,19 +125,49 @@ struct Shape {
     long long m, n, k;
     int m_tiles, n_tiles, k_steps;
     int fmt;
-    int pieces;  // of a tile's reduction; more than one: sums go to the workspace
+    int whole;   // tiles that are summed whole; the others' reductions are cut into
+    int pieces;  // pieces, whose sums go to the workspace
+    int across;  // neighbouring tiles of the order that run along one axis (tile_at)
+    bool rows_first;  // that axis is the rows'
 };
 
-// A pair's next piece of work: its tile's first row and column, its stages.
+// A pair's next piece of work: its tile's first row and column, its stages, and its place
+// in the workspace (-1: the whole tile).
 struct Item {
-    int m0, n0, k0, k1;
+    int m0, n0, k0, k1, slot;
 };
+
+// First row and column of a tile.  The order goes through bands of `across` tiles along
+// one axis, all of the other axis in each band, so that the tiles that run at a time share
+// their operands in L2 (tile_order).
+__device__ __forceinline__ int2 tile_at(const Shape& p, int tile)
+{
+    const int u_tiles = p.rows_first ? p.m_tiles : p.n_tiles, v_tiles = p.rows_first ? p.n_tiles : p.m_tiles;
+    const int band = tile / (p.across * v_tiles), in_band = tile - band * p.across * v_tiles;
+    const int left = u_tiles - band * p.across, width = left < p.across ? left : p.across;
+    const int v = in_band / width, u = band * p.across + in_band - v * width;
+    return p.rows_first ? make_int2(u * kTile, v * kTile) : make_int2(v * kTile, u * kTile);
+}
 
 __device__ __forceinline__ Item work_item(const Shape& p, int t)
 {
-    const int tile = p.pieces == 1 ? t : t / p.pieces, piece = t - tile * p.pieces;
-    return {tile % p.m_tiles * kTile, tile / p.m_tiles * kTile, p.k_steps * piece / p.pieces,
-            p.k_steps * (piece + 1) / p.pieces};
+    const int slot = t - p.whole;
+    const int tile = slot < 0 ? t : p.whole + slot / p.pieces, piece = slot < 0 ? 0 : slot % p.pieces;
+    const int2 at = tile_at(p, tile);
+    if (slot < 0) return {at.x, at.y, 0, p.k_steps, -1};
+    return {at.x, at.y, (int)((long long)p.k_steps * piece / p.pieces), (int)((long long)p.k_steps * (piece + 1) / p.pieces),
+            slot};
+}
+
+// Stages between two accumulator sets: all, or in the weight gradient equal parts of at
+// most kSegment.
+template <int KIND>
+__device__ __forceinline__ int segment_of(const Item& w)
+{
+    const int n = w.k1 - w.k0;
+    if (KIND != kGemmWgrad || n <= kSegment) return n;
+    const int parts = (n + kSegment - 1) / kSegment;
+    return (n + parts - 1) / parts;
 }
 
 // 32 values of one row through the epilogue: row r, columns c .. c + 31, `count` of them
@@ -281,19 +313,17 @@ __device__ __forceinline__ void box32(unsigned char* row, int lane, int half, co
 template <int KIND, int XT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(KIND), 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-            const __grid_constant__ CUtensorMap map_out, Shape p, Epilogue e, bool vec, bool tma_out, unsigned int* err)
+            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_sums, Shape p, Epilogue e,
+            bool vec, bool tma_out, unsigned int* err)
 {
-    // with pieces, map_out is the workspace's: [tile, piece, 256 rows] x 256 columns, fp32
+    // map_sums: the workspace, [slot, 256 rows] x 256 columns, fp32
     constexpr int AMN = KIND == kGemmWgrad, BMN = KIND != kGemmForward, EW = epilogue_warps(KIND);
-    // stages between two accumulator sets: equal parts of at most kSegment, or all
-    const int parts = KIND == kGemmWgrad ? (p.k_steps + kSegment * p.pieces - 1) / (kSegment * p.pieces) : 1;
-    const int segment = (p.k_steps + p.pieces * parts - 1) / (p.pieces * parts) + (p.pieces > 1);
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem& S = *reinterpret_cast<Smem*>(raw);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int items = p.m_tiles * p.n_tiles * p.pieces;
+    const int items = p.whole + (p.m_tiles * p.n_tiles - p.whole) * p.pieces;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_addr(&S.full[i]), 1);
@@ -361,6 +391,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             bool ok = true;
             for (int t = pair; t < items && ok; t += pairs) {
                 const Item w = work_item(p, t);
+                const int segment = segment_of<KIND>(w);
                 for (int k0 = w.k0; k0 < w.k1 && ok; k0 += segment, ++done) {
                     const int acc = done & 1;
                     ok = mbar_wait(smem_addr(&S.tempty[acc]), ((done >> 1) & 1) ^ 1, stop, err);
@@ -399,14 +430,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         for (int t = pair; t < items && ok; t += pairs) {
             const Item w = work_item(p, t);
             // rows and columns in the output, or in the workspace
-            const bool cut = p.pieces > 1;
-            const int out_row = cut ? t * kTile : w.m0, out_col = cut ? 0 : w.n0;
+            const bool cut = w.slot >= 0;
+            const int out_row = cut ? w.slot * kTile : w.m0, out_col = cut ? 0 : w.n0;
             if constexpr (KIND == kGemmWgrad) {
                 const int half = (warp - 4) >> 2;
                 unsigned char* box = S.box[warp - 4];
                 float sum[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+                const int segment = segment_of<KIND>(w);
                 for (int k0 = w.k0; k0 < w.k1 && ok; k0 += segment, ++done) {
                     const int acc = done & 1;
                     ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
@@ -454,7 +486,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             if (e.accumulate && !cut)
                                 tma_add_2d(&map_out, smem_addr(box), c, r0);
                             else
-                                tma_store_2d(&map_out, smem_addr(box), out_col + c - w.n0, out_row + local);
+                                tma_store_2d(cut ? &map_sums : &map_out, smem_addr(box), out_col + c - w.n0, out_row + local);
                             bulk_commit();
                         }
                     }
@@ -495,7 +527,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         fence_async_shared();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&map_out, smem_addr(box), c, out_row + local);
+                            tma_store_2d(&map_sums, smem_addr(box), c, out_row + local);
                             bulk_commit();
                         }
                     }
@@ -558,13 +590,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 template <int KIND, int XT>
 __global__ void __launch_bounds__(256) finish_kernel(Shape p, Epilogue e, const float* partial, bool vec)
 {
-    const int lane = threadIdx.x & 31, tile = blockIdx.x;
+    const int lane = threadIdx.x & 31, tile = p.whole + blockIdx.x;
     const int local = blockIdx.y * 8 + (threadIdx.x >> 5), c = blockIdx.z * 128 + 4 * lane;
-    const long long r = (long long)(tile % p.m_tiles) * kTile + local;
-    const long long n0 = (long long)(tile / p.m_tiles) * kTile;
+    const int2 at = tile_at(p, tile);
+    const long long r = (long long)at.x + local, n0 = at.y;
     pdl_wait();
     if (r >= p.m || n0 + blockIdx.z * 128 >= p.n) return;
-    const float* src = partial + ((long long)tile * p.pieces * kTile + local) * kTile + c;
+    const float* src = partial + ((long long)blockIdx.x * p.pieces * kTile + local) * kTile + c;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = 0; i < p.pieces; ++i) {
@@ -577,62 +609,90 @@ __global__ void __launch_bounds__(256) finish_kernel(Shape p, Epilogue e, const 
         finish_quad<XT>(e, r, n0 + c, p.n, v, vec);
 }
 
-// Pieces of a tile's reduction: as many as there are pairs for, at least four stages each.
-int reduction_pieces(long long tiles, int k_steps, int pairs)
+// The order of the tiles.  The axis with fewer tiles goes first: where its operand is
+// small enough to stay in L2 the other is read once (DRAM reads of the weight gradient of
+// 4096 tokens, 14336 x 4096: 1440 MB the other way round, 235 MB and 400 -> 347 us so).  Where it is not,
+// bands of about the square root of the tiles that run at a time read the least.
+void tile_order(Shape& s, int pairs)
 {
-    if (tiles > pairs / 2) return 1;
-    int p = pairs / (int)tiles;
-    if (p > k_steps / 4) p = k_steps / 4;
-    return p < 1 ? 1 : p;
+    constexpr long long kStays = 48ll << 20;
+    s.rows_first = s.m_tiles <= s.n_tiles;
+    const int tiles = s.rows_first ? s.m_tiles : s.n_tiles;
+    int root = 1;
+    while ((root + 1) * (root + 1) <= pairs) ++root;
+    s.across = 2ll * kTile * s.k * tiles <= kStays || tiles < root ? tiles : root;
 }
+
+// The tiles that whole rounds of the pairs leave over are cut, each into as many pieces as
+// there are pairs for, at least four stages each, where that saves more than the second
+// kernel costs.
+void cut_rest(Shape& s, int pairs)
+{
+    const long long tiles = (long long)s.m_tiles * s.n_tiles;
+    const int rest = (int)(tiles % pairs);
+    s.whole = (int)tiles;
+    s.pieces = 1;
+    if (rest == 0 || rest > pairs / 2) return;
+    int p = pairs / rest;
+    if (p > s.k_steps / 4) p = s.k_steps / 4;
+    if (p < 2) return;
+    if (tiles > rest && s.k_steps - s.k_steps / p < kWorthCutting) return;
+    s.whole = (int)(tiles - rest);
+    s.pieces = p;
+}
+
+Shape shape_of(long long m, long long n, long long k, int num_sms)
+{
+    Shape s = {};
+    s.m = m;
+    s.n = n;
+    s.k = k;
+    s.m_tiles = (int)((m + kTile - 1) / kTile);
+    s.n_tiles = (int)((n + kTile - 1) / kTile);
+    s.k_steps = (int)((k + kDepth - 1) / kDepth);
+    tile_order(s, num_sms / 2);
+    cut_rest(s, num_sms / 2);
+    return s;
+}
+
+long long slots(const Shape& s) { return s.pieces > 1 ? ((long long)s.m_tiles * s.n_tiles - s.whole) * s.pieces : 0; }
 
 template <int KIND, int XT>
 cudaError_t launch(const GemmProblem& g, const Epilogue& e, float* partial, int num_sms, unsigned int* err,
                    cudaStream_t stream)
 {
-    CUtensorMap ma, mb, mo;
+    const long long tiles = (g.m + kTile - 1) / kTile * ((g.n + kTile - 1) / kTile);
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    CUtensorMap ma, mb, mo, ms;
     const bool ok = (KIND == kGemmWgrad ? make_map_16bit(&ma, g.a, g.k, g.m, g.lda, 64)
                                         : make_map_16bit(&ma, g.a, g.m, g.k, g.lda, 128)) &&
                     (KIND == kGemmForward ? make_map_16bit(&mb, g.b, g.n, g.k, g.ldb, 128)
                                           : make_map_16bit(&mb, g.b, g.k, g.n, g.ldb, 64));
     if (!ok) return cudaErrorInvalidValue;
-    Shape s;
-    s.m = g.m;
-    s.n = g.n;
-    s.k = g.k;
-    s.m_tiles = (int)((g.m + kTile - 1) / kTile);
-    s.n_tiles = (int)((g.n + kTile - 1) / kTile);
-    s.k_steps = (int)((g.k + kDepth - 1) / kDepth);
+    Shape s = shape_of(g.m, g.n, g.k, num_sms);
     s.fmt = g.fmt;
     const int es = KIND == kGemmWgrad ? 4 : 2;
     bool vec = (reinterpret_cast<uintptr_t>(e.out) & 15) == 0 && e.ldo * es % 16 == 0;
-    const long long tiles = (long long)s.m_tiles * s.n_tiles;
-    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-    s.pieces = reduction_pieces(tiles, s.k_steps, num_sms / 2);
     const bool tma_out = vec;
-    if (s.pieces > 1) {
-        if (!make_map_out(&mo, partial, tiles * s.pieces * kTile, kTile, kTile, 4)) return cudaErrorInvalidValue;
-    } else if (!tma_out) {
-        mo = ma;  // not used
-    } else if (!make_map_out(&mo, e.out, g.m, g.n, e.ldo, es)) {
-        return cudaErrorInvalidValue;
-    }
+    mo = ms = ma;  // where they are not used
+    if (tma_out && !make_map_out(&mo, e.out, g.m, g.n, e.ldo, es)) return cudaErrorInvalidValue;
+    if (s.pieces > 1 && !make_map_out(&ms, partial, slots(s) * kTile, kTile, kTile, 4)) return cudaErrorInvalidValue;
     // the residual by 16-byte loads: rows of whole vectors
     if (e.residual)
         vec = (reinterpret_cast<uintptr_t>(e.residual) & 15) == 0 && e.ldr % 8 == 0 && g.n % 8 == 0;
     cudaError_t st = cudaFuncSetAttribute(gemm_kernel<KIND, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)sizeof(Smem));
     if (st != cudaSuccess) return st;
-    const long long items = tiles * s.pieces;
+    const long long items = s.whole + (s.pieces > 1 ? slots(s) : 0);
     const int pairs = (int)(items < num_sms / 2 ? items : num_sms / 2);
     // every product comes after a launch of its own call (the decode, the unpacking)
     st = launch_pdl(gemm_kernel<KIND, XT>, dim3(2 * pairs), dim3(gemm_threads(KIND)), sizeof(Smem), stream, true, ma, mb, mo,
-                    s, e, vec, tma_out, err);
+                    ms, s, e, vec, tma_out, err);
     if (st != cudaSuccess || s.pieces == 1) return st;
     // quads: 8-byte accesses
     bool quads = (reinterpret_cast<uintptr_t>(e.out) & 7) == 0 && e.ldo % 4 == 0;
     if (e.residual) quads = quads && (reinterpret_cast<uintptr_t>(e.residual) & 7) == 0 && e.ldr % 4 == 0;
-    return launch_pdl(finish_kernel<KIND, XT>, dim3((unsigned)tiles, kTile / 8, kTile / 128), dim3(256), 0, stream, true, s,
+    return launch_pdl(finish_kernel<KIND, XT>, dim3((unsigned)(tiles - s.whole), kTile / 8, kTile / 128), dim3(256), 0, stream, true, s,
                       e, static_cast<const float*>(partial), quads);
 }
 
@@ -640,10 +700,8 @@ cudaError_t launch(const GemmProblem& g, const Epilogue& e, float* partial, int 
 
 size_t gemm_partial_bytes(long long m, long long n, long long k, int num_sms)
 {
-    const long long tiles = (m + kTile - 1) / kTile * ((n + kTile - 1) / kTile);
-    if (tiles > num_sms / 2) return 0;
-    const int pieces = reduction_pieces(tiles, (int)((k + kDepth - 1) / kDepth), num_sms / 2);
-    return pieces > 1 ? (size_t)tiles * pieces * kTile * kTile * sizeof(float) : 0;
+    if ((m + kTile - 1) / kTile * ((n + kTile - 1) / kTile) > INT32_MAX / 2) return 0;  // refused by the launch
+    return (size_t)slots(shape_of(m, n, k, num_sms)) * kTile * kTile * sizeof(float);
 }
 
 cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, float* partial, int num_sms,
