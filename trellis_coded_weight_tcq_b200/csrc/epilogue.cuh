@@ -40,8 +40,7 @@ __device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long
                 e.z_codes[t * rows + r + i] = byte == 255u ? 0 : (uint8_t)(int8 ? q8_encode<TCQ_Q8_INT8>(v[i], inv)
                                                                               : q8_encode<TCQ_Q8_E4M3>(v[i], inv));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], e.act);
+    act_values(v, e.act);
     uint16_t* out = static_cast<uint16_t*>(e.out) + t * e.ldo + r;
     const uint16_t* res = e.residual ? static_cast<const uint16_t*>(e.residual) + t * e.ldr + r : nullptr;
     if (vec && count == 4) {

@@ -103,16 +103,18 @@ constexpr int kHalfBytes = 128 * kDepth * 2;  // one CTA's half of one operand's
 constexpr int kBoxBytes = 32 * 128;   // a warp's box of the output: 32 rows of 128 bytes
 constexpr int kSegment = 20;          // stages (1280 deep) at most that the weight gradient sums in tensor memory
 
-// Four epilogue warps, two boxes each; the weight gradient has eight with one box, a
-// half of the tile's columns each, because they hold their sums in registers.
-__host__ __device__ constexpr int epilogue_warps(int kind) { return kind == kGemmWgrad ? 8 : 4; }
+// The input gradient has four epilogue warps with two boxes each.  The others have eight
+// with one box, a half of the tile's columns each: the weight gradient's hold their sums in
+// registers, and four would take longer over the forward product's activations than the
+// tensor cores over the next tile (41k cycles against 37k for 4096 deep tiles, GELU).
+__host__ __device__ constexpr int epilogue_warps(int kind) { return kind == kGemmDgrad ? 4 : 8; }
 __host__ __device__ constexpr int gemm_threads(int kind) { return 128 + 32 * epilogue_warps(kind); }
 
 struct __align__(1024) Smem {
     unsigned char a[kStages][kHalfBytes];
     unsigned char b[kStages][kHalfBytes];
     unsigned char box[8][kBoxBytes];
-    float2 cols[kTile];  // (power of two, bias) of a tile's columns
+    float4 cols[kTile / 2];  // the powers of two and the biases of two columns of a tile
     unsigned long long full[kStages], empty[kStages], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int stop;
@@ -173,18 +175,19 @@ __device__ __forceinline__ int segment_of(const Item& w)
 // below n.
 template <int KIND, int XT>
 __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                        int count, bool vec, float row_scale, const float2* cols,
+                                        int count, bool vec, float row_scale, const float4* cols,
                                         const unsigned char* box_row, int half)
 {
+    if (e.row_scale) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= row_scale;
+        for (int i = 0; i < 32; ++i) v[i] *= row_scale;
+    }
     if constexpr (KIND == kGemmForward) {
         if (e.col_scale || e.bias) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {  // two columns per 16-byte read, the same in every lane
-                const float4 p = *reinterpret_cast<const float4*>(cols + i);
-                v[i] = fmaf(v[i], p.x, p.y);
-                v[i + 1] = fmaf(v[i + 1], p.z, p.w);
+                const float4 p = cols[i / 2];
+                f2_split(f2_fma(f2(v[i], v[i + 1]), f2(p.x, p.y), f2(p.z, p.w)), v[i], v[i + 1]);
             }
         }
         if (e.z_codes) {
@@ -217,25 +220,7 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
                     if (i < count) z[i] = (uint8_t)(code[i / 4] >> (8 * (i & 3)));
             }
         }
-        switch (e.act) {  // one loop per activation: the choice is made once
-        case TCQ_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_RELU);
-            break;
-        case TCQ_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_SILU);
-            break;
-        case TCQ_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_GELU);
-            break;
-        case TCQ_ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_value(v[i], TCQ_ACT_GELU_TANH);
-            break;
-        default: break;
-        }
+        act_values(v, e.act);
         if (e.residual) {
             const uint16_t* res = static_cast<const uint16_t*>(e.residual) + r * e.ldr + c;
             if (vec) {
@@ -491,34 +476,37 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                 }
             } else {
+                constexpr int boxes = 8 / EW, span = kTile * 4 / EW;  // a warp's boxes and columns
+                const int c0 = (warp - 4) / 4 * span;
                 const int local = (int)rank * 128 + quarter * 32;
                 const long long r0 = w.m0 + local, r = r0 + lane, n0 = w.n0;
                 const int acc = done & 1;
                 if constexpr (KIND == kGemmForward) {
                     // this tile's columns, while its product still runs
-                    named_barrier(1, 128);  // the last tile's have been read
-                    for (int i = threadIdx.x - 128; i < kTile; i += 128) {
+                    named_barrier(1, 32 * EW);  // the last tile's have been read
+                    for (int i = threadIdx.x - 128; i < kTile; i += 32 * EW) {
                         const long long c = n0 + i;
-                        S.cols[i] = make_float2(e.col_scale && c < p.n ? __ldcg(e.col_scale + c) : 1.f,
-                                                e.bias && c < p.n ? __ldg(e.bias + c) : 0.f);
+                        float* at = reinterpret_cast<float*>(S.cols + i / 2) + (i & 1);
+                        at[0] = e.col_scale && c < p.n ? __ldcg(e.col_scale + c) : 1.f;
+                        at[2] = e.bias && c < p.n ? __ldg(e.bias + c) : 0.f;
                     }
                 }
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
                 // the columns are there; after a wait that gave up all warps stop together, or
                 // the others would wait at the next barrier
-                if constexpr (KIND == kGemmForward) ok = named_all(1, 128, ok);
+                if constexpr (KIND == kGemmForward) ok = named_all(1, 32 * EW, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const float row_scale = e.row_scale && r < p.m ? __ldcg(e.row_scale + r) : 1.f;
                 if (cut) {  // the sums as they are, 32 columns at a time
 #pragma unroll 1
-                    for (int c = 0; c < kTile; c += 32) {
+                    for (int c = c0; c < c0 + span; c += 32) {
                         if (n0 + c >= p.n || r0 >= p.m) break;
-                        unsigned char* box = S.box[2 * quarter + ((c >> 5) & 1)];
-                        if (lane == 0) bulk_wait_read<1>();
-                        __syncwarp();
+                        unsigned char* box = S.box[(warp - 4) * boxes + ((c >> 5) & (boxes - 1))];
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c, v);
+                        if (lane == 0) bulk_wait_read<boxes - 1>();
+                        __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             *reinterpret_cast<float4*>(box + lane * 128 + ((i ^ (lane & 7)) << 4)) =
@@ -532,14 +520,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                 }
 #pragma unroll 1
-                for (int c = cut ? kTile : 0; c < kTile; c += 64) {
+                for (int c = cut ? c0 + span : c0; c < c0 + span; c += 64) {
                     if (n0 + c >= p.n || r0 >= p.m) break;  // the same in every lane
-                    unsigned char* box = S.box[2 * quarter + ((c >> 6) & 1)];
-                    if (lane == 0) bulk_wait_read<1>();  // the box's last store, two ago, has been read
-                    __syncwarp();
+                    unsigned char* box = S.box[(warp - 4) * boxes + ((c >> 6) & (boxes - 1))];
+                    auto box_free = [&] {  // its last store has been read
+                        if (lane == 0) bulk_wait_read<boxes - 1>();
+                        __syncwarp();
+                    };
                     const int rows = p.m - r0 < 32 ? (int)(p.m - r0) : 32, cols = p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64;
                     if (KIND == kGemmForward && e.residual && !vec) {
                         // each half's values make room for that half's outputs
+                        box_free();
                         load_rows(box, static_cast<const uint16_t*>(e.residual) + r0 * e.ldr + n0 + c, e.ldr, rows, cols, lane);
                         __syncwarp();
                     }
@@ -550,8 +541,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c + 32 * h, v);
                         const int count = p.n - ch < 32 ? (int)(p.n - ch) : 32;
-                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale, S.cols + c + 32 * h,
-                                                       box + lane * 128, h);
+                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale,
+                                                       S.cols + (c + 32 * h) / 2, box + lane * 128, h);
+                        if (h == 0 && !(KIND == kGemmForward && e.residual && !vec)) box_free();
                         box32<XT>(box + lane * 128, lane, h, v);
                         __syncwarp();
                     }

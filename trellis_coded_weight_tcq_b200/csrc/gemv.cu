@@ -53,7 +53,9 @@ struct VectorLayer {
     }
     static __device__ __forceinline__ void store(const Args& a, long long r, float v)
     {
-        v = act_value(a.e.bias ? v + __ldg(a.e.bias + r) : v, a.e.act);
+        float z[1] = {a.e.bias ? v + __ldg(a.e.bias + r) : v};
+        act_values(z, a.e.act);
+        v = z[0];
         if (a.e.residual) v += x_load<XT>(a.e.residual, r);
         static_cast<uint16_t*>(a.e.out)[r] = x_bits<XT>(v);
     }

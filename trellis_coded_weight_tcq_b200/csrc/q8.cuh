@@ -161,20 +161,6 @@ __device__ __forceinline__ float2 x_unpack2(uint32_t v)
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// 1 / (1 + e^-t); the exponential overflows to infinity and the quotient to 0 as they should
-__device__ __forceinline__ float sigmoidf(float t) { return __fdividef(1.f, 1.f + __expf(-t)); }
-
-__device__ __forceinline__ float act_value(float z, int act)
-{
-    switch (act) {
-    case TCQ_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
-    case TCQ_ACT_SILU: return z == -INFINITY ? -0.f : z * sigmoidf(z);
-    case TCQ_ACT_GELU: return z == -INFINITY ? -0.f : 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
-    case TCQ_ACT_GELU_TANH: return z == -INFINITY ? -0.f : z * sigmoidf(2.f * kGeluA * (z + kGeluB * z * z * z));
-    default: return z;
-    }
-}
-
 // ---- two fp32 operations in one instruction (each rounds like the scalar one)
 struct F2 {
     unsigned long long v;
@@ -238,6 +224,62 @@ __device__ __forceinline__ F2 f2_logistic2(F2 t)
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// z, or the lowest finite number where it is below (whose product with the logistic
+// function's 0 is 0); NaN stays
+__device__ __forceinline__ float finite_below(float z)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, 0fFF7FFFFF;" : "=f"(r) : "f"(z));
+    return r;
+}
+
+// An activation of two z.
+template <int ACT>
+__device__ __forceinline__ F2 act_value2(F2 z)
+{
+    if constexpr (ACT == TCQ_ACT_NONE) {
+        return z;
+    } else {
+        float a, b;
+        f2_split(z, a, b);
+        if constexpr (ACT == TCQ_ACT_RELU) {
+            return f2(a > 0.f ? a : (a != a ? a : 0.f), b > 0.f ? b : (b != b ? b : 0.f));
+        } else if constexpr (ACT == TCQ_ACT_GELU) {
+            auto gelu = [](float x) { return x == -INFINITY ? -0.f : 0.5f * x * (1.f + erff(x * 0.7071067811865476f)); };
+            return f2(gelu(a), gelu(b));
+        } else {
+            z = f2(finite_below(a), finite_below(b));
+            if constexpr (ACT == TCQ_ACT_SILU) return f2_mul(z, f2_logistic2(f2_mul(z, f2(-kLog2e, -kLog2e))));
+            constexpr float a0 = -2.f * kGeluA * kLog2e, a1 = a0 * kGeluB;
+            return f2_mul(z, f2_logistic2(f2_mul(z, f2_fma(f2_mul(z, z), f2(a1, a1), f2(a0, a0)))));
+        }
+    }
+}
+
+// N values at once: the choice is made once.
+template <int N>
+__device__ __forceinline__ void act_values(float (&v)[N], int act)
+{
+    auto all = [&](auto one) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            if constexpr (N == 1) {
+                float unused;
+                f2_split(one(f2(v[0], 0.f)), v[0], unused);
+            } else {
+                f2_split(one(f2(v[i], v[i + 1])), v[i], v[i + 1]);
+            }
+        }
+    };
+    switch (act) {
+    case TCQ_ACT_RELU: all([](F2 z) { return act_value2<TCQ_ACT_RELU>(z); }); break;
+    case TCQ_ACT_SILU: all([](F2 z) { return act_value2<TCQ_ACT_SILU>(z); }); break;
+    case TCQ_ACT_GELU: all([](F2 z) { return act_value2<TCQ_ACT_GELU>(z); }); break;
+    case TCQ_ACT_GELU_TANH: all([](F2 z) { return act_value2<TCQ_ACT_GELU_TANH>(z); }); break;
+    default: break;
+    }
+}
 
 // An activation's derivative at two finite z below 2^33 (0 at 0 for relu).  With s the
 // logistic function: silu' = s + z s (1 - s); gelu_tanh' = s + z s (1 - s) 2 u', s at 2 u.
