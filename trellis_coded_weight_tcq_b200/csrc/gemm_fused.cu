@@ -205,7 +205,8 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
 #pragma unroll
                 for (int h = 0; h < 2 * K; ++h) nwords[h] = 0u;
             }
-            if (bits && c < cols) {
+            if (bits && c < cols && TCQ_IN_BOUNDS(bits - w.bits + c / 32 * K + 2 * K - 1, w.rows * (cols / 32 * K)) &&
+                TCQ_IN_BOUNDS(start - w.start_state + j, w.rows * nb)) {
                 if (!p.boxes) load_words<K>(bits + c / 32 * K, nwords, wide);
                 if (nfirst)
                     nprev = __ldg(start + j);
@@ -241,7 +242,9 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                 float d[16];
                 tmem_load16(lanes + c, d);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) __stcg(out + (long long)(c + i) * kRows, d[i]);
+                for (int i = 0; i < 16; ++i)
+                    if (TCQ_IN_BOUNDS(out - partial + (long long)(c + i) * kRows, (long long)p.row_tiles * p.pieces * p.np * kRows))
+                        __stcg(out + (long long)(c + i) * kRows, d[i]);
             }
             tc_fence_before();
             __syncwarp();

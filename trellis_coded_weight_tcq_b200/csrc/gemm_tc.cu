@@ -7,7 +7,7 @@
 // 256 x 256 tile: each CTA loads its half of both operands by TMA, 128 x 64 elements
 // of each per stage, six stages deep (192 KB), and one thread of the first CTA issues
 // the pair's MMAs (256 x 256 x 16).  The accumulators take 256 columns of each CTA's
-// tensor memory; two sets of them let the four epilogue warps store a tile while the
+// tensor memory; two sets of them let the epilogue warps store a tile while the
 // next one is multiplied.  The grid is persistent, one pair per two SMs.
 //
 // Outputs that TMA can address (16-byte aligned base and rows) leave through shared
@@ -21,11 +21,13 @@
 // in registers (root mean square error against float64 at 4096 tokens, relative to the
 // gradient's: 1.6e-6 without, 2.8e-7 with).
 //
-// Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP): forward 373 us,
-// input gradient 339 us, weight gradient 363 us of kernel time; the plain product of the
-// vendor library takes 346 to 352 us there.  All of them run at the board's power limit
-// (SM clock 1.4 to 1.55 GHz of 1.965 GHz), so the bound is the energy of the MMAs: a
-// 256 x 512 tile with two thirds of the operand traffic is no faster.
+// Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP), with the second
+// kernel: forward with GELU 322 us, input gradient 311 us, weight gradient 335 us; @CUBLAS@.
+// In long runs the board's power limit holds the SM clock at 1.4 to 1.55 GHz of 1.965,
+// so what costs energy costs time: the order of the tiles took 50 us off the weight
+// gradient.  Clock stamps: a stage takes 571 cycles of the pipe's 512 in the input
+// gradient; the gap is the load behind the ring of six (a seventh stage does not fit beside
+// the boxes).
 //
 // The last round of tiles, where it has work for half the pairs or fewer: a reduction is cut
 // into as many pieces as there are pairs for, each writes its fp32 sums to the workspace,

@@ -87,9 +87,10 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
         uint32_t w[4];
 #pragma unroll
         for (int h = 0; h < 4; ++h) w[h] = x_pack2<TCQ_X_F16>(f[2 * h] * inv, f[2 * h + 1] * inv);
-        *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (TCQ_IN_BOUNDS(r * a.ldo + c + 7, a.n * a.ldo))
+            *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    for (long long c = vcols + threadIdx.x; c < a.cols; c += kThreads)
+    for (long long c = vcols + threadIdx.x; c < a.cols && TCQ_IN_BOUNDS(r * a.ldo + c, a.n * a.ldo); c += kThreads)
         o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (a.col_exponents ? power_of(a.col_exponents[c]) : 1.f) * inv);
 }
 
@@ -120,8 +121,9 @@ __global__ void __launch_bounds__(kThreads) copy16_kernel(const uint16_t* x, lon
             uint32_t v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? x[r * ldx + c + i] : 0u;
-            *reinterpret_cast<uint4*>(out + r * ldo + c) =
-                make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+            if (TCQ_IN_BOUNDS(r * ldo + c + 7, n * ldo))
+                *reinterpret_cast<uint4*>(out + r * ldo + c) =
+                    make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
         }
     if (blockIdx.x == gridDim.x - 1) pdl_wait();  // as above
 }

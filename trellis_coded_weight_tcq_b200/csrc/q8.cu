@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(kThreads) pack8_vec_kernel(const uint16_t* x, 
         for (long long i = (long long)blockIdx.y * blockDim.x + threadIdx.x; i - (threadIdx.x & 31) < 2 * groups;
              i += (long long)gridDim.y * blockDim.x) {
             const long long c = 16 * i;
-            const bool in = c < cols;
+            const bool in = c < cols && TCQ_IN_BOUNDS(r * ldx + c + 15, (n - 1) * ldx + cols) &&
+                            TCQ_IN_BOUNDS(r * cols + c + 15, n * cols);
             uint32_t w[8] = {};
             if (in) {
                 const uint4 a = *reinterpret_cast<const uint4*>(xr + c), b = *reinterpret_cast<const uint4*>(xr + c + 8);
@@ -109,8 +110,8 @@ __global__ void __launch_bounds__(kThreads) pack8_kernel(const uint16_t* x, long
             const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
             const uint32_t byte = q8_scale_byte<FMT>(top);
             const float inv = q8_inv(byte);
-            if (c < cols) codes[r * cols + c] = inv != 0.f ? (uint8_t)q8_encode<FMT>(v, inv) : (uint8_t)0;
-            if ((threadIdx.x & 31) == 0) scales[r * groups + g] = (uint8_t)byte;
+            if (c < cols && TCQ_IN_BOUNDS(r * cols + c, n * cols)) codes[r * cols + c] = inv != 0.f ? (uint8_t)q8_encode<FMT>(v, inv) : (uint8_t)0;
+            if ((threadIdx.x & 31) == 0 && TCQ_IN_BOUNDS(r * groups + g, n * groups)) scales[r * groups + g] = (uint8_t)byte;
         }
     }
 }
@@ -148,7 +149,8 @@ __global__ void __launch_bounds__(kThreads) unpack8_vec_kernel(const uint8_t* co
                 q8_codes4<FMT>(w[h].y, f + 4);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = in_range<XT>(f[j] * s);
-                store8<XT>(xr + 8 * (i + h * step), f);
+                if (TCQ_IN_BOUNDS(r * ldx + 8 * (i + h * step) + 7, (n - 1) * ldx + cols))
+                    store8<XT>(xr + 8 * (i + h * step), f);
             }
         }
     }
@@ -163,8 +165,9 @@ __global__ void __launch_bounds__(kThreads) unpack8_kernel(const uint8_t* codes,
     for (long long r = blockIdx.x; r < n; r += gridDim.x) {
         for (long long c = (long long)blockIdx.y * blockDim.x + threadIdx.x; c < cols;
              c += (long long)gridDim.y * blockDim.x)
-            x[r * ldx + c] = x_bits<XT>(
-                in_range<XT>(q8_decode<FMT>(codes[r * cols + c], q8_scale(__ldg(scales + r * groups + c / 32)))));
+            if (TCQ_IN_BOUNDS(r * ldx + c, (n - 1) * ldx + cols))
+                x[r * ldx + c] = x_bits<XT>(
+                    in_range<XT>(q8_decode<FMT>(codes[r * cols + c], q8_scale(__ldg(scales + r * groups + c / 32)))));
     }
 }
 
@@ -200,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 4) act_grad8_kernel(ActGradArgs a)
         const uint8_t* zs = ACT == TCQ_ACT_NONE ? nullptr : a.z_scales + first * groups + c / 32;
         auto fetch = [&]() {
             Row v = {};
-            if (ahead-- > 0) {
+            if (ahead-- > 0 &&
+                TCQ_IN_BOUNDS(dy - static_cast<const uint16_t*>(a.dy) + CPT - 1, (a.n - 1) * a.lddy + a.rows)) {
                 if constexpr (CPT == 8)
                     v.d = *reinterpret_cast<const uint4*>(dy);
                 else
@@ -242,10 +246,12 @@ __global__ void __launch_bounds__(kThreads, 4) act_grad8_kernel(ActGradArgs a)
                 f2_split(t, u, v);
                 o[i] = x_pack2<XT>(u, v);
             }
-            if constexpr (CPT == 8)
-                *reinterpret_cast<uint4*>(dz) = make_uint4(o[0], o[1], o[2], o[3]);
-            else
-                *dz = (uint16_t)o[0];
+            if (TCQ_IN_BOUNDS(dz - static_cast<uint16_t*>(a.dz) + CPT - 1, (a.n - 1) * a.lddz + a.rows)) {
+                if constexpr (CPT == 8)
+                    *reinterpret_cast<uint4*>(dz) = make_uint4(o[0], o[1], o[2], o[3]);
+                else
+                    *dz = (uint16_t)o[0];
+            }
             dz += kRowThreads * a.lddz;
             now = next;
         }
@@ -265,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 4) act_grad8_kernel(ActGradArgs a)
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < kRowThreads; ++k) s += part[k][j];
-        a.partial[(long long)blockIdx.y * a.rows + col] = s;
+        if (TCQ_IN_BOUNDS((long long)blockIdx.y * a.rows + col, a.splits * a.rows))
+            a.partial[(long long)blockIdx.y * a.rows + col] = s;
     }
 }
 
