@@ -21,13 +21,13 @@
 // in registers (root mean square error against float64 at 4096 tokens, relative to the
 // gradient's: 1.6e-6 without, 2.8e-7 with).
 //
-// Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP), with the second
-// kernel: forward with GELU 322 us, input gradient 311 us, weight gradient 335 us; @CUBLAS@.
-// In long runs the board's power limit holds the SM clock at 1.4 to 1.55 GHz of 1.965,
-// so what costs energy costs time: the order of the tiles took 50 us off the weight
-// gradient.  Clock stamps: a stage takes 571 cycles of the pipe's 512 in the input
-// gradient; the gap is the load behind the ring of six (a seventh stage does not fit beside
-// the boxes).
+// Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP), alone and with the
+// second kernel: forward with GELU about 315 us, input gradient 311 us, weight gradient
+// 335 us; the vendor library's bare products take 324 to 360 us there.  In long runs the
+// board's power limit holds the SM clock at 1.4 to 1.55 GHz of 1.965, so what costs energy
+// costs time: the order of the tiles took 50 us off the weight gradient.  Clock stamps: a
+// stage takes 571 cycles of the pipe's 512 in the input gradient; the gap is the latency of
+// loads behind a ring of six (a seventh stage does not fit beside the boxes).
 //
 // The last round of tiles, where it has work for half the pairs or fewer: a reduction is cut
 // into as many pieces as there are pairs for, each writes its fp32 sums to the workspace,
@@ -177,7 +177,7 @@ __device__ __forceinline__ int segment_of(const Item& w)
 // below n.
 template <int KIND, int XT>
 __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                        int count, bool vec, float row_scale, const float4* cols,
+                                        int count, float row_scale, const float4* cols,
                                         const unsigned char* box_row, int half)
 {
     if (e.row_scale) {
@@ -223,32 +223,16 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
             }
         }
         act_values(v, e.act);
-        if (e.residual) {
-            const uint16_t* res = static_cast<const uint16_t*>(e.residual) + r * e.ldr + c;
-            if (vec) {
+        if (e.residual) {  // from the warp's box (load_rows)
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    if (i >= count) break;  // rows of whole 16-byte vectors: all or none of the eight
-                    const uint4 t = *reinterpret_cast<const uint4*>(res + i);
-                    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+            for (int i = 0; i < 4; ++i) {
+                const uint4 t = *reinterpret_cast<const uint4*>(box_row + (((4 * half + i) ^ (threadIdx.x & 7)) << 4));
+                const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const float2 f = x_unpack2<XT>(w[h]);
-                        v[i + 2 * h] += f.x;
-                        v[i + 2 * h + 1] += f.y;
-                    }
-                }
-            } else {  // from the warp's box (load_rows)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 t = *reinterpret_cast<const uint4*>(box_row + (((4 * half + i) ^ (threadIdx.x & 7)) << 4));
-                    const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const float2 f = x_unpack2<XT>(w[h]);
-                        v[8 * i + 2 * h] += f.x;
-                        v[8 * i + 2 * h + 1] += f.y;
-                    }
+                for (int h = 0; h < 4; ++h) {
+                    const float2 f = x_unpack2<XT>(w[h]);
+                    v[8 * i + 2 * h] += f.x;
+                    v[8 * i + 2 * h + 1] += f.y;
                 }
             }
         }
@@ -271,9 +255,26 @@ __device__ __forceinline__ void store_rows(const unsigned char* box, T* out, lon
     }
 }
 
-// The reverse, for 16-bit rows that no vector load can reach.
-__device__ __forceinline__ void load_rows(unsigned char* box, const uint16_t* in, long long ld, int rows, int cols, int lane)
+// The reverse: a box from 16-bit rows.  `vec`: rows of whole 16-byte vectors, eight lanes a
+// row, all loads in flight together (a lane's own row would take 32 sectors per load).
+__device__ __forceinline__ void load_rows(unsigned char* box, const uint16_t* in, long long ld, int rows, int cols, int lane,
+                                          bool vec)
 {
+    if (vec) {
+        const int c = lane & 7;
+        uint4 t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            t[i] = r < rows && 8 * c < cols ? *reinterpret_cast<const uint4*>(in + r * ld + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            *reinterpret_cast<uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4)) = t[i];
+        }
+        return;
+    }
 #pragma unroll 4
     for (int i = 0; i < rows; ++i) {
 #pragma unroll
@@ -493,6 +494,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         at[2] = e.bias && c < p.n ? __ldg(e.bias + c) : 0.f;
                     }
                 }
+                // a box of the residual: each half's values make room for that half's outputs
+                const int rows = p.m - r0 < 32 ? (int)(p.m - r0) : 32;
+                auto residual_box = [&](unsigned char* box, int c) {
+                    if (lane == 0) bulk_wait_read<boxes - 1>();
+                    __syncwarp();
+                    load_rows(box, static_cast<const uint16_t*>(e.residual) + r0 * e.ldr + n0 + c, e.ldr, rows,
+                              p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64, lane, vec);
+                    __syncwarp();
+                };
+                const bool residual = KIND == kGemmForward && e.residual && !cut;
+                if (residual && r0 < p.m && n0 + c0 < p.n) residual_box(S.box[(warp - 4) * boxes], c0);
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
                 // the columns are there; after a wait that gave up all warps stop together, or
                 // the others would wait at the next barrier
@@ -525,17 +537,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 for (int c = cut ? c0 + span : c0; c < c0 + span; c += 64) {
                     if (n0 + c >= p.n || r0 >= p.m) break;  // the same in every lane
                     unsigned char* box = S.box[(warp - 4) * boxes + ((c >> 6) & (boxes - 1))];
-                    auto box_free = [&] {  // its last store has been read
-                        if (lane == 0) bulk_wait_read<boxes - 1>();
-                        __syncwarp();
-                    };
-                    const int rows = p.m - r0 < 32 ? (int)(p.m - r0) : 32, cols = p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64;
-                    if (KIND == kGemmForward && e.residual && !vec) {
-                        // each half's values make room for that half's outputs
-                        box_free();
-                        load_rows(box, static_cast<const uint16_t*>(e.residual) + r0 * e.ldr + n0 + c, e.ldr, rows, cols, lane);
-                        __syncwarp();
-                    }
+                    const int cols = p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64;
+                    if (residual && c != c0) residual_box(box, c);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const long long ch = n0 + c + 32 * h;
@@ -543,9 +546,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c + 32 * h, v);
                         const int count = p.n - ch < 32 ? (int)(p.n - ch) : 32;
-                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, vec, row_scale,
+                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, row_scale,
                                                        S.cols + (c + 32 * h) / 2, box + lane * 128, h);
-                        if (h == 0 && !(KIND == kGemmForward && e.residual && !vec)) box_free();
+                        if (h == 0 && !residual) {  // the box's last store has been read
+                            if (lane == 0) bulk_wait_read<boxes - 1>();
+                            __syncwarp();
+                        }
                         box32<XT>(box + lane * 128, lane, h, v);
                         __syncwarp();
                     }

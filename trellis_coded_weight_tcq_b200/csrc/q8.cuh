@@ -225,6 +225,34 @@ __device__ __forceinline__ F2 f2_logistic2(F2 t)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Phi(-a) = erfc(a / sqrt 2) / 2 of two a >= 0, and e = exp(-a^2 / 2): Hastings' rational
+// approximation of erf (Abramowitz and Stegun 7.1.26, within 1.5e-7), in packed operations
+// (a product with 3211 x 12032 outputs through GELU: 143 us with erff, 79 with it).
+__device__ __forceinline__ F2 f2_tail(F2 a, F2& e)
+{
+    constexpr float p = 0.3275911f * 0.7071067811865476f;
+    constexpr float c1 = 0.5f * 0.254829592f, c2 = 0.5f * -0.284496736f, c3 = 0.5f * 1.421413741f,
+                    c4 = 0.5f * -1.453152027f, c5 = 0.5f * 1.061405429f;
+    float x, y;
+    f2_split(f2_fma(a, f2(p, p), f2(1.f, 1.f)), x, y);
+    const F2 t = f2(rcp(x), rcp(y));
+    f2_split(f2_mul(f2_mul(a, a), f2(-0.5f * kLog2e, -0.5f * kLog2e)), x, y);
+    e = f2(ex2(x), ex2(y));
+    F2 s = f2_fma(t, f2(c5, c5), f2(c4, c4));
+    s = f2_fma(t, s, f2(c3, c3));
+    s = f2_fma(t, s, f2(c2, c2));
+    s = f2_fma(t, s, f2(c1, c1));
+    return f2_mul(f2_mul(t, s), e);
+}
+
+// |z|, at most the largest finite number; NaN stays
+__device__ __forceinline__ float finite_magnitude_of(float z)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r) : "f"(fabsf(z)));
+    return r;
+}
+
 // z, or the lowest finite number where it is below (whose product with the logistic
 // function's 0 is 0); NaN stays
 __device__ __forceinline__ float finite_below(float z)
@@ -246,8 +274,10 @@ __device__ __forceinline__ F2 act_value2(F2 z)
         if constexpr (ACT == TCQ_ACT_RELU) {
             return f2(a > 0.f ? a : (a != a ? a : 0.f), b > 0.f ? b : (b != b ? b : 0.f));
         } else if constexpr (ACT == TCQ_ACT_GELU) {
-            auto gelu = [](float x) { return x == -INFINITY ? -0.f : 0.5f * x * (1.f + erff(x * 0.7071067811865476f)); };
-            return f2(gelu(a), gelu(b));
+            // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
+            F2 e;
+            const F2 m = f2(finite_magnitude_of(a), finite_magnitude_of(b));
+            return f2_fma(f2_mul(m, f2(-1.f, -1.f)), f2_tail(m, e), f2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
         } else {
             z = f2(finite_below(a), finite_below(b));
             if constexpr (ACT == TCQ_ACT_SILU) return f2_mul(z, f2_logistic2(f2_mul(z, f2(-kLog2e, -kLog2e))));
@@ -302,10 +332,11 @@ __device__ __forceinline__ F2 act_slope2(F2 z)
         if constexpr (ACT == TCQ_ACT_RELU) {
             return f2(a > 0.f ? 1.f : (a != a ? a : 0.f), b > 0.f ? 1.f : (b != b ? b : 0.f));
         } else {
-            auto gelu = [](float x) {
-                return 0.5f * (1.f + erff(x * 0.7071067811865476f)) + x * ex2(x * x * (-0.5f * kLog2e)) * 0.3989422804014327f;
-            };
-            return f2(gelu(a), gelu(b));
+            F2 e;
+            float u, v;
+            f2_split(f2_tail(f2(fabsf(a), fabsf(b)), e), u, v);
+            const F2 phi = f2(a > 0.f ? 1.f - u : u, b > 0.f ? 1.f - v : v);
+            return f2_fma(f2_mul(z, e), f2(0.3989422804014327f, 0.3989422804014327f), phi);
         }
     }
 }
