@@ -309,6 +309,24 @@ def test_cut_last_round(dtype, rows, cuda_device):
     _check(dw, 2 * want, 2 * bound + 2.0**-23 * 2 * want.abs(), "wgrad8 accumulate")
 
 
+@pytest.mark.parametrize("cols", [320, 448])
+def test_dgrad_narrow_last_tiles(cols, cuda_device):
+    """Tiles of one and of three column blocks, a single stage each and many per
+    multiprocessor: a store may still read its box when the next tile's outputs come."""
+    from tests import gemm_reference as ref
+
+    rng = np.random.default_rng(cols)
+    rows, n = 60, 60000
+    args, w = ref.random_matrix(rng, 12, 2, 64, rows, cols, "f16", False, cuda_device)
+    dz = _x(rng, n, rows, _dtype("f16"), cuda_device)
+    d = dz.double()
+    want = d @ w
+    bound = ref.product_bound(d, w.T.contiguous(), 0.0) + 1e-300
+    bound = bound + ref.half_step(dz.dtype) * (want.abs() + bound) + 2.0**-25
+    for _ in range(5):
+        _check(tcq.gemm_dgrad(*args, dz), want, bound, "dgrad")
+
+
 @pytest.mark.parametrize("rows,nb,n", [(2603, 8, 2600), (14336, 9, 2100)])
 def test_dgrad_cut_last_round(rows, nb, n, cuda_device):
     """The same for the input gradient; the longer one goes through its tiles in bands, the

@@ -19,7 +19,7 @@
 // steps.  That does not show in 16-bit outputs; the weight gradient, fp32 and summed over
 // all tokens, takes its sums out of tensor memory every 1280 tokens at most and adds them
 // in registers (root mean square error against float64 at 4096 tokens, relative to the
-// gradient's: 1.6e-6 without, 2.8e-7 with).
+// gradient's: 1.6e-6 without, 2.8e-7 with; 8e-7 for 1111 tokens, one such sum).
 //
 // Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP), alone and with the
 // second kernel: forward with GELU about 315 us, input gradient 311 us, weight gradient
@@ -413,6 +413,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         int done = 0;
+        unsigned turn = 0;  // of the warp's boxes: the next one's last store is then the oldest
         bool ok = true;
         for (int t = pair; t < items && ok; t += pairs) {
             const Item w = work_item(p, t);
@@ -504,7 +505,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     __syncwarp();
                 };
                 const bool residual = KIND == kGemmForward && e.residual && !cut;
-                if (residual && r0 < p.m && n0 + c0 < p.n) residual_box(S.box[(warp - 4) * boxes], c0);
+                if (residual && r0 < p.m && n0 + c0 < p.n) residual_box(S.box[(warp - 4) * boxes + (turn & (boxes - 1))], c0);
                 ok = __all_sync(0xffffffffu, mbar_wait(smem_addr(&S.tfull[acc]), (done >> 1) & 1, stop, err));
                 // the columns are there; after a wait that gave up all warps stop together, or
                 // the others would wait at the next barrier
@@ -516,7 +517,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll 1
                     for (int c = c0; c < c0 + span; c += 32) {
                         if (n0 + c >= p.n || r0 >= p.m) break;
-                        unsigned char* box = S.box[(warp - 4) * boxes + ((c >> 5) & (boxes - 1))];
+                        unsigned char* box = S.box[(warp - 4) * boxes + (turn++ & (boxes - 1))];
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c, v);
                         if (lane == 0) bulk_wait_read<boxes - 1>();
@@ -536,7 +537,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll 1
                 for (int c = cut ? c0 + span : c0; c < c0 + span; c += 64) {
                     if (n0 + c >= p.n || r0 >= p.m) break;  // the same in every lane
-                    unsigned char* box = S.box[(warp - 4) * boxes + ((c >> 6) & (boxes - 1))];
+                    unsigned char* box = S.box[(warp - 4) * boxes + (turn++ & (boxes - 1))];
                     const int cols = p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64;
                     if (residual && c != c0) residual_box(box, c);
 #pragma unroll
