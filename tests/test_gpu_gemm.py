@@ -225,6 +225,58 @@ def test_gemm_extreme_ranges(cuda_device):
     assert torch.isnan(y[0]).all() and not torch.isfinite(y[6]).any() and not torch.isfinite(y[7]).any()
 
 
+@pytest.mark.parametrize("n", [1, 24, 600])
+@pytest.mark.parametrize("code,L,T", [("f16", 16, 256), ("f32", 12, 64), ("mad", 16, 100)])
+def test_matrix_arrays_at_element_alignment(code, L, T, n, cuda_device):
+    """Arrays of the matrix and the bias that start one element past any larger alignment,
+    and activations of an odd stride, with many tokens, too."""
+    import torch
+    from tests import gemm_reference as ref
+
+    def shifted(t):
+        return None if t is None else torch.cat([t.reshape(-1)[:1], t.reshape(-1)])[1:].view(t.shape)
+
+    rng = np.random.default_rng(L + T + n)
+    rows, cols = 270, 10 * T
+    args, w = ref.random_matrix(rng, L, 2, T, rows, cols, code, True, cuda_device)
+    odd = (shifted(args[0]), shifted(args[1]), shifted(args[2]), args[3] if code == "mad" else shifted(args[3]), *args[4:])
+    bias = shifted(torch.from_numpy(rng.standard_normal(rows)).float().to(cuda_device))
+    x = _x(rng, n, cols, torch.bfloat16, cuda_device, pad=3)
+    res = _x(rng, n, rows, torch.bfloat16, cuda_device, pad=5)
+    check_gemm(odd, w, x, tcq.gemm(*odd, x, bias=bias, act="gelu", residual=res), "gelu", bias, res)
+    dz = _x(rng, n, rows, torch.bfloat16, cuda_device, pad=7)
+    assert torch.equal(tcq.gemm_dgrad(*odd, dz), tcq.gemm_dgrad(*args, dz))
+
+
+@pytest.mark.parametrize("n", [1, 5, 300])
+def test_activations_of_extreme_values(n, cuda_device):
+    """Pre-activations of any size, infinite and NaN (through the bias)."""
+    import torch
+    from tests import gemm_reference as ref
+
+    inf = float("inf")
+    rng = np.random.default_rng(4)
+    args, _ = ref.random_matrix(rng, 16, 2, 256, 64, 256, "f16", True, cuda_device)
+    big = torch.tensor([inf, -inf, float("nan"), 3e38, -3e38, 1e20, -1e20, 3e4, -3e4, 200.0, -200.0, 20.0, -20.0, 0.0, -0.0],
+                       device=cuda_device)
+    bias = torch.zeros(64, device=cuda_device)
+    bias[:15] = big
+    x = torch.zeros((n, 256), dtype=torch.bfloat16, device=cuda_device)
+    for act in ("none", "relu", "silu", "gelu", "gelu_tanh"):
+        z = big.double()
+        want = torch.where(z == -inf, torch.zeros_like(z), ref.act(z.clamp(-1e30, 1e30), act)) if act != "none" else z
+        want = torch.where(z == inf, z, want)
+        want = torch.where((z.abs() > 1e30) & torch.isfinite(z), z if act == "none" else z.clamp_min(0), want)
+        got = tcq.gemm(*args, x, bias=bias, act=act)[:, :15]
+        want = want.float().to(torch.bfloat16)
+        assert torch.isnan(got[:, 2]).all()
+        keep = [i for i in range(15) if i != 2]
+        # a step of bfloat16, and what a vanishing slope leaves of an fp32 exponential
+        err = (got[:, keep].double() - want[keep].double()).abs()
+        err = torch.where(got[:, keep] == want[keep], torch.zeros_like(err), err)
+        assert (err <= 2.0**-7 * want[keep].double().abs() + 2.0**-20).all(), (act, got[0], want)
+
+
 def test_gemm_zero_and_one(cuda_device):
     import torch
     from tests import gemm_reference as ref

@@ -183,6 +183,40 @@ def test_given_stream_owns_what_a_call_allocates(cuda_device):
     assert torch.equal(got, want) and bool((other == 255).all())
 
 
+def test_calls_side_by_side(cuda_device):
+    """Blocks of different sizes on four streams at once, each several times, and a captured
+    one replayed among them, give the bits of the same calls alone."""
+    import torch
+
+    sizes = (1, 40, 300, 2000)
+    blocks = [_block(np.random.default_rng(60 + n), cuda_device, n, torch.bfloat16) for n in sizes]
+
+    def step(up, down, x, g):
+        h = up.forward(x)
+        y = down.forward(h, residual=x)
+        dx = up.backward(down.backward(g))
+        return y, dx, up.dw, up.db, down.dw, down.db
+
+    want = [[t.clone() for t in step(*b)] for b in blocks]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(*blocks[2])
+    streams = [torch.cuda.Stream() for _ in sizes]
+    got = [[] for _ in sizes]
+    for _ in range(6):
+        for i, (s, b) in enumerate(zip(streams, blocks)):
+            with torch.cuda.stream(s):
+                got[i].append(step(*b))
+        graph.replay()
+    torch.cuda.synchronize()
+    for runs, expected in zip(got, want):
+        for run in runs:
+            assert all(torch.equal(a, b) for a, b in zip(run, expected))
+    assert all(torch.equal(a, b) for a, b in zip(captured, want[2]))
+    del graph
+
+
 @pytest.mark.parametrize("n", [1, 40, 700])
 def test_capture_and_replay(n, cuda_device):
     """The block's forward and backward captured once and replayed on new inputs gives
