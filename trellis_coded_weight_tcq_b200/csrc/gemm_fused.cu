@@ -495,9 +495,9 @@ cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtenso
 
 // T a multiple of 64 keeps a stage inside one block and its words together.  More than
 // 256 tokens would decode the matrix again, and the product that decodes ahead wins.
-// Measured, here / decoded ahead, in us: 14336 x 4096 (binary16 table) 32 tokens 52 / 72,
-// 256 tokens 77 / 74, 257 tokens 112 / 90; 4096 x 14336 257 tokens 107 / 86; 4096 x 4096
-// 32 tokens 24 / 29, 257 tokens 41 / 37.
+// Measured, here / decoded ahead, in us (binary16 table): 14336 x 4096 32 tokens 52 / 71,
+// 192 68 / 73, 256 76 / 73, 257 112 / 90; 4096 x 14336 32 tokens 52 / 72, 256 70 / 77; 4096 x
+// 4096 32 tokens 24 / 28, 256 32 / 31; 512 x 512 32 tokens 12 / 13, 256 16 / 13.
 bool fused_shape(int T, long long rows, long long cols, long long n)
 {
     return T % kDepth == 0 && n <= 256 && (rows / kRows + 1) * (cols / 128 + 1) < (1ll << 30);
