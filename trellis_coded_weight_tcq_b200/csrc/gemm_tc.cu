@@ -244,13 +244,19 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
 template <typename T>
 __device__ __forceinline__ void store_rows(const unsigned char* box, T* out, long long ldo, int rows, int cols, int lane)
 {
-    constexpr int per = 128 / sizeof(T);  // columns of a box
-    for (int i = 0; i < rows; ++i) {
+    constexpr int per = 128 / sizeof(T), ahead = 8 * 32 / per;  // columns of a box, rows read together
+#pragma unroll 1
+    for (int i0 = 0; i0 < rows; i0 += ahead) {
+        T v[8];
 #pragma unroll
-        for (int h = 0; h < per; h += 32) {
-            const int c = lane + h, byte = c * (int)sizeof(T);
-            const T v = *reinterpret_cast<const T*>(box + i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15)));
-            if (c < cols) out[i * ldo + c] = v;
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * 32 / per, byte = (lane + j * 32 % per) * (int)sizeof(T);
+            v[j] = *reinterpret_cast<const T*>(box + i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15)));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = i0 + j * 32 / per, c = lane + j * 32 % per;
+            if (i < rows && c < cols) out[i * ldo + c] = v[j];
         }
     }
 }
