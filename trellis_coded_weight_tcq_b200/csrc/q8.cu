@@ -7,7 +7,8 @@
 // the slopes' transcendentals take most of the issue slots beside the loads).
 // Rows of a multiple of 8 elements (16 to pack) with 16-byte aligned 16-bit rows move whole
 // 16-byte vectors; other shapes take one element per lane, a warp per group, which needs
-// no alignment at all.  Rows that follow one another without gaps and hold whole groups
+// no alignment at all (unpacking reads such codes by the byte where its rows out are
+// aligned).  Rows that follow one another without gaps and hold whole groups
 // are one long row.
 #include "gemm.cuh"
 #include "pdl.cuh"
