@@ -381,15 +381,16 @@ tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 forma
  * More than 256 tokens of bfloat16 multiply in bfloat16, a weight being its codeword
  * times its block's scale rounded once.  All others multiply in binary16: a weight is
  * rounded once to binary16 (exact without scales for a binary16 table and the computed
- * code), relative to a power of two per row of W; a bfloat16 row of X is scaled to
+ * code), relative to a power of two per row of W and one of the table, so that neither
+ * scales nor entries need to lie near 1: with M the row's largest |scale| times the
+ * table's largest finite entry, weights keep binary16's 11 bits down to 2^-27 M (the
+ * computed code's to 2^-14 M) and are within 2^-38 M (2^-25 M) below.  A bfloat16 row of X is scaled to
  * binary16 by a power of two of its own, exactly for elements above 2^-32 of the row's
  * largest and within 2^-39 of that largest for the others.  A single token (n == 1, no checkpoint
  * of Z) takes tcq_gemv's kernels, with both operands in fp32.
  *
  *   bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols  as tcq_gemv
- *               (T % 4 == 0, cols % T == 0, a binary16 table when L >= 15; the
- *               entries of a table are at most 65504 in magnitude, and in the binary16
- *               products those below 2^-14 keep only multiples of 2^-24).
+ *               (T % 4 == 0, cols % T == 0, a binary16 table when L >= 15).
  *   x           [n, cols] of xdtype, row stride ldx.
  *   bias        fp32 [rows] or NULL.
  *   residual    [n, rows] of xdtype, row stride ldr, or NULL.

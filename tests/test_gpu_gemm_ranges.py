@@ -1,0 +1,95 @@
+"""Batched products with a trellis-coded matrix whose parts lie far from 1: tables of tiny
+and of huge entries, activations, scales and entries of opposite powers.
+
+Tolerances: tests/gemm_reference.py (product_bound), then half a step of the output's
+type.  Powers of two change no rounding, so the bounds are those of matrices near 1."""
+import numpy as np
+import pytest
+
+from trellis_coded_weight_tcq_b200 import tcq
+
+pytestmark = pytest.mark.gpu
+
+
+def _coded(rng, L, k, T, rows, cols, table, scale, device):
+    """(arguments of tcq.gemm up to cols, W in float64) for a given numpy table and
+    per-block scales (or None)."""
+    import torch
+    from oracle import oracle_decode
+
+    nb = rows * (cols // T)
+    W = tcq.tcq_words_per_block(k, T)
+    bits = rng.integers(0, 2**32, size=(nb, W), dtype=np.uint64).astype(np.uint32)
+    used = T * k - 32 * (W - 1)
+    if used < 32:
+        bits[:, -1] &= np.uint32(((1 << used) - 1) << (32 - used))
+    start = rng.integers(0, 2**32, size=nb, dtype=np.uint64).astype(np.uint32)
+    values = oracle_decode(bits, start, table, L, k, T).reshape(rows, cols)
+    if scale is not None:
+        values = values * np.repeat(scale.astype(np.float64).reshape(rows, -1), T, axis=1)
+        scale = torch.from_numpy(scale).to(device)
+    return (torch.from_numpy(bits.view(np.int32)).to(device), torch.from_numpy(start.view(np.int32)).to(device), scale,
+            torch.from_numpy(table).to(device), L, k, T, rows, cols), torch.from_numpy(values).to(device)
+
+
+def _table(rng, L, code, power):
+    """Normal entries of standard deviation 2^power."""
+    return (rng.standard_normal(1 << L) * 2.0**power).astype(np.float16 if code == "f16" else np.float32)
+
+
+def _check_dgrad(args, w, dz, what):
+    import torch
+    from tests import gemm_reference as ref
+    from tests.test_gpu_gemm import _check
+
+    dx = tcq.gemm_dgrad(*args, dz)
+    d = dz.double()
+    want = d @ w
+    half = ref.weight_half_step(dz.shape[0], dz.dtype, args[2] is None and args[3].dtype == torch.float16)
+    bound = ref.product_bound(d, w.T.contiguous(), half) + 1e-300
+    bound = bound + 2.0**-24 * (d.abs() @ w.abs().amax(1, keepdim=True))
+    _check(dx, want, bound + ref.half_step(dz.dtype) * (want.abs() + bound) +
+           (2.0**-25 if dz.dtype == torch.float16 else 0), what)
+
+
+@pytest.mark.parametrize("n", [1, 24, 600])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [64, 100])  # decoded inside the product, and ahead of it
+@pytest.mark.parametrize("code,power,scaled,xpower", [
+    ("f32", -24, True, 0), ("f32", -24, False, 8), ("f32", 20, True, 0), ("f32", 20, False, -13),
+    ("f16", -18, True, 0), ("f16", 13, True, 0), ("f16", 13, False, -8), ("f16", -18, False, 6)])
+def test_tables_far_from_one(code, power, scaled, xpower, T, dtype, n, cuda_device):
+    """Entries of about 6e-8 and 1e6 (binary32), of 4e-6 (steps of binary16's subnormals) and
+    of 8192 (binary16), with scales that bring the weights to about 0.02, and without."""
+    import torch
+    from tests.test_gpu_gemm import check_gemm
+
+    rng = np.random.default_rng(n + T + power + 100)
+    rows, cols, L = 130, 6 * T, 16 if code == "f16" else 12
+    scale = (rng.lognormal(-4.0, 0.5, rows * 6) * 2.0**-power).astype(np.float32) if scaled else None
+    args, w = _coded(rng, L, 2, T, rows, cols, _table(rng, L, code, power), scale, cuda_device)
+    dt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    x = torch.from_numpy(rng.standard_normal((n, cols)) * 2.0**xpower).to(cuda_device).to(dt)
+    check_gemm(args, w, x, tcq.gemm(*args, x))
+    dz = torch.from_numpy(rng.standard_normal((n, rows)) * 2.0**xpower).to(cuda_device).to(dt)
+    _check_dgrad(args, w, dz, "dgrad")
+
+
+@pytest.mark.parametrize("n", [1, 24, 600])
+@pytest.mark.parametrize("T", [64, 100])
+@pytest.mark.parametrize("xpower,spower,tpower", [(120, -118, 0), (-122, 110, 0), (60, 90, -100), (-60, -90, 100),
+                                                  (110, 0, -100), (-110, 0, 100)])
+def test_opposite_powers(xpower, spower, tpower, T, n, cuda_device):
+    """Activations, scales and table entries whose powers nearly cancel, while two of the
+    three together pass the ends of fp32's range."""
+    import torch
+    from tests.test_gpu_gemm import check_gemm
+
+    rng = np.random.default_rng(n + T + xpower + 200)
+    rows, cols, L = 130, 5 * T, 12
+    scale = (rng.lognormal(0.0, 0.5, rows * 5) * 2.0**spower).astype(np.float32) if spower else None
+    args, w = _coded(rng, L, 2, T, rows, cols, _table(rng, L, "f32", tpower), scale, cuda_device)
+    x = torch.from_numpy(rng.standard_normal((n, cols)) * 2.0**xpower).to(cuda_device).to(torch.bfloat16)
+    check_gemm(args, w, x, tcq.gemm(*args, x))
+    dz = torch.from_numpy(rng.standard_normal((n, rows)) * 2.0**xpower).to(cuda_device).to(torch.bfloat16)
+    _check_dgrad(args, w, dz, "dgrad")

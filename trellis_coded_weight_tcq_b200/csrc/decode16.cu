@@ -3,10 +3,11 @@
 //
 // A weight is scale * c[s], rounded once to binary16.  So that small scales do not
 // fall into binary16's subnormals, every row is divided by a power of two, the
-// least above its largest finite |scale|: the scales that multiply the codewords
-// are then below 1 and a product never overflows where the codeword does not.  The
-// products multiply the power back in (exactly).  Without scales a binary16 or
-// computed codeword is stored as it is.  For large bfloat16 batches the weights are
+// least above its largest finite |scale|, and tables by one of their own, so that
+// their largest entry ends in [2^14, 2^15): a weight is then below 2^15, and what a
+// row's largest weight is to its others, not how large they are, decides what they
+// lose.  The products multiply the powers back in (exactly).  Without scales a
+// binary16 or computed codeword is stored as it is.  For large bfloat16 batches the weights are
 // rounded once to bfloat16 instead, as they are: its range needs no powers.
 //
 // A warp takes 256 columns of a row at a time, eight per lane: their windows lie in
@@ -27,17 +28,29 @@ constexpr int kThreads = 768;  // leaves registers for the pass over the activat
 constexpr int kUnit = 256;  // columns per warp step
 constexpr int kAhead = 4;   // steps whose words are loaded together
 
+// The table's power in a decoding kernel, whose table is staged (the caller has synchronised).
+template <int CODE, bool BF16>
+__device__ __forceinline__ float power_of_table(const WeightPowers& powers, const unsigned char* sm, int L)
+{
+    if constexpr (BF16 || CODE == kCode16Mad) return 1.f;
+    if constexpr (CODE == kCode16F32) {
+        __shared__ uint32_t warps[kThreads / 32];
+        return powers.staged ? staged_table_power(reinterpret_cast<const float*>(sm), 1 << L, warps, powers.table_out) : 1.f;
+    }
+    return table_power(powers.table);
+}
+
 // Blocks of whole 32s: a row's stream words follow one another without gaps, so a lane's
 // words lie 8 k apart from unit to unit and its window offset never changes.  The next
 // four units' words load while the current four are decoded.
 template <int K, int CODE, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix w, uint16_t* out, long long ldw,
-                                                                    const float* row_pow2)
+                                                                    WeightPowers powers)
 {
     extern __shared__ __align__(16) unsigned char sm[];
     stage_table<CODE>(sm, w.cb, w.cb_f16, w.L);
-    pdl_wait();     // row_pow2
-    pdl_release();  // the pass over the activations may run beside this one (and read row_pow2)
+    pdl_wait();     // the powers
+    pdl_release();  // the pass over the activations may run beside this one (and read the powers)
     const int lane = threadIdx.x & 31;
     const int cols = (int)w.cols, T = w.T, nb = cols / T;
     const int upr = (cols + kUnit - 1) / kUnit;
@@ -53,6 +66,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix 
     const int word = ((8 * lane + 8) * K - 1) >> 5;  // the last window's word in a unit
     const int down = bits_behind((8 * lane + 8) * K);
     __syncthreads();
+    const float table = power_of_table<CODE, BF16>(powers, sm, w.L);
     struct Four {
         uint32_t hi[kAhead], lo[kAhead];
         float sc[kAhead];
@@ -88,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix 
             ++row;
         }
         if (left > 0) fetch(nxt, row, at);
-        const float inv = !BF16 && w.scale ? inverse_pow2(__ldcg(row_pow2 + r)) : 1.f;
+        const float inv = BF16 ? 1.f : inverse_pow2(power_product(powers.row ? __ldcg(powers.row + r) : 1.f, table));
         uint16_t* dst = out + r * ldw + a * kUnit + 8 * lane;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -106,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_rows_kernel(CodedMatrix 
 // Any block of whole quads; N = 8: whole eights, 4: two reads per lane.
 template <int K, int CODE, int N, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, uint16_t* out, long long ldw,
-                                                               const float* row_pow2)
+                                                               WeightPowers powers)
 {
     constexpr int H = 8 / N;  // reads per lane and unit
     extern __shared__ __align__(16) unsigned char sm[];
@@ -114,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
     pdl_wait();
     pdl_release();
     __syncthreads();
+    const float table = power_of_table<CODE, BF16>(powers, sm, w.L);
     const int lane = threadIdx.x & 31;
     const int cols = (int)w.cols, T = w.T, W = w.W, nb = cols / T;
     const int upr = (cols + kUnit - 1) / kUnit;
@@ -125,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
     long long row = u0 / upr;
     int at = (int)(u0 - row * upr);
     for (long long u = u0; u < u1; ++u) {
-        const float inv = !BF16 && w.scale ? inverse_pow2(__ldcg(row_pow2 + row)) : 1.f;
+        const float inv = BF16 ? 1.f : inverse_pow2(power_product(powers.row ? __ldcg(powers.row + row) : 1.f, table));
         const int c = at * kUnit + 8 * lane;
         uint32_t v[4];
 #pragma unroll
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
                     const uint32_t* p = w.bits + b * W + ((end - 1) >> 5);
                     lo = __ldg(p);
                     hi = __ldg(end > 32 ? p - 1 : w.start_state + b);
-                    sc = w.scale ? __ldg(w.scale + b) * inv : 1.f;
+                    sc = w.scale ? __ldg(w.scale + b) * inv : inv;
                 }
             }
             decode_weights<K, N, CODE, BF16>(hi, lo, down, mask, sm, sc, v + N / 2 * h);
@@ -158,10 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode16_kernel(CodedMatrix w, ui
 }
 
 template <int K, int CODE, bool BF16>
-cudaError_t launch(const CodedMatrix& w, void* out, long long ldw, const float* row_pow2, int num_sms,
+cudaError_t launch(const CodedMatrix& w, void* out, long long ldw, const WeightPowers& powers, int num_sms,
                    cudaStream_t stream)
 {
-    typedef void (*Kernel)(CodedMatrix, uint16_t*, long long, const float*);
+    typedef void (*Kernel)(CodedMatrix, uint16_t*, long long, WeightPowers);
     const Kernel kernel = w.T % 32 == 0  ? Kernel(decode16_rows_kernel<K, CODE, BF16>)
                           : w.T % 8 == 0 ? Kernel(decode16_kernel<K, CODE, 8, BF16>)
                                          : Kernel(decode16_kernel<K, CODE, 4, BF16>);
@@ -171,44 +186,51 @@ cudaError_t launch(const CodedMatrix& w, void* out, long long ldw, const float* 
     const long long units = (w.cols + kUnit - 1) / kUnit * w.rows;
     const long long need = (units + kThreads / 32 - 1) / (kThreads / 32);
     const int grid = (int)(need < num_sms ? need : num_sms);
-    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, !BF16 && w.scale, w,
-                      static_cast<uint16_t*>(out), ldw, row_pow2);
+    return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, stream, powers.row || powers.table, w,
+                      static_cast<uint16_t*>(out), ldw, powers);
 }
 
 template <int CODE, bool BF16>
-cudaError_t launch_k(const CodedMatrix& w, void* out, long long ldw, const float* row_pow2, int num_sms,
+cudaError_t launch_k(const CodedMatrix& w, void* out, long long ldw, const WeightPowers& powers, int num_sms,
                      cudaStream_t stream)
 {
     switch (w.K) {
-    case 1: return launch<1, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
-    case 2: return launch<2, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
-    case 3: return launch<3, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
-    default: return launch<4, CODE, BF16>(w, out, ldw, row_pow2, num_sms, stream);
+    case 1: return launch<1, CODE, BF16>(w, out, ldw, powers, num_sms, stream);
+    case 2: return launch<2, CODE, BF16>(w, out, ldw, powers, num_sms, stream);
+    case 3: return launch<3, CODE, BF16>(w, out, ldw, powers, num_sms, stream);
+    default: return launch<4, CODE, BF16>(w, out, ldw, powers, num_sms, stream);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, uint8_t* row_exponents,
-                            int num_sms, cudaStream_t stream)
+                            uint32_t* table_top, int num_sms, cudaStream_t stream)
 {
-    if (w.scale) {
-        const cudaError_t e = launch_prepare({}, {w.scale, w.rows, (int)(w.cols / w.T), row_pow2, row_exponents}, stream);
+    // the pass over the activations, which uses the exponents, may run beside this launch
+    const bool ahead = table_top && (w.cb_f16 || (w.scale && row_exponents));
+    WeightPowers powers;
+    if (w.scale) powers.row = row_pow2;
+    powers.staged = table_top && !w.cb_f16;
+    if (powers.staged && !ahead) powers.table_out = table_top;
+    if (!powers.staged) powers.table = table_top;
+    if (w.scale || ahead) {
+        const cudaError_t e = launch_prepare({}, powers_of(w, row_pow2, row_exponents, ahead ? table_top : nullptr), stream);
         if (e != cudaSuccess) return e;
     }
     switch (w.cb_f16) {
-    case kMadCodebook: return launch_k<kCode16Mad, false>(w, out, ldw, row_pow2, num_sms, stream);
-    case 1: return launch_k<kCode16F16, false>(w, out, ldw, row_pow2, num_sms, stream);
-    default: return launch_k<kCode16F32, false>(w, out, ldw, row_pow2, num_sms, stream);
+    case kMadCodebook: return launch_k<kCode16Mad, false>(w, out, ldw, powers, num_sms, stream);
+    case 1: return launch_k<kCode16F16, false>(w, out, ldw, powers, num_sms, stream);
+    default: return launch_k<kCode16F32, false>(w, out, ldw, powers, num_sms, stream);
     }
 }
 
 cudaError_t launch_decode_bf16(const CodedMatrix& w, void* out, long long ldw, int num_sms, cudaStream_t stream)
 {
     switch (w.cb_f16) {
-    case kMadCodebook: return launch_k<kCode16Mad, true>(w, out, ldw, nullptr, num_sms, stream);
-    case 1: return launch_k<kCode16F16, true>(w, out, ldw, nullptr, num_sms, stream);
-    default: return launch_k<kCode16F32, true>(w, out, ldw, nullptr, num_sms, stream);
+    case kMadCodebook: return launch_k<kCode16Mad, true>(w, out, ldw, {}, num_sms, stream);
+    case 1: return launch_k<kCode16F16, true>(w, out, ldw, {}, num_sms, stream);
+    default: return launch_k<kCode16F32, true>(w, out, ldw, {}, num_sms, stream);
     }
 }
 

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 
 #include "codes.cuh"
+#include "powers.cuh"
 
 namespace tcq {
 
@@ -124,30 +125,5 @@ __device__ __forceinline__ void decode_64(const uint32_t (&words)[2 * K], uint32
         }
     }
 }
-
-// Bits of |v|, or 0 for an infinity or NaN (magnitudes then compare as integers).
-__device__ __forceinline__ uint32_t finite_magnitude(float v)
-{
-    const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
-    return u < 0x7f800000u ? u : 0u;
-}
-
-// The least p with |v| < 2^p, from the bits of |v| (0 for v = 0, -126 for subnormals).
-__device__ __forceinline__ int power_above(uint32_t magnitude)
-{
-    if (magnitude == 0u) return 0;
-    const int p = (int)(magnitude >> 23) - 126;
-    return p;
-}
-
-// 2^e with e held to -126 .. 126, so that its inverse is a normal number too.
-__device__ __forceinline__ float pow2_clamped(int e)
-{
-    e = e < -126 ? -126 : e > 126 ? 126 : e;
-    return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
-// The inverse of such a power.
-__device__ __forceinline__ float inverse_pow2(float p) { return __uint_as_float(0x7f000000u - __float_as_uint(p)); }
 
 }  // namespace tcq

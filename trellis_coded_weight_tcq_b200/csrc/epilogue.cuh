@@ -3,6 +3,7 @@
 #pragma once
 
 #include "gemm.cuh"
+#include "powers.cuh"
 #include "q8.cuh"
 
 namespace tcq {
@@ -17,11 +18,19 @@ __device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long
 {
     const int lane = threadIdx.x & 31;
     const int count = rows - r < 4 ? (rows - r > 0 ? (int)(rows - r) : 0) : 4;
-    const float rs = e.row_scale ? __ldcg(e.row_scale + t) : 1.f;
+    const int row_exponent = e.row_scale ? exponent_of(__ldcg(e.row_scale + t)) : 0;
+    const TableParts parts(e.table_top);
+    float column[4], bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[i] *= rs;
-        if (i < count) v[i] = fmaf(v[i], e.col_scale ? __ldcg(e.col_scale + r + i) : 1.f, e.bias ? __ldg(e.bias + r + i) : 0.f);
+        column[i] = i < count && e.col_scale ? __ldcg(e.col_scale + r + i) : 1.f;
+        bias[i] = i < count && e.bias ? __ldg(e.bias + r + i) : 0.f;
+    }
+    const float table = parts.power();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 p = power_halves(row_exponent + exponent_of(power_product(column[i], table)));
+        v[i] = fmaf(v[i] * p.x, p.y, bias[i]);
     }
     if (e.z_codes) {  // a group of 32 is eight lanes
         uint32_t top = 0u;

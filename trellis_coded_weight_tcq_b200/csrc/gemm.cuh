@@ -21,6 +21,7 @@ struct CodedMatrix {
 struct Epilogue {
     const float* row_scale;  // power of two per output row, or nullptr
     const float* col_scale;  // power of two per output column, or nullptr
+    const uint32_t* table_top;  // the table's power (table_power), in all outputs, or nullptr
     const float* bias;       // per output column, or nullptr
     const void* residual;    // output type, or nullptr
     long long ldr;
@@ -64,17 +65,29 @@ size_t gemm_partial_bytes(long long m, long long n, long long k, int num_sms);
 cudaError_t launch_gemm_tc(GemmKind kind, const GemmProblem& p, const Epilogue& e, float* partial, int num_sms,
                            unsigned int* err, cudaStream_t stream);
 
+// The powers that a weight is stored over; nullptr: 1.
+struct WeightPowers {
+    const float* row = nullptr;       // per row
+    const uint32_t* table = nullptr;  // of a binary16 table (table_power)
+    // of a binary32 table, small enough that every CTA finds it from its own copy: `staged`,
+    // and where to leave it for the epilogue, or nullptr
+    bool staged = false;
+    uint32_t* table_out = nullptr;
+};
+
 // W as binary16 [rows, ldw], each weight over its row's power of two (row_pow2[r] and its
-// exponent field row_exponents[r], or nullptr; written when the matrix has scales).
+// exponent field row_exponents[r], or nullptr; written when the matrix has scales) and
+// over the table's (table_top, written unless it is nullptr: with row_exponents before this
+// launch, else by it or before it).
 cudaError_t launch_decode16(const CodedMatrix& w, void* out, long long ldw, float* row_pow2, uint8_t* row_exponents,
-                            int num_sms, cudaStream_t stream);
+                            uint32_t* table_top, int num_sms, cudaStream_t stream);
 
 // W as bfloat16, each weight scale * codeword rounded once.
 cudaError_t launch_decode_bf16(const CodedMatrix& w, void* out, long long ldw, int num_sms, cudaStream_t stream);
 
 // x [n, cols] as binary16 rows over a power of two each (row_pow2[n]).  col_exponents (or
 // nullptr, 8-byte aligned): fp32 exponent fields of powers of two that multiply the
-// columns first.  `early`: the launch before it in the stream is one of this call's
+// columns first, each with the power of table_top (or nullptr).  `early`: the launch before it in the stream is one of this call's
 // (launch_decode16), which it may run beside; the exponents may then be those of the row
 // powers that launch_decode16 read.
 struct ScaleRows {
@@ -82,6 +95,7 @@ struct ScaleRows {
     int xdtype = TCQ_X_F16;
     long long ldx = 0, n = 0, cols = 0;
     const uint8_t* col_exponents = nullptr;
+    const uint32_t* table_top = nullptr;
     void* out = nullptr;
     long long ldo = 0;
     float* row_pow2 = nullptr;
@@ -90,16 +104,38 @@ struct ScaleRows {
 };
 
 // out[r] for the rows of a coded matrix, per_row scales each: the least power of two
-// above the largest finite |scale|, and its exponent field (or nullptr).
+// above the largest finite |scale|, and its exponent field (or nullptr).  table_top
+// [kTableParts], unless nullptr: the largest finite magnitudes of the table's parts.
 struct RowPowers {
     const float* scale = nullptr;
     long long rows = 0;
     int per_row = 0;
     float* out = nullptr;
     uint8_t* exponents = nullptr;
+    const void* table = nullptr;
+    int table_f16 = 0, table_log2 = 0;
+    uint32_t* table_top = nullptr;
 };
 
-// Either or both (n == 0 or rows == 0: not wanted), in one launch.
+// What to ask for the powers of a matrix, those of its rows where it has scales.
+inline RowPowers powers_of(const CodedMatrix& w, float* row_pow2, uint8_t* row_exponents, uint32_t* table_top)
+{
+    RowPowers p;
+    if (w.scale) {
+        p.scale = w.scale;
+        p.rows = w.rows;
+        p.per_row = (int)(w.cols / w.T);
+        p.out = row_pow2;
+        p.exponents = row_exponents;
+    }
+    p.table = w.cb;
+    p.table_f16 = w.cb_f16;
+    p.table_log2 = w.L;
+    p.table_top = table_top;
+    return p;
+}
+
+// Any of them (n == 0, rows == 0, no table_top: not wanted), in one launch.
 cudaError_t launch_prepare(ScaleRows a, RowPowers p, cudaStream_t stream);
 
 // 16-bit rows copied to another stride, beside the launch before it in the stream (one of
@@ -113,7 +149,7 @@ cudaError_t launch_copy16(const void* x, long long ldx, long long n, long long c
 bool fused_shape(int T, long long rows, long long cols, long long n);
 size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, long long n, int num_sms);
 cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx, long long n, int xdtype,
-                              const float* row_pow2, float* partial, const Epilogue& e, int num_sms, unsigned int* err,
+                              const WeightPowers& powers, float* partial, const Epilogue& e, int num_sms, unsigned int* err,
                               bool early, cudaStream_t stream);
 
 cudaError_t launch_pack8(const void* x, int xdtype, long long ldx, long long n, long long cols, int format,

@@ -74,10 +74,15 @@ CodedMatrix matrix(const uint32_t* bits, const uint32_t* start, const float* sca
 // Small ones keep 11 bits: there the pass is a few microseconds.
 bool bf16_operands(tcq_xdtype xdtype, int64_t n) { return xdtype == TCQ_X_BF16 && n > 256; }
 
-// Workspace of a product: the binary16 matrix, its row powers, the binary16
-// activations (rows of `inner` elements) and theirs.
+// Whether weights are stored over a power of two of their table (powers.cuh): a binary32
+// table's entries may be of any size; binary16 ones without scales are stored exactly as
+// they are, and the computed code's lie near 1.
+bool table_power_wanted(tcq_dtype dt, const float* scale) { return dt == TCQ_F32 || (dt == TCQ_F16 && scale); }
+
+// Workspace of a product: the binary16 matrix, its row powers and its table's, the
+// binary16 activations (rows of `inner` elements) and theirs.
 struct GemmSpace {
-    size_t row_pow2, row_exponents, x, x_pow2, partial, total;
+    size_t row_pow2, row_exponents, table_top, x, x_pow2, partial, total;
 };
 
 // `weights`: bytes of the binary16 matrix; `partial`: of the sums of a reduction's pieces
@@ -86,7 +91,8 @@ GemmSpace gemm_space(size_t weights, int64_t rows, int64_t n, int64_t inner, siz
     GemmSpace s;
     s.row_pow2 = align256(weights);
     s.row_exponents = s.row_pow2 + align256((size_t)rows * 4);
-    s.x = s.row_exponents + align256((size_t)rows);
+    s.table_top = s.row_exponents + align256((size_t)rows);
+    s.x = s.table_top + 256;
     s.x_pow2 = s.x + align256((size_t)n * round_up(inner, 8) * 2);
     s.partial = s.x_pow2 + align256((size_t)n * 4);
     s.total = s.partial + align256(partial);
@@ -182,6 +188,7 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     float* row_pow2 = reinterpret_cast<float*>(ws + sp.row_pow2);
     float* x_pow2 = reinterpret_cast<float*>(ws + sp.x_pow2);
     float* partial = reinterpret_cast<float*>(ws + sp.partial);
+    uint32_t* table_top = table_power_wanted(cb_dtype, scale) ? reinterpret_cast<uint32_t*>(ws + sp.table_top) : nullptr;
     const int64_t ldw = round_up(cols, 8);
 
     const bool fused = fused_shape(T, rows, cols, n);
@@ -214,17 +221,18 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
         }
         ep.row_scale = nullptr;
         scale = nullptr;  // in the weights
+        table_top = nullptr;
     } else if (fused) {
-        RowPowers rp;
-        if (scale) rp = {scale, rows, (int)(cols / T), row_pow2, nullptr};
-        if (scaled || scale) e = launch_prepare(sx, rp, st);
+        // a binary32 table's power is found by the product
+        if (scaled || scale) e = launch_prepare(sx, powers_of(w, row_pow2, nullptr, w.cb_f16 ? table_top : nullptr), st);
     } else {
-        e = launch_decode16(w, ws, ldw, row_pow2, nullptr, num_sms, st);
+        e = launch_decode16(w, ws, ldw, row_pow2, nullptr, table_top, num_sms, st);
         sx.early = true;
         if (e == cudaSuccess && scaled) e = launch_prepare(sx, {}, st);
     }
     if (e != cudaSuccess) return TCQ_ERR_CUDA;
     ep.col_scale = scale ? row_pow2 : nullptr;
+    ep.table_top = table_top;
     ep.bias = bias;
     ep.residual = residual;
     ep.ldr = ldr;
@@ -232,9 +240,16 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
     ep.z_codes = z_codes;
     ep.z_scales = z_scales;
     ep.z_format = z_format;
-    if (fused)
-        return status(launch_gemm_fused(w, p.a, p.lda, n, xdtype, row_pow2, partial, ep, num_sms, err,
-                                        scaled || scale, st));
+    if (fused) {
+        WeightPowers powers;
+        powers.row = ep.col_scale;
+        powers.staged = table_top && !w.cb_f16;
+        if (powers.staged)
+            powers.table_out = table_top;
+        else
+            powers.table = table_top;
+        return status(launch_gemm_fused(w, p.a, p.lda, n, xdtype, powers, partial, ep, num_sms, err, scaled || scale, st));
+    }
     return status(launch_gemm_tc(kGemmForward, p, ep, partial, num_sms, err, st));
 }
 
@@ -274,6 +289,7 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
     const int64_t ldw = round_up(cols, 8);
 
     uint8_t* row_exponents = ws + sp.row_exponents;
+    uint32_t* table_top = table_power_wanted(cb_dtype, scale) ? reinterpret_cast<uint32_t*>(ws + sp.table_top) : nullptr;
     GemmProblem p = {dz, lddz, ws, ldw, n, cols, rows, 0, xdtype};
     Epilogue ep = plain_epilogue(dx, lddx);
     if (bf16_operands(xdtype, n)) {
@@ -287,9 +303,11 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
         p.fmt = 1;
         return status(launch_gemm_tc(kGemmDgrad, p, ep, partial, num_sms, err, st));
     }
-    cudaError_t e = launch_decode16(w, ws, ldw, row_pow2, row_exponents, num_sms, st);
+    cudaError_t e = launch_decode16(w, ws, ldw, row_pow2, row_exponents, table_top, num_sms, st);
     if (e != cudaSuccess) return TCQ_ERR_CUDA;
-    // W's rows run along the reduction: their powers go with dZ's columns
+    // W's rows run along the reduction: their powers go with dZ's columns, and the table's
+    // with them; without scales the epilogue multiplies it in
+    if (!scale) ep.table_top = table_top;
     if (xdtype != TCQ_X_F16 || scale || !direct(dz, lddz)) {
         const int64_t ldz = round_up(rows, 8);
         ScaleRows sx;
@@ -299,6 +317,7 @@ tcq_status tcq_gemm_dgrad(const uint32_t* bits, const uint32_t* start_state, con
         sx.n = n;
         sx.cols = rows;
         sx.col_exponents = scale ? row_exponents : nullptr;
+        sx.table_top = scale ? table_top : nullptr;
         sx.out = ws + sp.x;
         sx.ldo = ldz;
         sx.row_pow2 = x_pow2;

@@ -53,6 +53,7 @@ struct Barriers {
     uint32_t tmem;
     int stop;
     int fills[kSlots];  // warps that have filled a slot, counted from the start
+    uint32_t tops[kThreads / 32];  // of the table (staged_table_power)
 };
 
 struct Plan {
@@ -121,7 +122,7 @@ __device__ __forceinline__ void read_words(const unsigned char* p, uint32_t (&w)
 template <int K, int CODE>
 __global__ void __launch_bounds__(kThreads, 1)
 fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_words,
-             Plan p, const float* row_pow2, float* partial, unsigned int* err)
+             Plan p, WeightPowers powers, float* partial, unsigned int* err)
 {
     constexpr int RB = box_row_bytes(K);
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -153,8 +154,15 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    pdl_wait();  // the scaled activations and the row powers
+    float table = 1.f;  // the table's power
+    if constexpr (CODE == kCode16F32) {
+        // written ahead of the wait below: a launch that starts early follows one of this call's,
+        // which began after whatever used the workspace before
+        if (powers.staged) table = staged_table_power(reinterpret_cast<const float*>(sm), 1 << w.L, B.tops, powers.table_out);
+    }
+    pdl_wait();  // the scaled activations and the weights' powers
     pdl_release();
+    const TableParts parts(CODE == kCode16F16 ? powers.table : nullptr);
     const uint32_t tmem = B.tmem;
     volatile int* stop = &B.stop;
     const long long u0 = first_unit(p, blockIdx.x), u1 = first_unit(p, blockIdx.x + 1);
@@ -178,7 +186,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
             bits = row < w.rows ? w.bits + row * (cols / 32 * K) : nullptr;
             start = w.start_state + row * nb;
             scale = w.scale ? w.scale + row * nb : nullptr;
-            if (bits && scale) inv = __ldcg(row_pow2 + row);
+            if (bits && scale) inv = __ldcg(powers.row + row);
         };
         auto advance = [&](int by) {
             for (ks += by; ks >= p.steps; ks -= p.steps) {
@@ -218,6 +226,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
         bool ok = true;
         long long u = u0 + group;
         if (u < u1) fetch();
+        if constexpr (CODE == kCode16F16) table = parts.power();
         // Slots of a unit belong to a group each, slots of a stage to a half of every unit.
         const int slot = p.per == 2 ? group : half;
         const uint32_t go = smem_addr(&B.go[group]);
@@ -275,7 +284,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                     if (!first) prev = before;
                 }
                 uint32_t v[32];
-                decode_64<K, CODE>(words, prev, mask, sm, sc * inverse_pow2(pw), v);
+                decode_64<K, CODE>(words, prev, mask, sm, sc * inverse_pow2(power_product(pw, table)), v);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_addr(&B.go[group ^ 1]));
@@ -468,26 +477,26 @@ Plan make_plan(int code, int L, int K, long long rows, long long cols, long long
 
 template <int K, int CODE>
 cudaError_t launch(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p,
-                   const float* row_pow2, float* partial, unsigned int* err, bool early, cudaStream_t stream)
+                   const WeightPowers& powers, float* partial, unsigned int* err, bool early, cudaStream_t stream)
 {
     const cudaError_t e = cudaFuncSetAttribute(fused_kernel<K, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSmemBytes);
     if (e != cudaSuccess) return e;
     const size_t smem = p.table + (size_t)kSlots * p.per * (kABytes + p.np * kDepth * 2) +
                         2 * p.boxes * kRows * box_row_bytes(K) + sizeof(Barriers);
-    return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, words, p, row_pow2,
+    return launch_pdl(fused_kernel<K, CODE>, dim3(p.ctas), dim3(kThreads), smem, stream, early, w, map, words, p, powers,
                       partial, err);
 }
 
 template <int CODE>
 cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtensorMap& words, const Plan& p,
-                     const float* row_pow2, float* partial, unsigned int* err, bool early, cudaStream_t stream)
+                     const WeightPowers& powers, float* partial, unsigned int* err, bool early, cudaStream_t stream)
 {
     switch (w.K) {
-    case 1: return launch<1, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
-    case 2: return launch<2, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
-    case 3: return launch<3, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
-    default: return launch<4, CODE>(w, map, words, p, row_pow2, partial, err, early, stream);
+    case 1: return launch<1, CODE>(w, map, words, p, powers, partial, err, early, stream);
+    case 2: return launch<2, CODE>(w, map, words, p, powers, partial, err, early, stream);
+    case 3: return launch<3, CODE>(w, map, words, p, powers, partial, err, early, stream);
+    default: return launch<4, CODE>(w, map, words, p, powers, partial, err, early, stream);
     }
 }
 
@@ -511,7 +520,7 @@ size_t fused_partial_bytes(int cb_f16, int L, long long rows, long long cols, lo
 }
 
 cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx, long long n, int xdtype,
-                              const float* row_pow2, float* partial, const Epilogue& e, int num_sms, unsigned int* err,
+                              const WeightPowers& powers, float* partial, const Epilogue& e, int num_sms, unsigned int* err,
                               bool early, cudaStream_t stream)
 {
     const int code = code_of(w);
@@ -524,9 +533,9 @@ cudaError_t launch_gemm_fused(const CodedMatrix& w, const void* x, long long ldx
         words = map;  // not used
     else if (!make_map_words(&words, w.bits, w.rows, row_words, 4 * (w.K + 1), kRows))
         return cudaErrorInvalidValue;
-    cudaError_t st = code == kCode16Mad   ? launch_k<kCode16Mad>(w, map, words, p, row_pow2, partial, err, early, stream)
-                     : code == kCode16F16 ? launch_k<kCode16F16>(w, map, words, p, row_pow2, partial, err, early, stream)
-                                          : launch_k<kCode16F32>(w, map, words, p, row_pow2, partial, err, early, stream);
+    cudaError_t st = code == kCode16Mad   ? launch_k<kCode16Mad>(w, map, words, p, powers, partial, err, early, stream)
+                     : code == kCode16F16 ? launch_k<kCode16F16>(w, map, words, p, powers, partial, err, early, stream)
+                                          : launch_k<kCode16F32>(w, map, words, p, powers, partial, err, early, stream);
     if (st != cudaSuccess) return st;
     bool vec = (reinterpret_cast<uintptr_t>(e.out) & 7) == 0 && e.ldo % 4 == 0;
     if (e.residual) vec = vec && (reinterpret_cast<uintptr_t>(e.residual) & 7) == 0 && e.ldr % 4 == 0;

@@ -177,15 +177,27 @@ __device__ __forceinline__ int segment_of(const Item& w)
 // below n.
 template <int KIND, int XT>
 __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
-                                        int count, float row_scale, const float4* cols,
+                                        int count, int row_exponent, const float4* cols,
                                         const unsigned char* box_row, int half)
 {
-    if (e.row_scale) {
+    if constexpr (KIND == kGemmDgrad) {
+        if (e.row_scale || e.table_top) {
+            const float2 h = power_halves(row_exponent);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= row_scale;
+            for (int i = 0; i < 32; i += 2)
+                f2_split(f2_mul(f2_mul(f2(v[i], v[i + 1]), f2(h.x, h.x)), f2(h.y, h.y)), v[i], v[i + 1]);
+        }
     }
     if constexpr (KIND == kGemmForward) {
-        if (e.col_scale || e.bias) {
+        if (e.row_scale) {  // the row's and the column's powers together: each alone may pass fp32's range
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float4 p = cols[i / 2];
+                const float2 a = power_halves(row_exponent + exponent_of(p.x)), b = power_halves(row_exponent + exponent_of(p.y));
+                v[i] = fmaf(v[i] * a.x, a.y, p.z);
+                v[i + 1] = fmaf(v[i + 1] * b.x, b.y, p.w);
+            }
+        } else if (e.col_scale || e.table_top || e.bias) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {  // two columns per 16-byte read, the same in every lane
                 const float4 p = cols[i / 2];
@@ -418,6 +430,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     } else if (warp >= 4) {
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const float table = KIND != kGemmWgrad ? table_power(e.table_top) : 1.f;
         int done = 0;
         unsigned turn = 0;  // of the warp's boxes: the next one's last store is then the oldest
         bool ok = true;
@@ -497,7 +510,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     for (int i = threadIdx.x - 128; i < kTile; i += 32 * EW) {
                         const long long c = n0 + i;
                         float* at = reinterpret_cast<float*>(S.cols + i / 2) + (i & 1);
-                        at[0] = e.col_scale && c < p.n ? __ldcg(e.col_scale + c) : 1.f;
+                        at[0] = power_product(e.col_scale && c < p.n ? __ldcg(e.col_scale + c) : 1.f, table);
                         at[2] = e.bias && c < p.n ? __ldg(e.bias + c) : 0.f;
                     }
                 }
@@ -518,7 +531,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 if constexpr (KIND == kGemmForward) ok = named_all(1, 32 * EW, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const float row_scale = e.row_scale && r < p.m ? __ldcg(e.row_scale + r) : 1.f;
+                const int row_exponent = (e.row_scale && r < p.m ? exponent_of(__ldcg(e.row_scale + r)) : 0) +
+                                         (KIND == kGemmDgrad ? exponent_of(table) : 0);
                 if (cut) {  // the sums as they are, 32 columns at a time
 #pragma unroll 1
                     for (int c = c0; c < c0 + span; c += 32) {
@@ -553,7 +567,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c + 32 * h, v);
                         const int count = p.n - ch < 32 ? (int)(p.n - ch) : 32;
-                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, row_scale,
+                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, row_exponent,
                                                        S.cols + (c + 32 * h) / 2, box + lane * 128, h);
                         if (h == 0 && !residual) {  // the box's last store has been read
                             if (lane == 0) bulk_wait_read<boxes - 1>();

@@ -1,5 +1,5 @@
 // operands.cu -- the passes that bring the activations of a product to binary16 rows,
-// and the powers of two of a coded matrix's rows.
+// and the powers of two of a coded matrix's rows and of its table.
 //
 // A bfloat16 row scaled by a power of two of its own is exact in binary16 down to
 // 2^-32 of its largest element (binary16 has three more bits, and 30 powers below the
@@ -31,6 +31,40 @@ __device__ __forceinline__ void row_power(const RowPowers& p, long long r)
     }
 }
 
+// The largest finite magnitude of a part of the table, 16 bytes a thread and step where
+// its address allows (a 128 KB table: four loads in flight per thread of each of the parts).
+__device__ __forceinline__ void table_part(const RowPowers& p, int part)
+{
+    __shared__ uint32_t warps[kThreads / 32];
+    const int entries = 1 << p.table_log2, bytes = entries * (p.table_f16 ? 2 : 4);
+    const int first = part * kThreads + threadIdx.x;
+    uint32_t top = 0u;
+    if ((reinterpret_cast<uintptr_t>(p.table) & 15) == 0 && bytes % 16 == 0) {
+#pragma unroll 4
+        for (int i = first; i < bytes / 16; i += kTableParts * kThreads) {
+            const uint4 v = __ldg(static_cast<const uint4*>(p.table) + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const float2 t = p.table_f16 ? x_unpack2<TCQ_X_F16>(w[h]) : make_float2(__uint_as_float(w[h]), 0.f);
+                top = max(top, max(finite_magnitude(t.x), finite_magnitude(t.y)));
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int i = first; i < entries; i += kTableParts * kThreads)
+            top = max(top, finite_magnitude(load_codeword(p.table, p.table_f16, (uint32_t)i)));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 1; i < kThreads / 32; ++i) top = max(top, warps[i]);
+        p.table_top[part] = top;
+    }
+}
+
 // The power of two with this exponent field.
 __device__ __forceinline__ float power_of(uint32_t exponent) { return __uint_as_float(exponent << 23); }
 
@@ -43,6 +77,9 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
     const uint16_t* xr = static_cast<const uint16_t*>(a.x) + r * a.ldx;
     uint16_t* o = static_cast<uint16_t*>(a.out) + r * a.ldo;
     uint32_t top = 0u;
+    // the columns' exponent fields with the table's power, held like power_product
+    const int table = exponent_of(table_power(a.table_top));
+    auto column = [&](uint32_t field) { return power_of((uint32_t)max(min((int)field + table, 253), 1)); };
     auto eight = [&](long long c, float (&f)[8]) {
         const uint4 v = *reinterpret_cast<const uint4*>(xr + c);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -56,8 +93,8 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
             const uint2 e = *reinterpret_cast<const uint2*>(a.col_exponents + c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                f[i] *= power_of((e.x >> (8 * i)) & 0xffu);
-                f[4 + i] *= power_of((e.y >> (8 * i)) & 0xffu);
+                f[i] *= column((e.x >> (8 * i)) & 0xffu);
+                f[4 + i] *= column((e.y >> (8 * i)) & 0xffu);
             }
         }
     };
@@ -69,7 +106,7 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
         for (int i = 0; i < 8; ++i) top = max(top, finite_magnitude(f[i]));
     }
     for (long long c = vcols + threadIdx.x; c < a.cols; c += kThreads)
-        top = max(top, finite_magnitude(x_load<XT>(xr, c) * (a.col_exponents ? power_of(a.col_exponents[c]) : 1.f)));
+        top = max(top, finite_magnitude(x_load<XT>(xr, c) * (a.col_exponents ? column(a.col_exponents[c]) : 1.f)));
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
     __syncthreads();
@@ -91,18 +128,22 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
             *reinterpret_cast<uint4*>(o + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     for (long long c = vcols + threadIdx.x; c < a.cols && TCQ_IN_BOUNDS(r * a.ldo + c, a.n * a.ldo); c += kThreads)
-        o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (a.col_exponents ? power_of(a.col_exponents[c]) : 1.f) * inv);
+        o[c] = x_bits<TCQ_X_F16>(x_load<XT>(xr, c) * (a.col_exponents ? column(a.col_exponents[c]) : 1.f) * inv);
 }
 
-// CTAs below a.n scale a row of activations each, the others take eight rows of W.
+// The first CTAs take the parts of the table, the next a.n scale a row of activations
+// each, the others take eight rows of W.
 template <int XT>
 __global__ void __launch_bounds__(kThreads) prepare_kernel(ScaleRows a, RowPowers p)
 {
     pdl_release();
-    if (blockIdx.x < a.n) {
-        scale_row<XT>(a, blockIdx.x);
+    const long long cta = (long long)blockIdx.x - (p.table_top ? kTableParts : 0);
+    if (cta < 0) {
+        table_part(p, blockIdx.x);
+    } else if (cta < a.n) {
+        scale_row<XT>(a, cta);
     } else {
-        const long long r = (blockIdx.x - a.n) * (kThreads / 32) + (threadIdx.x >> 5);
+        const long long r = (cta - a.n) * (kThreads / 32) + (threadIdx.x >> 5);
         if (r < p.rows) row_power(p, r);
     }
     // The grid ends after the launch that it ran beside: one CTA waits for that (if all
@@ -133,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) copy16_kernel(const uint16_t* x, lon
 cudaError_t launch_prepare(ScaleRows a, RowPowers p, cudaStream_t stream)
 {
     a.vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ldx % 8 == 0;
-    const long long grid = a.n + (p.rows + kThreads / 32 - 1) / (kThreads / 32);
+    const long long grid = (p.table_top ? kTableParts : 0) + a.n + (p.rows + kThreads / 32 - 1) / (kThreads / 32);
     return launch_pdl(a.xdtype == TCQ_X_BF16 ? prepare_kernel<TCQ_X_BF16> : prepare_kernel<TCQ_X_F16>,
                       dim3((unsigned)grid), dim3(kThreads), 0, stream, a.early, a, p);
 }
