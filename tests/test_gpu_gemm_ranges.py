@@ -1,5 +1,5 @@
 """Batched products with a trellis-coded matrix whose parts lie far from 1: tables of tiny
-and of huge entries, activations, scales and entries of opposite powers.
+and of huge entries, activations, scales and entries of opposite powers, entries that are not finite.
 
 Tolerances: tests/gemm_reference.py (product_bound), then half a step of the output's
 type.  Powers of two change no rounding, so the bounds are those of matrices near 1."""
@@ -93,3 +93,29 @@ def test_opposite_powers(xpower, spower, tpower, T, n, cuda_device):
     check_gemm(args, w, x, tcq.gemm(*args, x))
     dz = torch.from_numpy(rng.standard_normal((n, rows)) * 2.0**xpower).to(cuda_device).to(torch.bfloat16)
     _check_dgrad(args, w, dz, "dgrad")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("n", [1, 24, 600])
+@pytest.mark.parametrize("T,nb", [(64, 3), (100, 3)])
+def test_table_entry_that_is_not_finite(T, nb, n, scaled, bad, cuda_device):
+    """The outputs of rows that never decode to it are what they are with any other entry
+    there, behind the last column, too."""
+    import torch
+
+    rng = np.random.default_rng(T + n)
+    rows, cols = 20, T * nb
+    table = _table(rng, 16, "f16", 0)
+    scale = rng.lognormal(-4.0, 0.5, rows * nb).astype(np.float32) if scaled else None
+    state = rng.bit_generator.state
+    args, w = _coded(rng, 16, 2, T, rows, cols, table, scale, cuda_device)
+    table[0] = bad
+    rng.bit_generator.state = state
+    args2, w2 = _coded(rng, 16, 2, T, rows, cols, table, scale, cuda_device)
+    keep = torch.isfinite(w2).all(1)
+    assert torch.equal(args[0], args2[0]) and int(keep.sum()) >= 10
+    x = torch.from_numpy(rng.standard_normal((n, cols))).to(cuda_device).to(torch.bfloat16)
+    y, y2 = tcq.gemm(*args, x), tcq.gemm(*args2, x)
+    assert torch.isfinite(y2[:, keep]).all()
+    assert torch.equal(y2[:, keep], y[:, keep])

@@ -201,11 +201,12 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
         // power, and without the ring of boxes its words and the one before them.
         uint32_t nwords[2 * K], nprev = 0u;
         float nsc = 0.f, npw = 1.f;
-        bool nfirst = false;
+        bool nfirst = false, nout = false;  // columns behind the last
         auto fetch = [&]() {
             const int c = ks * 128 + half * kDepth;
             const int j = tshift >= 0 ? c >> tshift : c / T;
             nfirst = c == j * T;
+            nout = c >= cols;
             nsc = 0.f;
             nprev = 0u;
             npw = inv;
@@ -266,7 +267,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
             for (; u < s1; u += 2, ++own) {
                 uint32_t words[2 * K], prev = nprev;
                 const float sc = nsc, pw = npw;
-                const bool first = nfirst;
+                const bool first = nfirst, out = nout;
 #pragma unroll
                 for (int h = 0; h < 2 * K; ++h) words[h] = nwords[h];
                 if (u + 2 < u1) {
@@ -285,6 +286,10 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
                 }
                 uint32_t v[32];
                 decode_64<K, CODE>(words, prev, mask, sm, sc * inverse_pow2(power_product(pw, table)), v);
+                if (out) {  // no weight: entry 0 need not be finite, and 0 times it would spoil the row
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) v[h] = 0u;
+                }
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(smem_addr(&B.go[group ^ 1]));
