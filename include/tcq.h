@@ -385,8 +385,9 @@ tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 forma
  * scales nor entries need to lie near 1: with M the row's largest |scale| times the
  * table's largest finite entry, weights keep binary16's 11 bits down to 2^-27 M (the
  * computed code's to 2^-14 M) and are within 2^-38 M (2^-25 M) below.  A bfloat16 row of X is scaled to
- * binary16 by a power of two of its own, exactly for elements above 2^-32 of the row's
- * largest and within 2^-39 of that largest for the others.  A single token (n == 1, no checkpoint
+ * binary16 by a power of two of its own, exactly for elements from 2^-31 of the row's
+ * largest up and within 2^-39 of that largest for the others; so are binary16 rows
+ * that are not all 16-byte aligned (exact from 2^-28 up).  A single token (n == 1, no checkpoint
  * of Z) takes tcq_gemv's kernels, with both operands in fp32.
  *
  *   bits, start_state, scale, codebook, cb_dtype, L, k, T, rows, cols  as tcq_gemv
@@ -419,7 +420,10 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
 
 /*
  * Input gradient: dX[i, c] = sum_r dZ[i, r] W[r, c], with tcq_gemm's operand
- * formats (dZ takes the place of X), fp32 sums, rounded once to xdtype.
+ * formats (dZ takes the place of X), fp32 sums, rounded once to xdtype.  In the binary16
+ * products of a matrix with scales dZ[i, r] is multiplied by the powers of two of W's row r
+ * first, in either type; what holds for elements beside their row's largest then holds
+ * for those products.
  *   dz  [n, rows], row stride lddz.   dx  out: [n, cols], row stride lddx.
  * rows == 0 gives dX = 0; n == 0 or cols == 0 is a no-op.  Everything else as tcq_gemm.
  */

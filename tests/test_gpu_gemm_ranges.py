@@ -119,3 +119,48 @@ def test_table_entry_that_is_not_finite(T, nb, n, scaled, bad, cuda_device):
     y, y2 = tcq.gemm(*args, x), tcq.gemm(*args2, x)
     assert torch.isfinite(y2[:, keep]).all()
     assert torch.equal(y2[:, keep], y[:, keep])
+
+
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [4, 64])
+def test_small_elements_beside_a_large_one(T, dtype, scaled, cuda_device):
+    """Rows brought to binary16 by a power of two are exact down to 2^-31 of their largest
+    element (bfloat16) or 2^-28 (binary16, rows that are not aligned), and within 2^-39 of
+    it below.  The identity, in codes of one symbol per weight, shows every element."""
+    import torch
+
+    k = L = 4
+    size = 64
+    if dtype == "bf16":
+        dt, pad, top, least, eps = torch.bfloat16, 0, 1.0, 2.0**-31, 2.0**-7
+        small = [2.0**-20 * (1 + eps), least, least * (1 + eps), least * (2 - eps), least / 2 * (1 + eps), 2.0**-36 * 1.25,
+                 2.0**-60]
+    else:
+        dt, pad, top, least, eps = torch.float16, 1, 2.0**15, 2.0**-13, 2.0**-10
+        small = [1 + eps, least, least * (1 + eps), least * (2 - eps), least / 2 * (1 + eps), 2.0**-24]
+    table = np.zeros(16, dtype=np.float16)
+    table[1] = 1.0
+    blocks = np.eye(size, dtype=np.uint64).reshape(-1, T)
+    words = np.zeros((blocks.shape[0], max(1, T * k // 32)), dtype=np.uint64)
+    for t in range(T):
+        words[:, t * k // 32] |= blocks[:, t] << np.uint64(32 - k - t * k % 32)
+    bits = torch.from_numpy(words.astype(np.uint32).view(np.int32)).to(cuda_device)
+    start = torch.zeros(blocks.shape[0], dtype=torch.int32, device=cuda_device)
+    times = 0.5 if scaled else 1.0
+    scale = torch.full((blocks.shape[0],), times, device=cuda_device) if scaled else None
+    x = torch.zeros((2, size + 2 * pad), dtype=dt, device=cuda_device)[:, pad:pad + size]
+    for i, v in enumerate(small):
+        x[0, 5 * i + 1] = v
+        assert float(x[0, 5 * i + 1]) == v
+    x[0, 0] = top
+    args = (bits, start, scale, torch.from_numpy(table).to(cuda_device), L, k, T, size, size)
+    for y in (tcq.gemm(*args, x), tcq.gemm_dgrad(*args, x)):
+        for i, v in enumerate(small):
+            got = float(y[0, 5 * i + 1])
+            if v >= least and (dtype == "bf16" or v * times >= 2.0**-13):
+                assert got == v * times
+            else:  # and the output's own half step
+                off = 2.0**-39 * top * times
+                assert abs(got - v * times) <= off + max(eps / 2 * (v * times + off), 2.0**-25 if dtype == "f16" else 0)
+        assert float(y[0, 0]) == top * times and bool((y[1] == 0).all())

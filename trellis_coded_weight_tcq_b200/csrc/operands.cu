@@ -1,10 +1,10 @@
 // operands.cu -- the passes that bring the activations of a product to binary16 rows,
 // and the powers of two of a coded matrix's rows and of its table.
 //
-// A bfloat16 row scaled by a power of two of its own is exact in binary16 down to
-// 2^-32 of its largest element (binary16 has three more bits, and 30 powers below the
-// largest before its subnormals begin to cut); binary16 keeps the weights exact where
-// bfloat16 would not.  The rows are read twice (the second time from L2) and written
+// A row's largest element is brought to [2^14, 2^15).  A bfloat16 row is then exact down to
+// 2^-31 of that element (eight bits from 2^-17 up end above 2^-24, binary16's last), a
+// binary16 one down to 2^-28, and smaller elements are off by at most 2^-25; binary16
+// keeps the weights exact where bfloat16 would not.  The rows are read twice (the second time from L2) and written
 // once: bound by memory, about 4 bytes per element.
 #include "decode16.cuh"
 #include "gemm.cuh"
