@@ -6,7 +6,7 @@ The library links the CUDA runtime statically, so it loads next to PyTorch's
 own runtime without a version clash; device pointers and streams are shared
 through the primary context.  ``--debug`` also builds ``libtcq_debug.so``: the
 same sources with TCQ_DEBUG defined (every global-memory index of the encode,
-decode and matrix-vector kernels checked against its buffer, a failure
+decode, matrix-vector and batched-layer kernels checked against its buffer, a failure
 recorded in the device error word and the access skipped) and relocatable
 device code, so that one error word serves every kernel file.
 """

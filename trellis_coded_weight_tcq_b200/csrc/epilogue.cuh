@@ -8,23 +8,23 @@
 
 namespace tcq {
 
-// Outputs (t, r .. r + 3), those below `rows`, from their sums: the powers of two, bias,
-// 8-bit checkpoint, activation and residual, rounded once.  All lanes of a warp have the
+// Outputs (t, r .. r + 3) of [tokens, rows], those below `rows`, from their sums: the powers
+// of two, bias, 8-bit checkpoint, activation and residual, rounded once.  All lanes of a warp have the
 // same t and consecutive quads, eight lanes a group of 32.  `vec`: out and residual rows
 // that 8-byte accesses can reach.
 template <int XT>
-__device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long long r, long long rows, float (&v)[4],
-                                            bool vec)
+__device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long long r, long long tokens, long long rows,
+                                            float (&v)[4], bool vec)
 {
     const int lane = threadIdx.x & 31;
     const int count = rows - r < 4 ? (rows - r > 0 ? (int)(rows - r) : 0) : 4;
-    const int row_exponent = e.row_scale ? exponent_of(__ldcg(e.row_scale + t)) : 0;
+    const int row_exponent = e.row_scale && TCQ_IN_BOUNDS(t, tokens) ? exponent_of(__ldcg(e.row_scale + t)) : 0;
     const TableParts parts(e.table_top);
     float column[4], bias[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        column[i] = i < count && e.col_scale ? __ldcg(e.col_scale + r + i) : 1.f;
-        bias[i] = i < count && e.bias ? __ldg(e.bias + r + i) : 0.f;
+        column[i] = i < count && e.col_scale && TCQ_IN_BOUNDS(r + i, rows) ? __ldcg(e.col_scale + r + i) : 1.f;
+        bias[i] = i < count && e.bias && TCQ_IN_BOUNDS(r + i, rows) ? __ldg(e.bias + r + i) : 0.f;
     }
     const float table = parts.power();
 #pragma unroll
@@ -42,14 +42,17 @@ __device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long
         const bool int8 = e.z_format == TCQ_Q8_INT8;
         const uint32_t byte = int8 ? q8_scale_byte<TCQ_Q8_INT8>(top) : q8_scale_byte<TCQ_Q8_E4M3>(top);
         const float inv = q8_inv(byte);
-        if (count > 0 && (lane & 7) == 0) e.z_scales[t * ((rows + 31) / 32) + r / 32] = (uint8_t)byte;
+        if (count > 0 && (lane & 7) == 0 && TCQ_IN_BOUNDS(t * ((rows + 31) / 32) + r / 32, tokens * ((rows + 31) / 32))) e.z_scales[t * ((rows + 31) / 32) + r / 32] = (uint8_t)byte;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i < count)
+            if (i < count && TCQ_IN_BOUNDS(t * rows + r + i, tokens * rows))
                 e.z_codes[t * rows + r + i] = byte == 255u ? 0 : (uint8_t)(int8 ? q8_encode<TCQ_Q8_INT8>(v[i], inv)
                                                                               : q8_encode<TCQ_Q8_E4M3>(v[i], inv));
     }
     act_values(v, e.act);
+    if (count > 0 && !(TCQ_IN_BOUNDS(t * e.ldo + r + count - 1, (tokens - 1) * e.ldo + rows) &&
+                       (!e.residual || TCQ_IN_BOUNDS(t * e.ldr + r + count - 1, (tokens - 1) * e.ldr + rows))))
+        return;
     uint16_t* out = static_cast<uint16_t*>(e.out) + t * e.ldo + r;
     const uint16_t* res = e.residual ? static_cast<const uint16_t*>(e.residual) + t * e.ldr + r : nullptr;
     if (vec && count == 4) {
@@ -67,13 +70,13 @@ __device__ __forceinline__ void finish_quad(const Epilogue& e, long long t, long
 }
 
 // The fp32 outputs of the weight gradient.
-__device__ __forceinline__ void finish_quad_f32(const Epilogue& e, long long t, long long r, long long rows,
-                                                const float (&v)[4])
+__device__ __forceinline__ void finish_quad_f32(const Epilogue& e, long long t, long long r, long long tokens,
+                                                long long rows, const float (&v)[4])
 {
     float* out = static_cast<float*>(e.out) + t * e.ldo + r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (r + i < rows) out[i] = e.accumulate ? out[i] + v[i] : v[i];
+        if (r + i < rows && TCQ_IN_BOUNDS(t * e.ldo + r + i, (tokens - 1) * e.ldo + rows)) out[i] = e.accumulate ? out[i] + v[i] : v[i];
 }
 
 }  // namespace tcq

@@ -186,7 +186,7 @@ fused_kernel(CodedMatrix w, const __grid_constant__ CUtensorMap map_x, const __g
             bits = row < w.rows ? w.bits + row * (cols / 32 * K) : nullptr;
             start = w.start_state + row * nb;
             scale = w.scale ? w.scale + row * nb : nullptr;
-            if (bits && scale) inv = __ldcg(powers.row + row);
+            if (bits && scale && TCQ_IN_BOUNDS(row, w.rows)) inv = __ldcg(powers.row + row);
         };
         auto advance = [&](int by) {
             for (ks += by; ks >= p.steps; ks -= p.steps) {
@@ -443,10 +443,12 @@ __global__ void __launch_bounds__(256) fused_finish_kernel(Plan p, Epilogue e, l
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = 0; i < pieces; ++i) {
+        if (!TCQ_IN_BOUNDS(src - partial + (long long)i * p.np * kRows + 3, (long long)p.row_tiles * p.pieces * p.np * kRows))
+            break;
         const float4 d = __ldcg(reinterpret_cast<const float4*>(src + (long long)i * p.np * kRows));
         v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
     }
-    finish_quad<XT>(e, t, r, rows, v, vec);
+    finish_quad<XT>(e, t, r, p.n, rows, v, vec);
 }
 
 int code_of(const CodedMatrix& w) { return w.cb_f16 == 1 ? kCode16F16 : w.cb_f16 == 0 ? kCode16F32 : kCode16Mad; }

@@ -173,10 +173,10 @@ __device__ __forceinline__ int segment_of(const Item& w)
     return (n + parts - 1) / parts;
 }
 
-// 32 values of one row through the epilogue: row r, columns c .. c + 31, `count` of them
+// 32 values of one row through the epilogue: row r of m, columns c .. c + 31, `count` of them
 // below n.
 template <int KIND, int XT>
-__device__ __forceinline__ void apply32(const Epilogue& e, long long r, long long c, long long n, float (&v)[32],
+__device__ __forceinline__ void apply32(const Epilogue& e, long long r, long long c, long long m, long long n, float (&v)[32],
                                         int count, int row_exponent, const float4* cols,
                                         const unsigned char* box_row, int half)
 {
@@ -214,7 +214,7 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
             const bool int8 = e.z_format == TCQ_Q8_INT8;
             const uint32_t byte = int8 ? q8_scale_byte<TCQ_Q8_INT8>(top) : q8_scale_byte<TCQ_Q8_E4M3>(top);
             const float inv = q8_inv(byte);
-            e.z_scales[group] = (uint8_t)byte;
+            if (TCQ_IN_BOUNDS(group, m * ((n + 31) / 32))) e.z_scales[group] = (uint8_t)byte;
             uint32_t code[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) code[i] = 0u;
@@ -225,10 +225,11 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
                     code[i / 4] |= q << (8 * (i & 3));
                 }
             }
-            if (count == 32 && (reinterpret_cast<uintptr_t>(z) & 15) == 0) {
+            const bool in = TCQ_IN_BOUNDS(r * n + c + count - 1, m * n);
+            if (in && count == 32 && (reinterpret_cast<uintptr_t>(z) & 15) == 0) {
                 reinterpret_cast<uint4*>(z)[0] = make_uint4(code[0], code[1], code[2], code[3]);
                 reinterpret_cast<uint4*>(z)[1] = make_uint4(code[4], code[5], code[6], code[7]);
-            } else {
+            } else if (in) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (i < count) z[i] = (uint8_t)(code[i / 4] >> (8 * (i & 3)));
@@ -252,10 +253,13 @@ __device__ __forceinline__ void apply32(const Epilogue& e, long long r, long lon
 }
 
 // A box's rows to outputs that TMA cannot address, row by row: neighbouring lanes store
-// neighbouring elements (2 or 4 bytes each).
+// neighbouring elements (2 or 4 bytes each).  The box starts `at` elements into `base`,
+// which has `most`.
 template <typename T>
-__device__ __forceinline__ void store_rows(const unsigned char* box, T* out, long long ldo, int rows, int cols, int lane)
+__device__ __forceinline__ void store_rows(const unsigned char* box, T* base, long long at, long long most, long long ldo,
+                                           int rows, int cols, int lane)
 {
+    T* out = base + at;
     constexpr int per = 128 / sizeof(T), ahead = 8 * 32 / per;  // columns of a box, rows read together
 #pragma unroll 1
     for (int i0 = 0; i0 < rows; i0 += ahead) {
@@ -268,23 +272,24 @@ __device__ __forceinline__ void store_rows(const unsigned char* box, T* out, lon
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int i = i0 + j * 32 / per, c = lane + j * 32 % per;
-            if (i < rows && c < cols) out[i * ldo + c] = v[j];
+            if (i < rows && c < cols && TCQ_IN_BOUNDS(at + i * ldo + c, most)) out[i * ldo + c] = v[j];
         }
     }
 }
 
 // The reverse: a box from 16-bit rows.  `vec`: rows of whole 16-byte vectors, eight lanes a
 // row, all loads in flight together (a lane's own row would take 32 sectors per load).
-__device__ __forceinline__ void load_rows(unsigned char* box, const uint16_t* in, long long ld, int rows, int cols, int lane,
-                                          bool vec)
+__device__ __forceinline__ void load_rows(unsigned char* box, const uint16_t* base, long long at, long long most, long long ld,
+                                          int rows, int cols, int lane, bool vec)
 {
+    const uint16_t* in = base + at;
     if (vec) {
         const int c = lane & 7;
         uint4 t[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3);
-            t[i] = r < rows && 8 * c < cols ? *reinterpret_cast<const uint4*>(in + r * ld + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+            t[i] = r < rows && 8 * c < cols && TCQ_IN_BOUNDS(at + r * ld + 8 * c + 7, most) ? *reinterpret_cast<const uint4*>(in + r * ld + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -299,7 +304,7 @@ __device__ __forceinline__ void load_rows(unsigned char* box, const uint16_t* in
         for (int h = 0; h < 64; h += 32) {
             const int c = lane + h, byte = 2 * c;
             *reinterpret_cast<uint16_t*>(box + i * 128 + ((((byte >> 4) ^ (i & 7)) << 4) | (byte & 15))) =
-                c < cols ? in[i * ld + c] : (uint16_t)0;
+                c < cols && TCQ_IN_BOUNDS(at + i * ld + c, most) ? in[i * ld + c] : (uint16_t)0;
         }
     }
 }
@@ -473,7 +478,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         const float* o = static_cast<const float*>(e.out) + (long long)(r0 + lane) * e.ldo + c;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (c + i < p.n) sum[32 * j + i] += o[i];
+                            if (c + i < p.n && TCQ_IN_BOUNDS((long long)(r0 + lane) * e.ldo + c + i, (p.m - 1) * e.ldo + p.n))
+                                sum[32 * j + i] += o[i];
                     }
                     {
                         if (lane == 0) bulk_wait_read<0>();
@@ -486,8 +492,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         if (!plain) fence_async_shared();
                         __syncwarp();
                         if (plain) {
-                            store_rows(box, static_cast<float*>(e.out) + (long long)r0 * e.ldo + c, e.ldo,
-                                       p.m - r0 < 32 ? (int)(p.m - r0) : 32, p.n - c < 32 ? (int)(p.n - c) : 32, lane);
+                            store_rows(box, static_cast<float*>(e.out), (long long)r0 * e.ldo + c, (p.m - 1) * e.ldo + p.n,
+                                       e.ldo, p.m - r0 < 32 ? (int)(p.m - r0) : 32, p.n - c < 32 ? (int)(p.n - c) : 32, lane);
                             __syncwarp();
                         } else if (lane == 0) {
                             if (e.accumulate && !cut)
@@ -519,7 +525,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 auto residual_box = [&](unsigned char* box, int c) {
                     if (lane == 0) bulk_wait_read<boxes - 1>();
                     __syncwarp();
-                    load_rows(box, static_cast<const uint16_t*>(e.residual) + r0 * e.ldr + n0 + c, e.ldr, rows,
+                    load_rows(box, static_cast<const uint16_t*>(e.residual), r0 * e.ldr + n0 + c,
+                              (p.m - 1) * e.ldr + p.n, e.ldr, rows,
                               p.n - n0 - c < 64 ? (int)(p.n - n0 - c) : 64, lane, vec);
                     __syncwarp();
                 };
@@ -567,7 +574,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         float v[32];
                         tmem_load32(lanes + acc * 256 + c + 32 * h, v);
                         const int count = p.n - ch < 32 ? (int)(p.n - ch) : 32;
-                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.n, v, count, row_exponent,
+                        if (r < p.m) apply32<KIND, XT>(e, r, ch, p.m, p.n, v, count, row_exponent,
                                                        S.cols + (c + 32 * h) / 2, box + lane * 128, h);
                         if (h == 0 && !residual) {  // the box's last store has been read
                             if (lane == 0) bulk_wait_read<boxes - 1>();
@@ -584,7 +591,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             bulk_commit();
                         }
                     } else {
-                        store_rows(box, static_cast<uint16_t*>(e.out) + r0 * e.ldo + n0 + c, e.ldo, rows, cols, lane);
+                        store_rows(box, static_cast<uint16_t*>(e.out), r0 * e.ldo + n0 + c, (p.m - 1) * e.ldo + p.n, e.ldo,
+                                   rows, cols, lane);
                         __syncwarp();
                     }
                 }
@@ -620,13 +628,16 @@ __global__ void __launch_bounds__(256) finish_kernel(Shape p, Epilogue e, const 
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int i = 0; i < p.pieces; ++i) {
+        if (!TCQ_IN_BOUNDS(src - partial + (long long)i * kTile * kTile + 3,
+                           ((long long)p.m_tiles * p.n_tiles - p.whole) * p.pieces * kTile * kTile))
+            break;
         const float4 d = __ldcg(reinterpret_cast<const float4*>(src + (long long)i * kTile * kTile));
         v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
     }
     if constexpr (KIND == kGemmWgrad)
-        finish_quad_f32(e, r, n0 + c, p.n, v);
+        finish_quad_f32(e, r, n0 + c, p.m, p.n, v);
     else
-        finish_quad<XT>(e, r, n0 + c, p.n, v, vec);
+        finish_quad<XT>(e, r, n0 + c, p.m, p.n, v, vec);
 }
 
 // The order of the tiles.  The axis with fewer tiles goes first: where its operand is

@@ -21,10 +21,10 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ void row_power(const RowPowers& p, long long r)
 {
     uint32_t top = 0u;
-    for (int j = threadIdx.x & 31; j < p.per_row; j += 32)
+    for (int j = threadIdx.x & 31; j < p.per_row && TCQ_IN_BOUNDS(r * p.per_row + j, p.rows * p.per_row); j += 32)
         top = max(top, finite_magnitude(__ldg(p.scale + r * p.per_row + j)));
     top = __reduce_max_sync(0xffffffffu, top);
-    if ((threadIdx.x & 31) == 0) {
+    if ((threadIdx.x & 31) == 0 && TCQ_IN_BOUNDS(r, p.rows)) {
         const float v = pow2_clamped(power_above(top));
         p.out[r] = v;
         if (p.exponents) p.exponents[r] = (uint8_t)(__float_as_uint(v) >> 23);
@@ -41,7 +41,7 @@ __device__ __forceinline__ void table_part(const RowPowers& p, int part)
     uint32_t top = 0u;
     if ((reinterpret_cast<uintptr_t>(p.table) & 15) == 0 && bytes % 16 == 0) {
 #pragma unroll 4
-        for (int i = first; i < bytes / 16; i += kTableParts * kThreads) {
+        for (int i = first; i < bytes / 16 && TCQ_IN_BOUNDS(16 * i + 15, bytes); i += kTableParts * kThreads) {
             const uint4 v = __ldg(static_cast<const uint4*>(p.table) + i);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -52,7 +52,7 @@ __device__ __forceinline__ void table_part(const RowPowers& p, int part)
         }
     } else {
 #pragma unroll 4
-        for (int i = first; i < entries; i += kTableParts * kThreads)
+        for (int i = first; i < entries && TCQ_IN_BOUNDS(i, entries); i += kTableParts * kThreads)
             top = max(top, finite_magnitude(load_codeword(p.table, p.table_f16, (uint32_t)i)));
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -61,7 +61,7 @@ __device__ __forceinline__ void table_part(const RowPowers& p, int part)
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 1; i < kThreads / 32; ++i) top = max(top, warps[i]);
-        p.table_top[part] = top;
+        if (TCQ_IN_BOUNDS(part, kTableParts)) p.table_top[part] = top;
     }
 }
 
@@ -81,7 +81,8 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
     const int table = exponent_of(table_power(a.table_top));
     auto column = [&](uint32_t field) { return power_of((uint32_t)max(min((int)field + table, 253), 1)); };
     auto eight = [&](long long c, float (&f)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(xr + c);
+        const uint4 v = TCQ_IN_BOUNDS(r * a.ldx + c + 7, (a.n - 1) * a.ldx + a.cols) ? *reinterpret_cast<const uint4*>(xr + c)
+                                                                                    : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -105,7 +106,7 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = max(top, finite_magnitude(f[i]));
     }
-    for (long long c = vcols + threadIdx.x; c < a.cols; c += kThreads)
+    for (long long c = vcols + threadIdx.x; c < a.cols && TCQ_IN_BOUNDS(r * a.ldx + c, (a.n - 1) * a.ldx + a.cols); c += kThreads)
         top = max(top, finite_magnitude(x_load<XT>(xr, c) * (a.col_exponents ? column(a.col_exponents[c]) : 1.f)));
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
@@ -117,7 +118,7 @@ __device__ __forceinline__ void scale_row(const ScaleRows& a, long long r)
     if (top != 0u) p = power_above(top) - 15;
     if (p < -126) p = -126;
     const float inv = pow2_clamped(-p);
-    if (threadIdx.x == 0) a.row_pow2[r] = pow2_clamped(p);
+    if (threadIdx.x == 0 && TCQ_IN_BOUNDS(r, a.n)) a.row_pow2[r] = pow2_clamped(p);
     for (long long c = 8ll * threadIdx.x; c < vcols; c += 8 * kThreads) {
         float f[8];
         eight(c, f);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) copy16_kernel(const uint16_t* x, lon
         for (long long c = 8ll * threadIdx.x; c < cols; c += 8 * kThreads) {
             uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? x[r * ldx + c + i] : 0u;
+            for (int i = 0; i < 8; ++i) v[i] = c + i < cols && TCQ_IN_BOUNDS(r * ldx + c + i, (n - 1) * ldx + cols) ? x[r * ldx + c + i] : 0u;
             if (TCQ_IN_BOUNDS(r * ldo + c + 7, n * ldo))
                 *reinterpret_cast<uint4*>(out + r * ldo + c) =
                     make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) pack8_vec_kernel(const uint16_t* x, 
             }
             if (in) {
                 *reinterpret_cast<uint4*>(cr + c) = make_uint4(code[0], code[1], code[2], code[3]);
-                if ((i & 1) == 0) sr[i / 2] = (uint8_t)byte;
+                if ((i & 1) == 0 && TCQ_IN_BOUNDS(r * groups + i / 2, n * groups)) sr[i / 2] = (uint8_t)byte;
             }
         }
     }
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) pack8_kernel(const uint16_t* x, long
         for (long long g = (long long)blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32; g < groups;
              g += (long long)gridDim.y * (blockDim.x / 32)) {
             const long long c = 32 * g + (threadIdx.x & 31);
-            const float v = c < cols ? x_load<XT>(x, r * ldx + c) : 0.f;
+            const float v = c < cols && TCQ_IN_BOUNDS(r * ldx + c, (n - 1) * ldx + cols) ? x_load<XT>(x, r * ldx + c) : 0.f;
             const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
             const uint32_t byte = q8_scale_byte<FMT>(top);
             const float inv = q8_inv(byte);
@@ -131,23 +131,26 @@ __global__ void __launch_bounds__(kThreads) unpack8_vec_kernel(const uint8_t* co
     for (long long r = blockIdx.x; r < n; r += gridDim.x) {
         const uint8_t* cr = codes + r * cols;
         auto fetch = [&](long long i) {
-            if constexpr (!BYTES) return __ldg(reinterpret_cast<const uint2*>(cr) + i);
+            if constexpr (!BYTES)
+                return TCQ_IN_BOUNDS(r * cols + 8 * i + 7, n * cols) ? __ldg(reinterpret_cast<const uint2*>(cr) + i)
+                                                                     : make_uint2(0u, 0u);
             uint32_t b[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) b[j] = 8 * i + j < cols ? __ldg(cr + 8 * i + j) : 0u;
+            for (int j = 0; j < 8; ++j) b[j] = 8 * i + j < cols && TCQ_IN_BOUNDS(r * cols + 8 * i + j, n * cols) ? __ldg(cr + 8 * i + j) : 0u;
             return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
         };
         const uint8_t* sr = scales + r * groups;
+        auto group = [&](long long g) { return TCQ_IN_BOUNDS(r * groups + g, n * groups) ? (uint32_t)__ldg(sr + g) : 0u; };
         uint16_t* xr = x + r * ldx;
         for (long long i = (long long)blockIdx.y * 2 * step + threadIdx.x; i < pieces; i += (long long)gridDim.y * 2 * step) {
             const bool two = i + step < pieces;
             uint2 w[2];
             uint32_t byte[2];
             w[0] = fetch(i);
-            byte[0] = __ldg(sr + i / 4);
+            byte[0] = group(i / 4);
             if (two) {
                 w[1] = fetch(i + step);
-                byte[1] = __ldg(sr + (i + step) / 4);
+                byte[1] = group((i + step) / 4);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) unpack8_vec_kernel(const uint8_t* co
                 if (BYTES && c + 8 > cols) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (c + j < cols) xr[c + j] = x_bits<XT>(f[j]);
+                        if (c + j < cols && TCQ_IN_BOUNDS(r * ldx + c + j, (n - 1) * ldx + cols)) xr[c + j] = x_bits<XT>(f[j]);
                 } else if (TCQ_IN_BOUNDS(r * ldx + c + 7, (n - 1) * ldx + cols)) {
                     store8<XT>(xr + c, f);
                 }
@@ -180,7 +183,8 @@ __global__ void __launch_bounds__(kThreads) unpack8_kernel(const uint8_t* codes,
     for (long long r = blockIdx.x; r < n; r += gridDim.x) {
         for (long long c = (long long)blockIdx.y * blockDim.x + threadIdx.x; c < cols;
              c += (long long)gridDim.y * blockDim.x)
-            if (TCQ_IN_BOUNDS(r * ldx + c, (n - 1) * ldx + cols))
+            if (TCQ_IN_BOUNDS(r * ldx + c, (n - 1) * ldx + cols) && TCQ_IN_BOUNDS(r * cols + c, n * cols) &&
+                TCQ_IN_BOUNDS(r * groups + c / 32, n * groups))
                 x[r * ldx + c] = x_bits<XT>(
                     in_range<XT>(q8_decode<FMT>(codes[r * cols + c], q8_scale(__ldg(scales + r * groups + c / 32)))));
     }
@@ -226,6 +230,8 @@ __global__ void __launch_bounds__(kThreads, 4) act_grad8_kernel(ActGradArgs a)
                     v.d.x = *dy;
                 dy += kRowThreads * a.lddy;
                 if constexpr (ACT != TCQ_ACT_NONE) {
+                    if (!TCQ_IN_BOUNDS(zc - a.z_codes + CPT - 1, a.n * a.rows) || !TCQ_IN_BOUNDS(zs - a.z_scales, a.n * groups))
+                        return v;
                     if constexpr (CPT == 8)
                         v.z = __ldg(reinterpret_cast<const uint2*>(zc));
                     else
@@ -301,14 +307,14 @@ __global__ void __launch_bounds__(kThreads) sum_ranges_kernel(const float* parti
     float s = 0.f;
     if (c < rows) {
 #pragma unroll 4
-        for (int i = rt; i < ranges; i += kRowThreads) s += partial[(long long)i * rows + c];
+        for (int i = rt; i < ranges && TCQ_IN_BOUNDS((long long)i * rows + c, ranges * rows); i += kRowThreads) s += partial[(long long)i * rows + c];
     }
     part[rt][ct] = s;
     __syncthreads();
     if (rt == 0 && c < rows) {
 #pragma unroll
         for (int k = 1; k < kRowThreads; ++k) s += part[k][ct];
-        out[c] = s;
+        if (TCQ_IN_BOUNDS(c, rows)) out[c] = s;
     }
 }
 
