@@ -424,7 +424,8 @@ tcq_status tcq_gemm(const uint32_t* bits, const uint32_t* start_state, const flo
  * products of a matrix with scales dZ[i, r] is multiplied by the powers of two of W's row r
  * first, in either type; what holds for elements beside their row's largest then holds
  * for those products.
- *   dz  [n, rows], row stride lddz.   dx  out: [n, cols], row stride lddx.
+ *   dz  [n, rows], row stride lddz.   dx  out: [n, cols], row stride lddx; it must not
+ *   overlap dz.
  * rows == 0 gives dX = 0; n == 0 or cols == 0 is a no-op.  Everything else as tcq_gemm.
  */
 size_t tcq_gemm_dgrad_workspace_bytes(int L, int k, int T, int64_t rows, int64_t cols, int64_t n,

@@ -637,6 +637,18 @@ def _check_out(out, shape, dtype, device, what) -> int:
     return ld if n > 1 and cols else max(cols, 1)
 
 
+def _check_apart(out, ldo, t, ldt, what):
+    """Refuses a 16-bit ``out`` that shares elements with ``t``, which other rows or tiles
+    of the call still read.  Columns of one buffer may interleave."""
+    a, b, wide, width = out.data_ptr(), t.data_ptr(), out.shape[1], t.shape[1]
+    if (out.numel() == 0 or t.numel() == 0 or b >= a + 2 * ((out.shape[0] - 1) * ldo + wide) or
+            a >= b + 2 * ((t.shape[0] - 1) * ldt + width)):
+        return
+    if out.shape[0] > 1 and ldo == ldt and 2 * wide <= (b - a) % (2 * ldo) <= 2 * (ldo - width):
+        return
+    raise ValueError(f"out overlaps {what}")
+
+
 def _check_device(t, device, what):
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
@@ -767,7 +779,8 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
 
     ``bias`` float32 [rows]; ``residual`` like the result; ``checkpoint`` a Packed8 of
     [n, rows] that receives the pre-activation in 8 bits.  ``workspace`` (uint8, at
-    least tcq_gemm_workspace_bytes) and ``out`` are allocated when not given."""
+    least tcq_gemm_workspace_bytes) and ``out`` are allocated when not given; ``out`` may
+    be ``residual`` itself, and overlaps neither ``x`` nor a part of ``residual``."""
     torch, lib = _torch(), load_library()
     xt, n, width, ldx = _rows(x, "x")
     dev, dtype = x.device, x.dtype
@@ -786,6 +799,9 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
         out, ldy = _empty(x, (n, rows), dtype, stream), max(rows, 1)
     else:
         ldy = _check_out(out, (n, rows), dtype, dev, "out")
+        _check_apart(out, ldy, x, ldx, "x")
+        if residual is not None and (residual.data_ptr() != out.data_ptr() or ldr != ldy):
+            _check_apart(out, ldy, residual, ldr, "a part of residual")
     zc = zs = None
     zf = TCQ_Q8_INT8
     if checkpoint is not None:
@@ -817,6 +833,7 @@ def gemm_dgrad(bits, start_state, scale, codebook, L: int, k: int, T: int, rows:
         out, lddx = _empty(dz, (n, cols), dz.dtype, stream), max(cols, 1)
     else:
         lddx = _check_out(out, (n, cols), dz.dtype, dev, "out")
+        _check_apart(out, lddx, dz, lddz, "dz")
     cb = cb_dtype_of(codebook)
     ws = _scratch(workspace, _sized(dev, "tcq_gemm_dgrad_workspace_bytes", L, k, T, rows, cols, n, cb), dz,
                   "gemm_dgrad", stream)
@@ -845,6 +862,8 @@ def act_grad8(dy, checkpoint, act: str, dbias: bool = True, out=None, workspace=
         out, lddz = _empty(dy, (n, rows), dy.dtype, stream), max(rows, 1)
     else:
         lddz = _check_out(out, (n, rows), dy.dtype, dev, "out")
+        if out.data_ptr() != dy.data_ptr() or lddz != lddy:
+            _check_apart(out, lddz, dy, lddy, "a part of dy")
     db, dp, wp, wb = None, None, None, 0
     if dbias:
         db = _empty(dy, rows, torch.float32, stream)
