@@ -1,9 +1,9 @@
 // device_errors.cu -- the device-side error word and tcq_device_errors.
 //
 // Kernels report failures that do not fault the GPU by OR-ing a flag into one
-// 32-bit word per device: a bounded wait that gave up (the tensor-core feedback
-// product of tcq_ldlq), and, in the TCQ_DEBUG build, an index that failed its
-// bounds check (the access is skipped).  The host reads and clears the word
+// 32-bit word per device: a bounded wait that gave up (the tensor-core products:
+// the feedback of tcq_ldlq, tcq_gemm, tcq_gemm_dgrad and tcq_wgrad8), and, in the
+// TCQ_DEBUG build, an index that failed its bounds check (the access is skipped).  The host reads and clears the word
 // with tcq_device_errors, which synchronises the caller's stream first.
 #include <mutex>
 

@@ -67,11 +67,14 @@ CodedMatrix matrix(const uint32_t* bits, const uint32_t* start, const float* sca
             tcq_words_per_block(k, T), rows, cols};
 }
 
-// Large bfloat16 batches multiply in bfloat16: the weights are rounded to 8 bits of
-// precision, which leaves the result off by about as much again as its own rounding to
-// bfloat16 (1.4 times in all), and saves the pass that scales the activations to
-// binary16 rows (48 us of 480 for the input gradient of 4096 tokens and 14336 x 4096).
-// Small ones keep 11 bits: there the pass is a few microseconds.
+// Large bfloat16 batches multiply in bfloat16, the operands a bfloat16 layer has anyway: the
+// weights are rounded to 8 bits of precision, which leaves the result off by about as much
+// again as its own rounding to bfloat16 (2.4e-3 of its norm in all against 1.7e-3 with
+// 11-bit weights), and saves the pass that scales the activations to binary16 rows and some
+// of the multipliers' power.  Measured with 8 / with 11 bits, 14336 x 4096, in long runs: 4096
+// tokens forward 416 / 454 us, input gradient 422 / 494; 512 tokens 95 / 106 and 96 / 108;
+// 257 tokens 91 / 101 and 90 / 99.  Up to 256 tokens, where the matrix is mostly decoded
+// inside the product, the pass takes a few microseconds, and the weights keep 11 bits.
 bool bf16_operands(tcq_xdtype xdtype, int64_t n) { return xdtype == TCQ_X_BF16 && n > 256; }
 
 // Whether weights are stored over a power of two of their table (powers.cuh): a binary32

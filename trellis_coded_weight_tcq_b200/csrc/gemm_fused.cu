@@ -18,10 +18,10 @@
 // warp reads whole 32-byte sectors of its rows.  Warp 16 loads the activations' tiles,
 // warp 18 the stream words, one thread of warp 17 issues the MMAs.
 //
-// Measured on a B200, 14336 x 4096, L = 16, k = 2: 48 us for 24 tokens and 64 us for 200
-// (the look-ups alone: 24 us; 24 and 200 tokens' MMAs: 2 and 14 us), with the pieces'
-// sums 5 and 8 us more.  Writing the matrix out first (39 us) and multiplying it takes 96 and
-// 133 us.
+// Measured on a B200, 14336 x 4096, L = 16, k = 2, bfloat16: 53 us for 24 tokens and 76 us
+// for 200, of which the pass before (the activations' and the matrix's powers) and the
+// pieces' sums after it take 6 and 6 us alone (the look-ups: 24 us; 24 and 200 tokens' MMAs: 2
+// and 14 us).  Writing the matrix out first (38 us) and multiplying it takes 81 and 84 us.
 //
 // Work is split over the SMs evenly, in units: a CTA takes a contiguous run of (tile,
 // unit) pairs, so a tile's reduction may be cut into pieces; each writes its fp32 sums
@@ -462,7 +462,8 @@ Plan make_plan(int code, int L, int K, long long rows, long long cols, long long
     p.row_tiles = (int)((rows + kRows - 1) / kRows);
     p.steps = (int)((cols + 127) / 128);
     p.units = (long long)p.row_tiles * p.steps;
-    // at least two units per CTA, one for each group of decoding warps
+    // two units per CTA at least, one for each group of decoding warps (of an odd number of
+    // units one CTA may get a single one, and its second group none)
     long long ctas = (p.units + 1) / 2;
     if (ctas > num_sms) ctas = num_sms;
     p.ctas = (int)ctas;
@@ -511,9 +512,10 @@ cudaError_t launch_k(const CodedMatrix& w, const CUtensorMap& map, const CUtenso
 
 // T a multiple of 64 keeps a stage inside one block and its words together.  More than
 // 256 tokens would decode the matrix again, and the product that decodes ahead wins.
-// Measured, here / decoded ahead, in us (binary16 table): 14336 x 4096 32 tokens 52 / 71,
-// 192 68 / 73, 256 76 / 73, 257 112 / 90; 4096 x 14336 32 tokens 52 / 72, 256 70 / 77; 4096 x
-// 4096 32 tokens 24 / 28, 256 32 / 31; 512 x 512 32 tokens 12 / 13, 256 16 / 13.
+// Measured, here / decoded ahead, in us (bfloat16, binary16 table, scales): 14336 x 4096 32
+// tokens 53 / 78, 192 75 / 82, 256 84 / 84; 4096 x 14336 32 tokens 55 / 77, 256 76 / 84;
+// 4096 x 4096 32 tokens 26 / 31, 256 35 / 38; 512 x 512 32 tokens 13 / 18, 256 18 / 18.
+// Nor does this one need room for the matrix in 16 bits.
 bool fused_shape(int T, long long rows, long long cols, long long n)
 {
     return T % kDepth == 0 && n <= 256 && (rows / kRows + 1) * (cols / 128 + 1) < (1ll << 30);

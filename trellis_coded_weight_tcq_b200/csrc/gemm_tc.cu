@@ -19,13 +19,15 @@
 // steps.  That does not show in 16-bit outputs; the weight gradient, fp32 and summed over
 // all tokens, takes its sums out of tensor memory every 1280 tokens at most and adds them
 // in registers (root mean square error against float64 at 4096 tokens, relative to the
-// gradient's: 1.6e-6 without, 2.8e-7 with; 8e-7 for 1111 tokens, one such sum).
+// gradient's: 1.6e-6 without, 2.9e-7 with; 8e-7 for 1111 tokens, one such sum).
 //
-// Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP), alone and with the
-// second kernel: forward with GELU about 315 us, input gradient 311 us, weight gradient
-// 335 us; the vendor library's bare products take 324 to 360 us there.  In long runs the
-// board's power limit holds the SM clock at 1.4 to 1.55 GHz of 1.965, so what costs energy
-// costs time: the order of the tiles took 50 us off the weight gradient.  Clock stamps: a
+// Measured on a B200, 4096 tokens through 14336 x 4096 (481 GFLOP), each launch by itself,
+// with the second kernel: forward with GELU 323 us, input gradient 318 us, weight gradient
+// 338 us (83, 86 and 75 % of the tensor pipe); the vendor library's bare products take 324 to
+// 360 us there.  In runs of a second the board's power limit holds the SM clock at 1.4 to
+// 1.5 GHz of 1.965 and whole calls take 413 to 420 us (weight gradient 395), so what costs energy
+// costs time: the order of the tiles took 50 us off the weight gradient, whose kernel spills
+// 12 bytes beside its 128 running sums.  Clock stamps: a
 // stage takes 571 cycles of the pipe's 512 in the input gradient; the gap is the latency of
 // loads behind a ring of six (a seventh stage does not fit beside the boxes).
 //

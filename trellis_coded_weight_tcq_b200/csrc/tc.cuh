@@ -111,8 +111,9 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// ---- TMA (no multicast).  The innermost coordinate is always a multiple of 64
-// elements of 2 bytes, so every copy starts on a 16-byte boundary.
+// ---- TMA (no multicast).  Every copy starts on a 16-byte boundary: the innermost
+// coordinate is a multiple of 64 elements of 2 bytes (operands, 16-bit outputs), of 32 of 4
+// bytes (fp32 outputs and sums), or of 4 stream words (-4 for the words before a row).
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes "

@@ -585,6 +585,9 @@ def decode_vec(bits, start_state, codebook, L: int, k: int, V: int, T: int, out=
 
 # ---------------------------------------------------------------------------
 # batched 16-bit products and 8-bit checkpoints
+#
+# A wait inside a product is bounded: one that gives up leaves the call's outputs
+# unspecified and a flag that device_errors() returns (no call synchronises to look).
 # ---------------------------------------------------------------------------
 @dataclass
 class Packed8:
@@ -780,7 +783,13 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
     ``bias`` float32 [rows]; ``residual`` like the result; ``checkpoint`` a Packed8 of
     [n, rows] that receives the pre-activation in 8 bits.  ``workspace`` (uint8, at
     least tcq_gemm_workspace_bytes) and ``out`` are allocated when not given; ``out`` may
-    be ``residual`` itself, and overlaps neither ``x`` nor a part of ``residual``."""
+    be ``residual`` itself, and overlaps neither ``x`` nor a part of ``residual``.
+
+    Sums are fp32; how a weight (scale times codeword) enters them depends on the number of
+    tokens, so that a token's result may differ in its last bits with the batch it comes in:
+    fp32 for a single token without a checkpoint, rounded to binary16 (relative to powers of
+    two of its row and the table) for 2 to 256 and for any number of float16 ones, rounded
+    to bfloat16 for more than 256 bfloat16 tokens."""
     torch, lib = _torch(), load_library()
     xt, n, width, ldx = _rows(x, "x")
     dev, dtype = x.device, x.dtype
@@ -822,7 +831,8 @@ def gemm(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, 
 def gemm_dgrad(bits, start_state, scale, codebook, L: int, k: int, T: int, rows: int, cols: int, dz, out=None,
                workspace=None, stream=None):
     """dz W for a trellis-coded W [rows, cols] and ``dz`` float16 or bfloat16 [n, rows];
-    [n, cols] of dz's type."""
+    [n, cols] of dz's type.  ``out`` must not overlap ``dz``.  Weights are rounded like
+    ``gemm``'s, those of a single token to binary16."""
     lib = load_library()
     xt, n, width, lddz = _rows(dz, "dz")
     dev = dz.device
