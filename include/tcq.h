@@ -383,8 +383,8 @@ tcq_status tcq_unpack8(const uint8_t* codes, const uint8_t* scales, tcq_q8 forma
  * rounded once to binary16 (exact without scales for a binary16 table and the computed
  * code), relative to a power of two per row of W and one of the table, so that neither
  * scales nor entries need to lie near 1: with M the row's largest |scale| times the
- * table's largest finite entry, weights keep binary16's 11 bits down to 2^-27 M (the
- * computed code's to 2^-14 M) and are within 2^-38 M (2^-25 M) below.  A bfloat16 row of X is scaled to
+ * code's largest finite number, weights keep binary16's 11 bits down to 2^-27 M and are
+ * within 2^-38 M below.  A bfloat16 row of X is scaled to
  * binary16 by a power of two of its own, exactly for elements from 2^-31 of the row's
  * largest up and within 2^-39 of that largest for the others; so are binary16 rows
  * that are not all 16-byte aligned (exact from 2^-28 up).  A single token (n == 1, no checkpoint

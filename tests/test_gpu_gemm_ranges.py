@@ -164,3 +164,36 @@ def test_small_elements_beside_a_large_one(T, dtype, scaled, cuda_device):
                 off = 2.0**-39 * top * times
                 assert abs(got - v * times) <= off + max(eps / 2 * (v * times + off), 2.0**-25 if dtype == "f16" else 0)
         assert float(y[0, 0]) == top * times and bool((y[1] == 0).all())
+
+
+@pytest.mark.parametrize("n", [1, 24, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T", [64, 100])
+@pytest.mark.parametrize("code", ["f16", "f32", "mad"])
+def test_blocks_of_unequal_scale(code, T, dtype, n, cuda_device):
+    """A row's blocks of scales 2^20 apart, met by activations as much larger: the small
+    block's weights keep their bits, in its columns of the input gradient, too.  The bound has
+    a half step of each weight and nothing relative to the row's largest."""
+    import torch
+    from tests import gemm_reference as ref
+    from tests.test_gpu_gemm import _check
+
+    rng = np.random.default_rng(T + n + len(code))
+    rows, nb, L = 130, 4, 12
+    size = np.where(np.arange(nb) % 2 == 0, 1.0, 2.0**-20)
+    scale = (rng.lognormal(-2.0, 0.3, (rows, nb)) * size).astype(np.float32).reshape(-1)
+    if code == "mad":
+        args, w = ref.random_matrix(rng, L, 2, T, rows, nb * T, "mad", False, cuda_device)
+        w = w * torch.from_numpy(np.repeat(scale.astype(np.float64).reshape(rows, nb), T, axis=1)).to(cuda_device)
+        args = (*args[:2], torch.from_numpy(scale).to(cuda_device), *args[3:])
+    else:
+        args, w = _coded(rng, L, 2, T, rows, nb * T, _table(rng, L, code, 0), scale, cuda_device)
+    dt = {"f16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    reach = torch.from_numpy(np.repeat(np.where(size == 1, 2.0**-10, 2.0**10), T)).to(cuda_device)
+    x = (torch.from_numpy(rng.standard_normal((n, nb * T))).to(cuda_device) * reach).to(dt)
+    dz = torch.from_numpy(rng.standard_normal((n, rows)) * 2.0**8).to(cuda_device).to(dt)
+    half = ref.weight_half_step(n, dt, False)
+    for got, a, b in ((tcq.gemm(*args, x), x.double(), w), (tcq.gemm_dgrad(*args, dz), dz.double(), w.T.contiguous())):
+        want = a @ b.T
+        bound = (a.shape[1] / 16 + 2) * 2.0**-22 * (a.abs() @ b.abs().T) + 8 * half * ((a * a) @ (b * b).T).sqrt()
+        _check(got, want, bound + ref.half_step(dt) * (want.abs() + bound) + (2.0**-25 if dtype == "f16" else 0), "unequal blocks")

@@ -4,7 +4,7 @@
 // A weight is scale * c[s], rounded once to binary16.  So that small scales do not
 // fall into binary16's subnormals, every row is divided by a power of two, the
 // least above its largest finite |scale|, and tables by one of their own, so that
-// their largest entry ends in [2^14, 2^15): a weight is then below 2^15, and what a
+// their largest entry ends in [2^14, 2^15) (the computed code's numbers too): a weight is then below 2^15, and what a
 // row's largest weight is to its others, not how large they are, decides what they
 // lose.  The products multiply the powers back in (exactly).  Without scales a
 // binary16 or computed codeword is stored as it is.  For large bfloat16 batches the weights are

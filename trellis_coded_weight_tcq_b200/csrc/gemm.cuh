@@ -2,6 +2,7 @@
 // trellis-coded matrix, their gradients and the 8-bit checkpoints.
 #pragma once
 
+#include "codes.cuh"
 #include "common.cuh"
 
 namespace tcq {
@@ -104,12 +105,12 @@ struct ScaleRows {
 };
 
 // out[r] for the rows of a coded matrix, per_row scales each: the least power of two
-// above the largest finite |scale|, and its exponent field (or nullptr).  table_top
+// above the largest finite |scale|, times 2^-down, and its exponent field (or nullptr).  table_top
 // [kTableParts], unless nullptr: the largest finite magnitudes of the table's parts.
 struct RowPowers {
     const float* scale = nullptr;
     long long rows = 0;
-    int per_row = 0;
+    int per_row = 0, down = 0;
     float* out = nullptr;
     uint8_t* exponents = nullptr;
     const void* table = nullptr;
@@ -125,6 +126,8 @@ inline RowPowers powers_of(const CodedMatrix& w, float* row_pow2, uint8_t* row_e
         p.scale = w.scale;
         p.rows = w.rows;
         p.per_row = (int)(w.cols / w.T);
+        // the computed code's numbers are below 2: its part of the power is known
+        p.down = w.cb_f16 == kMadCodebook ? 14 : 0;
         p.out = row_pow2;
         p.exponents = row_exponents;
     }

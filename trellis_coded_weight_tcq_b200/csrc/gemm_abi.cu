@@ -79,7 +79,7 @@ bool bf16_operands(tcq_xdtype xdtype, int64_t n) { return xdtype == TCQ_X_BF16 &
 
 // Whether weights are stored over a power of two of their table (powers.cuh): a binary32
 // table's entries may be of any size; binary16 ones without scales are stored exactly as
-// they are, and the computed code's lie near 1.
+// they are, and the computed code's lie below 2 (powers_of).
 bool table_power_wanted(tcq_dtype dt, const float* scale) { return dt == TCQ_F32 || (dt == TCQ_F16 && scale); }
 
 // Workspace of a product: the binary16 matrix, its row powers and its table's, the

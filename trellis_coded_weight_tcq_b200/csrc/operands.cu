@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The power of two above the largest finite |scale| of a row of W: one warp per row.
+// A row's power, from the largest finite |scale| of a row of W: one warp per row.
 __device__ __forceinline__ void row_power(const RowPowers& p, long long r)
 {
     uint32_t top = 0u;
@@ -25,7 +25,7 @@ __device__ __forceinline__ void row_power(const RowPowers& p, long long r)
         top = max(top, finite_magnitude(__ldg(p.scale + r * p.per_row + j)));
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0 && TCQ_IN_BOUNDS(r, p.rows)) {
-        const float v = pow2_clamped(power_above(top));
+        const float v = pow2_clamped(power_above(top) - p.down);
         p.out[r] = v;
         if (p.exponents) p.exponents[r] = (uint8_t)(__float_as_uint(v) >> 23);
     }

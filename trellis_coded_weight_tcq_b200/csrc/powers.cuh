@@ -3,8 +3,8 @@
 //
 // A weight is scale * codeword.  It is stored over the product of two powers, one per row
 // of the matrix (the least above its largest finite |scale|) and, for tables, one of the
-// table (so that its largest finite entry ends in [2^14, 2^15)); the epilogue multiplies
-// both back.  Neither changes a rounding.
+// table (so that its largest finite entry ends in [2^14, 2^15); the computed code's is
+// 2^-14, part of the rows'); the epilogue multiplies both back.  Neither changes a rounding.
 #pragma once
 
 #include <cuda_runtime.h>
